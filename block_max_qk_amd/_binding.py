@@ -8,9 +8,11 @@ library is missing the call raises: there is no fallback implementation.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
+import struct
 import threading
-from typing import Optional
+from typing import NamedTuple, Optional, Sequence
 
 import torch
 
@@ -28,11 +30,13 @@ DTYPE_CODE = {
 }
 LAYOUT_CODE = {"TND": 0, "BBND": 1, "BNBD": 2}
 STATUS_NAMES = ["MSA_OK", "MSA_ERR_NULL", "MSA_ERR_LAYOUT", "MSA_ERR_DTYPE", "MSA_ERR_SHAPE",
-                "MSA_ERR_STRIDE", "MSA_ERR_SCALE", "MSA_ERR_ATTR", "MSA_ERR_HIP"]
+                "MSA_ERR_STRIDE", "MSA_ERR_SCALE", "MSA_ERR_ATTR", "MSA_ERR_HIP",
+                "MSA_ERR_WORKSPACE"]
 EXPORTED = ("msa_index_score", "msa_index_score_family", "msa_index_score_ex",
             "msa_index_score_mxfp4", "msa_index_score_mxfp4_family",
             "msa_index_score_out_width", "msa_status_str",
-            "msa_index_score_kernel_family", "msa_block_topk")
+            "msa_index_score_kernel_family", "msa_block_topk", "msa_cache_append",
+            "msa_attention", "msa_block_attention", "msa_attention_workspace")
 LOCAL_MODE_CODE = {"request": 0, "query": 1}
 
 
@@ -99,6 +103,23 @@ def load_library(path: Optional[str] = None):
         lib.msa_block_topk.argtypes = [ptr, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64,
                                        ctypes.c_int64, ctypes.c_int32, ptr, ptr]
         lib.msa_block_topk.restype = ctypes.c_int
+        i64 = ctypes.c_int64
+        # items, num_items, cos, sin, positions, rotary_dim, interleaved,
+        # block_table, max_blocks, cu_seqlens_q, kv_len, batch, block_size, stream
+        lib.msa_cache_append.argtypes = [ptr, i32, ptr, ptr, i64, i32, i32, ptr, i64, ptr, ptr,
+                                         i32, i32, ptr]
+        lib.msa_cache_append.restype = ctypes.c_int
+        # block_table, max_blocks, cu_seqlens_q, kv_len, batch, block_size,
+        # layout, sparse_mode, softmax_scale, out, lse, workspace,
+        # workspace_bytes, stream
+        tail = [ptr, i64, ptr, ptr, i32, i32, i32, i32, ctypes.c_float, ptr, ptr, ptr, i64, ptr]
+        three = [ctypes.POINTER(MsaTensor)] * 3
+        lib.msa_attention.argtypes = three + tail
+        lib.msa_attention.restype = ctypes.c_int
+        lib.msa_block_attention.argtypes = three + [ptr, i32] + tail
+        lib.msa_block_attention.restype = ctypes.c_int
+        lib.msa_attention_workspace.argtypes = [i64, i32, i32, i32, i64, i32]
+        lib.msa_attention_workspace.restype = i64
         if path is None:
             _lib = lib
         return lib
@@ -400,3 +421,297 @@ def block_topk(scores: torch.Tensor, num_valid: Optional[int] = None, k: int = 1
     Hq, T, W = scores.shape
     out = torch.empty((T, Hq, k), dtype=torch.int32, device=scores.device)
     return msa_block_topk(scores, W if num_valid is None else num_valid, k, out, stream=stream)
+
+
+# ---------------------------------------------------------------------------
+# around the index branch: the cache append and the attention
+# ---------------------------------------------------------------------------
+
+ROWS = 3   # MSA_LAYOUT_ROWS: one row per new token, not a cache
+APPEND_MAX_ITEMS = 8
+
+
+class CacheItem(NamedTuple):
+    """One tensor of a ``msa_cache_append`` call: ``src`` [T, H, 128] f16/bf16
+    rows, rotated if ``rotate``, go to ``dst``: a cache of ``layout`` TND, BBND
+    or BNBD, or with "ROWS" [T, H, ...] (the queries).  ``dst``'s type says how
+    they are stored; int8 and uint8 (MXFP4) take ``scale``."""
+    src: torch.Tensor
+    dst: torch.Tensor
+    layout: object
+    scale: Optional[torch.Tensor] = None
+    rotate: bool = False
+
+
+# msa_append_item_t: two msa_tensor_t (data, dtype, ndim, shape[4], stride[4]),
+# scale, layout, rotate
+_ITEM = struct.Struct("<Qii4q4qQii4q4qQii")
+
+
+def _dims(t: torch.Tensor):
+    n = t.dim()
+    if n > 4:
+        raise ValueError(f"a tensor of {n} axes: at most 4 are taken")
+    pad = (0,) * (4 - n)
+    return (t.data_ptr(), DTYPE_CODE.get(t.dtype, -1), n, *t.shape, *pad, *t.stride(), *pad)
+
+
+def _on_device(dev, named):
+    for name, t in named:
+        if t is not None and t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, the call's first tensor on {dev}")
+
+
+def _check_lengths(cu_seqlens_q, kv_len, block_table, max_blocks, paged) -> int:
+    """The request count B, from tensors whose extents the C ABI takes on trust."""
+    for name, t in (("cu_seqlens_q", cu_seqlens_q), ("kv_len", kv_len),
+                    ("block_table", block_table)):
+        if t is not None and (t.dtype != torch.int32 or not t.is_contiguous()):
+            raise ValueError(f"{name} must be a contiguous int32 tensor")
+    if kv_len.dim() != 1:
+        raise ValueError("kv_len must be 1-D [B] (per-request lengths)")
+    B = kv_len.shape[0]
+    if cu_seqlens_q.dim() != 1 or cu_seqlens_q.shape[0] != B + 1:
+        raise ValueError(f"cu_seqlens_q must be [B+1] = [{B + 1}], got "
+                         f"{tuple(cu_seqlens_q.shape)}")
+    if paged:
+        if block_table is None:
+            raise ValueError("paged layouts need a block_table")
+        if (block_table.dim() != 2 or block_table.shape[0] < B or
+                block_table.shape[1] != max_blocks):
+            raise ValueError(f"block_table must be [>= {B}, max_blocks = {max_blocks}], got "
+                             f"{tuple(block_table.shape)}")
+    return B
+
+
+def _stream_of(handle, dev):
+    """The torch stream of a raw handle (0: the device's default stream)."""
+    if not handle:
+        return torch.cuda.default_stream(dev)
+    return torch.cuda.ExternalStream(handle, device=dev)
+
+
+class _On:
+    """The device of a call, and its stream's handle (a stream of another
+    device than the current one is launched on with its own made current)."""
+
+    def __init__(self, dev, stream):
+        self.guard = None
+        if dev.type == "cuda" and torch.cuda.current_device() != dev.index:
+            self.guard = torch.cuda.device(dev)
+        self.handle = _stream_handle(stream, dev)
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+        return self.handle
+
+    def __exit__(self, *e):
+        if self.guard is not None:
+            self.guard.__exit__(*e)
+
+
+def _item_layout(layout) -> int:
+    if isinstance(layout, str):
+        return ROWS if layout.upper() == "ROWS" else LAYOUT_CODE.get(layout.upper(), -1)
+    return int(layout)
+
+
+def msa_cache_append(items: Sequence[CacheItem], cos: Optional[torch.Tensor],
+                     sin: Optional[torch.Tensor], block_table: Optional[torch.Tensor],
+                     cu_seqlens_q: torch.Tensor, kv_len: torch.Tensor,
+                     interleaved: bool = False, stream=None,
+                     block_size: int = BLOCK_SIZE) -> None:
+    """Append the new tokens' rows to their caches, rotated by their positions
+    and encoded as the caches hold them, and rotate or encode the queries, in
+    one launch (see ``CacheItem``; the C ABI's header defines the encodings).
+
+    ``cos`` and ``sin`` [positions, rotary_dim / 2] float32 may be None if no
+    item is rotated, ``block_table`` [>= B, MB] int32 if no item is paged;
+    ``kv_len`` counts the new tokens."""
+    lib = load_library()
+    if not 1 <= len(items) <= APPEND_MAX_ITEMS:
+        raise ValueError(f"1 to {APPEND_MAX_ITEMS} items, got {len(items)}")
+    dev = items[0].src.device
+    _on_device(dev, (("cos", cos), ("sin", sin), ("block_table", block_table),
+                     ("cu_seqlens_q", cu_seqlens_q), ("kv_len", kv_len)))
+    max_blocks = 0 if block_table is None or block_table.dim() != 2 else block_table.shape[1]
+    B = _check_lengths(cu_seqlens_q, kv_len, block_table, max_blocks, block_table is not None)
+    positions = rotary = 0
+    if cos is not None or sin is not None:
+        if cos is None or sin is None or cos.shape != sin.shape or cos.dim() != 2:
+            raise ValueError("cos and sin must both be [positions, rotary_dim / 2]")
+        for name, t in (("cos", cos), ("sin", sin)):
+            if t.dtype != torch.float32 or not t.is_contiguous():
+                raise ValueError(f"{name} must be a contiguous float32 tensor")
+        positions, rotary = cos.shape[0], 2 * cos.shape[1]
+    elif any(it.rotate for it in items):
+        raise ValueError("rotated items need cos and sin")
+    buf = bytearray(_ITEM.size * len(items))
+    for i, it in enumerate(items):
+        src, dst, scale = it.src, it.dst, it.scale
+        _on_device(dev, (("src", src), ("dst", dst), ("scale", scale)))
+        lay = _item_layout(it.layout)
+        sp = 0
+        if scale is not None:
+            i8 = dst.dtype == torch.int8
+            want = torch.float32 if i8 else torch.uint8
+            n = dst.numel() // (128 if i8 else 16)
+            if scale.dtype != want or not scale.is_contiguous() or scale.numel() != n:
+                raise ValueError(f"item {i}: scale must be a contiguous {want} tensor of {n} "
+                                 f"elements, got {scale.dtype} {tuple(scale.shape)}")
+            sp = scale.data_ptr()
+        if lay in (1, 2) and block_table is None:
+            raise ValueError(f"item {i}: paged layouts need a block_table")
+        _ITEM.pack_into(buf, i * _ITEM.size, *_dims(src), *_dims(dst), sp, lay,
+                        int(bool(it.rotate)))
+    arr = (ctypes.c_char * len(buf)).from_buffer(buf)
+    with _On(dev, stream) as handle:
+        st = lib.msa_cache_append(ctypes.addressof(arr), len(items), _ptr(cos), _ptr(sin),
+                                  positions, rotary, int(bool(interleaved)), _ptr(block_table),
+                                  max_blocks, _ptr(cu_seqlens_q), _ptr(kv_len), B,
+                                  int(block_size), handle)
+    _raise_status(st)
+
+
+def msa_attention_workspace(T: int, batch: int, Hq: int, Hkv: int, max_blocks: int,
+                            num_blocks: int = 0) -> int:
+    """Bytes of workspace that an attention call of these sizes needs
+    (``num_blocks`` 0: dense)."""
+    return int(load_library().msa_attention_workspace(int(T), int(batch), int(Hq), int(Hkv),
+                                                      int(max_blocks), int(num_blocks)))
+
+
+def _attention(query, key, value, blocks, block_table, cu_seqlens_q, kv_len, layout, sparse_mode,
+               softmax_scale, out, lse, max_blocks, workspace, stream, block_size):
+    lib = load_library()
+    dev = query.device
+    _on_device(dev, (("key", key), ("value", value), ("blocks", blocks), ("out", out),
+                     ("lse", lse), ("block_table", block_table), ("cu_seqlens_q", cu_seqlens_q),
+                     ("kv_len", kv_len), ("workspace", workspace)))
+    lay = _layout_code(layout)
+    max_blocks = int(max_blocks)
+    B = _check_lengths(cu_seqlens_q, kv_len, block_table, max_blocks, lay in (1, 2))
+    if query.dim() != 3:
+        raise ValueError(f"query must be [T, Hq, 128], got {tuple(query.shape)}")
+    T, Hq = query.shape[0], query.shape[1]
+    if out.dtype != query.dtype or not out.is_contiguous() or out.shape != query.shape:
+        raise ValueError(f"out must be a contiguous {query.dtype} {tuple(query.shape)} tensor")
+    if lse is not None and (lse.dtype != torch.float32 or not lse.is_contiguous() or
+                            tuple(lse.shape) != (T, Hq)):
+        raise ValueError(f"lse must be a contiguous float32 [{T}, {Hq}] tensor")
+    kr = _key_rows(key, lay)
+    Hkv = kr[1] if kr is not None else 0
+    k = 0
+    if blocks is not None:
+        if (blocks.dtype != torch.int32 or not blocks.is_contiguous() or blocks.dim() != 3 or
+                tuple(blocks.shape[:2]) != (T, Hkv)):
+            raise ValueError(f"blocks must be a contiguous int32 [{T}, {Hkv}, k] tensor, got "
+                             f"{blocks.dtype} {tuple(blocks.shape)}")
+        k = blocks.shape[2]
+    if workspace is not None and not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    scale = 1.0 / math.sqrt(query.shape[2]) if softmax_scale is None else float(softmax_scale)
+    qd, kd, vd = describe(query), describe(key), describe(value)
+    with _On(dev, stream) as handle:
+        need = lib.msa_attention_workspace(T, B, Hq, Hkv, max_blocks, k)
+        if need and workspace is None:
+            # memory of the stream that the kernels run on, so that it is
+            # handed on only behind them
+            if stream is None:
+                workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+            else:
+                with torch.cuda.stream(_stream_of(handle, dev)):
+                    workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        wb = 0 if workspace is None else workspace.numel() * workspace.element_size()
+        tail = (_ptr(block_table), max_blocks, _ptr(cu_seqlens_q), _ptr(kv_len), B,
+                int(block_size), lay, int(sparse_mode), scale, _ptr(out), _ptr(lse),
+                _ptr(workspace), wb, handle)
+        head = (ctypes.byref(qd), ctypes.byref(kd), ctypes.byref(vd))
+        if blocks is None:
+            st = lib.msa_attention(*head, *tail)
+        else:
+            st = lib.msa_block_attention(*head, _ptr(blocks), k, *tail)
+    _raise_status(st)
+    return out
+
+
+def msa_attention(query: torch.Tensor, key: torch.Tensor, value: torch.Tensor,
+                  block_table: Optional[torch.Tensor], cu_seqlens_q: torch.Tensor,
+                  kv_len: torch.Tensor, layout, sparse_mode: int, softmax_scale: Optional[float],
+                  out: torch.Tensor, max_blocks: int, lse: Optional[torch.Tensor] = None,
+                  workspace: Optional[torch.Tensor] = None, stream=None,
+                  block_size: int = BLOCK_SIZE) -> torch.Tensor:
+    """Call the C ABI: ``out`` ([T, Hq, 128], the query's type) receives the
+    attention of every new token over its request's visible keys, ``lse``
+    ([T, Hq] float32, if given) the log of its softmax's sum; asynchronous on
+    ``stream`` (default: torch's current stream).  ``softmax_scale`` None is
+    1 / sqrt(128).  Without ``workspace`` the memory that a split over the keys
+    needs (``msa_attention_workspace``) is allocated here."""
+    return _attention(query, key, value, None, block_table, cu_seqlens_q, kv_len, layout,
+                      sparse_mode, softmax_scale, out, lse, max_blocks, workspace, stream,
+                      block_size)
+
+
+def msa_block_attention(query: torch.Tensor, key: torch.Tensor, value: torch.Tensor,
+                        blocks: torch.Tensor, block_table: Optional[torch.Tensor],
+                        cu_seqlens_q: torch.Tensor, kv_len: torch.Tensor, layout,
+                        sparse_mode: int, softmax_scale: Optional[float], out: torch.Tensor,
+                        max_blocks: int, lse: Optional[torch.Tensor] = None,
+                        workspace: Optional[torch.Tensor] = None, stream=None,
+                        block_size: int = BLOCK_SIZE) -> torch.Tensor:
+    """``msa_attention`` over the blocks that ``blocks`` ([T, Hkv, k] int32, as
+    ``msa_block_topk`` writes them) names for each token and KV head."""
+    if blocks is None:
+        raise ValueError("blocks is required")
+    return _attention(query, key, value, blocks, block_table, cu_seqlens_q, kv_len, layout,
+                      sparse_mode, softmax_scale, out, lse, max_blocks, workspace, stream,
+                      block_size)
+
+
+def _allocated(query, key, block_table, layout, max_blocks, return_lse, stream):
+    """(out, lse, max_blocks) of a call that leaves them to the binding."""
+    if max_blocks is None:
+        if block_table is not None:
+            max_blocks = block_table.shape[-1]
+        else:
+            max_blocks = (key.shape[0] + 127) // 128   # packed: no more than all keys
+
+    def make():
+        out = torch.empty(query.shape, dtype=query.dtype, device=query.device)
+        lse = (torch.empty(query.shape[:2], dtype=torch.float32, device=query.device)
+               if return_lse else None)
+        return out, lse, max_blocks
+
+    if stream is None or query.device.type != "cuda":
+        return make()
+    # results of a call on a given stream belong to that stream, as its
+    # workspace does
+    with torch.cuda.stream(_stream_of(_stream_handle(stream, query.device), query.device)):
+        return make()
+
+
+def attention(query: torch.Tensor, key: torch.Tensor, value: torch.Tensor,
+              block_table: Optional[torch.Tensor], cu_seqlens_q: torch.Tensor,
+              kv_len: torch.Tensor, layout, sparse_mode: int = 3,
+              softmax_scale: Optional[float] = None, max_blocks: Optional[int] = None,
+              return_lse: bool = False, stream=None):
+    """Allocate ``out`` (and ``lse``) and fill them with ``msa_attention``;
+    returns ``out`` or ``(out, lse)``."""
+    out, lse, mb = _allocated(query, key, block_table, layout, max_blocks, return_lse, stream)
+    msa_attention(query, key, value, block_table, cu_seqlens_q, kv_len, layout, sparse_mode,
+                  softmax_scale, out, mb, lse=lse, stream=stream)
+    return (out, lse) if return_lse else out
+
+
+def block_attention(query: torch.Tensor, key: torch.Tensor, value: torch.Tensor,
+                    blocks: torch.Tensor, block_table: Optional[torch.Tensor],
+                    cu_seqlens_q: torch.Tensor, kv_len: torch.Tensor, layout,
+                    sparse_mode: int = 3, softmax_scale: Optional[float] = None,
+                    max_blocks: Optional[int] = None, return_lse: bool = False, stream=None):
+    """Allocate ``out`` (and ``lse``) and fill them with
+    ``msa_block_attention``; returns ``out`` or ``(out, lse)``."""
+    out, lse, mb = _allocated(query, key, block_table, layout, max_blocks, return_lse, stream)
+    msa_block_attention(query, key, value, blocks, block_table, cu_seqlens_q, kv_len, layout,
+                        sparse_mode, softmax_scale, out, mb, lse=lse, stream=stream)
+    return (out, lse) if return_lse else out

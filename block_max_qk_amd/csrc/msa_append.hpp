@@ -1,0 +1,320 @@
+// The cache append kernel (gfx950 only): rows of new tokens rotated by their
+// positions, encoded in the destination's type and stored in their pages.
+//
+// Bound by memory: every row is read once and written once, the angles of a
+// token once per wave.  A wave takes one token and a run of steps; a step is
+// four head rows of one item, 16 lanes to a row and 8 elements to a lane
+// (16-byte loads, whole lines per row).  The step's item is the same for the
+// whole wave, so its type, layout and pointers are scalars and nothing
+// diverges.  The next step's rows are loaded before a step is computed.
+#pragma once
+
+#include "msa_device.hpp"
+
+namespace msa {
+
+constexpr int kAppendItems = 8;
+constexpr int kAppendWaves = 4;
+constexpr int kLayoutRows = 3;        // MSA_LAYOUT_ROWS
+
+struct AppendItem {
+  const uint8_t* src;
+  uint8_t* dst;
+  uint8_t* scale;
+  int64_t src_row, src_head;          // bytes between tokens, between heads
+  int64_t page, row, head;            // dst bytes (ROWS: row per token)
+  int64_t s_page, s_row, s_head;      // scale bytes
+  int64_t limit;                      // pages, or packed tokens
+  int32_t heads, steps;               // steps = ceil(heads / 4)
+  int32_t kind;                       // KeyKind of dst
+  int32_t layout, rotate;
+};
+
+struct AppendParams {
+  AppendItem item[kAppendItems];
+  const float* cos;
+  const float* sin;
+  const int32_t* block_table;
+  const int32_t* cu_q;
+  const int32_t* kv_len;
+  int64_t positions;                  // rows of the angle table
+  int64_t T;
+  int32_t B, MB;
+  int32_t items, steps;               // steps of all items
+  int32_t per_wave, groups;           // steps per wave, waves per token
+  int32_t half;                       // rotary_dim / 2 (0: no rotation)
+  int32_t interleaved, packed;        // packed: some item is TND
+};
+
+// The request of token t: the largest b with cu[b] <= t, found 64 bounds at a
+// time (one load per factor 64 of the batch); -1 if no request holds t.
+__device__ __forceinline__ int request_of(const int32_t* cu, int B, int64_t t) {
+  const int l = lane_id();
+  int lo = 0, hi = B;                 // the answer is in [lo, hi)
+  while (hi - lo > 1) {
+    const int step = (hi - lo + 63) / 64;
+    // (64-bit: lo + 64 step passes 2^31 for the largest batches)
+    const int64_t at = (int64_t)lo + (int64_t)(l + 1) * step;
+    const bool below = at < hi && (int64_t)cu[at < hi ? at : hi] <= t;
+    const int k = __popcll(__ballot(below));
+    lo += k * step;
+    hi = min(lo + step, hi);
+  }
+  return (int64_t)cu[lo] <= t && t < (int64_t)cu[lo + 1] ? lo : -1;
+}
+
+__device__ __forceinline__ float elem16(uint32_t w, int hi, bool bf) {
+  const uint32_t x = hi ? w >> 16 : w & 0xFFFFu;
+  if (bf) return __builtin_bit_cast(float, x << 16);
+  return (float)__builtin_bit_cast(_Float16, (uint16_t)x);
+}
+
+// max over the 16 lanes of a row (or 4 of a group), in float64
+template <int LANES>
+__device__ __forceinline__ double lanes_max(double x) {
+#pragma unroll
+  for (int d = LANES / 2; d > 0; d >>= 1) x = fmax(x, __shfl_xor(x, d));
+  return x;
+}
+template <int LANES>
+__device__ __forceinline__ bool lanes_any(bool x) {
+  const int l = lane_id();
+  const unsigned long long m = __ballot(x) >> (l & ~(LANES - 1));
+  return (m & ((1ull << LANES) - 1)) != 0;
+}
+
+// Elements 8 i .. 8 i + 7 of a row (lane i of its 16), rotated, in type F.
+// The partners of halves-style pairs lie `half` elements away, in another
+// lane; c and s hold the lane's angles: of its 8 elements (halves) or of its 4
+// pairs (interleaved).
+template <typename F>
+__device__ __forceinline__ void rotate8(F* x, const float* c, const float* s, int i, int half,
+                                        bool interleaved) {
+  if (interleaved) {
+    if (8 * i < 2 * half) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const F a = x[2 * k], b = x[2 * k + 1];
+        x[2 * k] = a * (F)c[k] - b * (F)s[k];
+        x[2 * k + 1] = b * (F)c[k] + a * (F)s[k];
+      }
+    }
+  }
+}
+
+template <bool BF>
+__global__ __launch_bounds__(64 * kAppendWaves) void append_kernel(AppendParams p) {
+  const int64_t wid = (int64_t)blockIdx.x * kAppendWaves +
+                      __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t t = wid / p.groups;
+  if (t >= p.T) return;
+  int step = (int)(wid - t * p.groups) * p.per_wave;
+  const int step_end = min(step + p.per_wave, p.steps);
+
+  const int b = __builtin_amdgcn_readfirstlane(request_of(p.cu_q, p.B, t));
+  if (b < 0) return;
+  const int q0 = p.cu_q[b];
+  const int lq = p.cu_q[b + 1] - q0;
+  const int64_t pos = (int64_t)p.kv_len[b] - lq + (t - q0);
+  if (pos < 0 || (p.half > 0 && pos >= p.positions)) return;
+  const int l = lane_id();
+  const int i = l & 15, rr = l >> 4;
+
+  // where the token lives: its page and slot, or its packed row
+  const int64_t blk = pos / kP;
+  const int slot = (int)(pos - blk * kP);
+  int page = -1;
+  if (p.block_table && blk < p.MB) page = p.block_table[(int64_t)b * p.MB + blk];
+  int64_t packed = 0;
+  if (p.packed) {
+    for (int base = 0; base < b; base += 64)
+      packed += lane_at(wave_incl_scan(base + l < b ? (int64_t)max(p.kv_len[base + l], 0) : 0), 63);
+    packed += pos;
+  }
+
+  // this lane's angles
+  float c[8], s[8];
+  if (p.half > 0) {
+    const float* cr = p.cos + pos * p.half;
+    const float* sr = p.sin + pos * p.half;
+    const int at = 8 * i < 2 * p.half ? (p.interleaved ? 4 * i : (8 * i) % p.half) : 0;
+#pragma unroll
+    for (int k = 0; k < 8; k += 4) {
+      const int a = p.interleaved ? at : at + k;
+      const f32x4 cv = *reinterpret_cast<const f32x4*>(cr + a);
+      const f32x4 sv = *reinterpret_cast<const f32x4*>(sr + a);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        c[k + e] = cv[e];
+        s[k + e] = sv[e];
+      }
+    }
+  }
+  // halves: the partner's lane and this lane's sign of the sine
+  const int hc = p.half / 8;                       // lanes of one half
+  const bool rot_lane = i < 2 * hc;
+  const int partner = (l & 48) | (rot_lane ? (i < hc ? i + hc : i - hc) : i);
+
+  // the step's item, and its first head in it
+  int it = 0, first = 0;
+  while (step >= first + p.item[it].steps) first += p.item[it++].steps;
+  auto load = [&](int item, int st) -> i32x4 {
+    const AppendItem& a = p.item[item];
+    const int h = 4 * st + rr;
+    if (h >= a.heads) return i32x4{0, 0, 0, 0};
+    return ld16(a.src + t * a.src_row + (int64_t)h * a.src_head + 16 * i);
+  };
+  i32x4 next = load(it, step - first);
+  for (; step < step_end; ++step) {
+    const int cur = it, st = step - first;
+    i32x4 raw = next;
+    if (step + 1 < step_end) {
+      while (step + 1 >= first + p.item[it].steps) first += p.item[it++].steps;
+      next = load(it, step + 1 - first);
+    }
+    const AppendItem& a = p.item[cur];
+    const int h = 4 * st + rr;
+    int64_t off, soff;
+    bool ok = h < a.heads;
+    if (a.layout == kLayoutRows) {
+      off = t * a.row;
+      soff = t * a.s_row;
+    } else if (a.layout == 0) {
+      ok = ok && packed < a.limit;
+      off = packed * a.row;
+      soff = packed * a.s_row;
+    } else {
+      ok = ok && page >= 0 && page < a.limit;
+      off = page * a.page + slot * a.row;
+      soff = page * a.s_page + slot * a.s_row;
+    }
+    uint8_t* const dst = a.dst + off + (int64_t)h * a.head;
+    uint8_t* const scl = a.scale + soff + (int64_t)h * a.s_head;
+
+    if (a.kind == KF16 || a.kind == KBF16) {
+      if (a.rotate) {
+        float x[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) x[k] = elem16((uint32_t)raw[k >> 1], k & 1, BF);
+        if (p.interleaved) {
+          rotate8(x, c, s, i, p.half, true);
+        } else {
+          // (every lane takes part in the exchange)
+          i32x4 other;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) other[e] = __shfl(raw[e], partner);
+          if (rot_lane) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const float y = elem16((uint32_t)other[k >> 1], k & 1, BF);
+              x[k] = i < hc ? x[k] * c[k] - y * s[k] : x[k] * c[k] + y * s[k];
+            }
+          }
+        }
+        typedef __attribute__((ext_vector_type(8))) float f32x8;
+        f32x8 v;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = x[k];
+        if constexpr (BF)
+          raw = __builtin_bit_cast(i32x4, __builtin_convertvector(v, bf16x8));
+        else
+          raw = __builtin_bit_cast(i32x4, __builtin_convertvector(v, f16x8));
+      }
+      if (ok) *reinterpret_cast<i32x4*>(dst + 16 * i) = raw;
+      continue;
+    }
+
+    // encoded types: in float64 up to the one rounding
+    double y[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) y[k] = elem16((uint32_t)raw[k >> 1], k & 1, BF);
+    if (a.rotate) {
+      if (p.interleaved) {
+        rotate8(y, c, s, i, p.half, true);
+      } else {
+        i32x4 other;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) other[e] = __shfl(raw[e], partner);
+        if (rot_lane) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const double z = elem16((uint32_t)other[k >> 1], k & 1, BF);
+            y[k] = i < hc ? y[k] * c[k] - z * s[k] : y[k] * c[k] + z * s[k];
+          }
+        }
+      }
+    }
+    if (a.kind == KF8E4M3 || a.kind == KF8E5M2) {
+      const float top = a.kind == KF8E4M3 ? 448.f : 57344.f;
+      float f[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float v = (float)y[k];
+        f[k] = v != v ? v : fminf(fmaxf(v, -top), top);
+      }
+      int w[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        if (a.kind == KF8E4M3) {
+          w[e] = __builtin_amdgcn_cvt_pk_fp8_f32(f[4 * e], f[4 * e + 1], 0, false);
+          w[e] = __builtin_amdgcn_cvt_pk_fp8_f32(f[4 * e + 2], f[4 * e + 3], w[e], true);
+        } else {
+          w[e] = __builtin_amdgcn_cvt_pk_bf8_f32(f[4 * e], f[4 * e + 1], 0, false);
+          w[e] = __builtin_amdgcn_cvt_pk_bf8_f32(f[4 * e + 2], f[4 * e + 3], w[e], true);
+        }
+      }
+      if (ok) *reinterpret_cast<int2*>(dst + 8 * i) = int2{w[0], w[1]};
+      continue;
+    }
+    double top = 0.0;
+    bool odd = false;                  // an infinity or NaN
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const double m = fabs(y[k]);
+      odd = odd || !(m < __builtin_inf());
+      top = fmax(top, m);
+    }
+    if (a.kind == KI8) {
+      odd = lanes_any<16>(odd);
+      top = lanes_max<16>(top);
+      const float sc = (float)(top / 127.0);
+      uint32_t w[2] = {0, 0};
+      if (!odd && sc > 0.f) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int q = (int)fmin(fmax(rint(y[k] / (double)sc), -127.0), 127.0);
+          w[k >> 2] |= (uint32_t)(q & 255) << (8 * (k & 3));
+        }
+      }
+      if (ok) {
+        *reinterpret_cast<uint2*>(dst + 8 * i) = uint2{w[0], w[1]};
+        if (i == 0) *reinterpret_cast<float*>(scl) = odd ? __builtin_nanf("") : sc;
+      }
+      continue;
+    }
+    // MXFP4: groups of 32 elements are 4 lanes
+    odd = lanes_any<4>(odd);
+    top = lanes_max<4>(top);
+    const int ex = (int)((__builtin_bit_cast(uint64_t, top) >> 52) & 2047) - 1023;
+    const int e8 = top == 0.0 ? 0 : min(max(ex - 2 + 127, 0), 254);
+    const double inv = __builtin_bit_cast(double, (uint64_t)(127 - e8 + 1023) << 52);
+    uint32_t w = 0;
+    if (!odd) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        // E2M1: steps of 1/2 below 2, 1 below 4, 2 above; codes 0..4, 4..6, 6..7
+        const double m = fabs(y[k]) * inv;
+        const double r = m < 2.0 ? rint(2.0 * m) : m < 4.0 ? rint(m) + 2.0 : rint(0.5 * m) + 4.0;
+        uint32_t code = (uint32_t)(int)fmin(r, 7.0);
+        if (code && y[k] < 0.0) code |= 8;
+        w |= code << (4 * k);
+      }
+    }
+    if (ok) {
+      *reinterpret_cast<uint32_t*>(dst + 4 * i) = w;
+      if ((i & 3) == 0) scl[i >> 2] = odd ? 255 : (uint8_t)e8;
+    }
+  }
+}
+
+}  // namespace msa

@@ -1,0 +1,217 @@
+// Host side of msa_attention and msa_block_attention: argument validation (all
+// of it before any HIP call), the split of the work, and the launch of one
+// gfx950 kernel, or two where the keys are split, on the caller's stream.
+// Nothing is allocated or kept between calls.
+#include "msa_index_score.h"
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+
+#include "msa_attention.hpp"
+#include "msa_host.hpp"
+
+namespace {
+
+using msa::AttnParams;
+
+constexpr int64_t kMaxSplit = 64;      // one lane per part in the join
+
+struct Plan {
+  int rows;          // rows per tile: 16 (attn_rows_kernel), 128 or 256 (attn_tile_kernel)
+  int hpt, tpt, hchunks;
+  int64_t ntiles;
+  int nsplit, min_blocks;
+};
+
+// Tiles of 16 rows when the requests' new tokens fill no more on average (or
+// each token has blocks of its own); else 128 rows, or 256 where the batch
+// holds enough of them.  Few tiles are split over the keys until the parts
+// cover the chip's 256 CUs several times; a part takes at least min_blocks
+// blocks, whatever the table's width.
+Plan plan_for(int64_t T, int64_t B, int64_t Hq, int64_t Hkv, int64_t MB, int64_t nsel) {
+  Plan p{};
+  const int64_t g = Hq / Hkv;
+  const bool few = nsel > 0 || T * std::min<int64_t>(g, 16) <= 16 * B;
+  p.rows = few ? msa::kAttnRows : 128;
+  if (!few) {
+    const int64_t big = (T * std::min<int64_t>(g, 256) + 255) / 256 * Hkv;
+    if (T * std::min<int64_t>(g, 256) >= 192 * B && big >= 128) p.rows = 256;
+  }
+  p.hpt = (int)std::min<int64_t>(g, p.rows);
+  p.tpt = nsel > 0 ? 1 : p.rows / p.hpt;
+  p.hchunks = (int)((g + p.hpt - 1) / p.hpt);
+  p.ntiles = std::min<int64_t>(T, (T + B * (p.tpt - 1)) / p.tpt);
+  const int64_t items = std::max<int64_t>(p.ntiles * Hkv * p.hchunks, 1);
+  const int64_t blocks = std::max<int64_t>(nsel > 0 ? std::min(nsel, MB) : MB, 1);
+  p.min_blocks = few ? 2 : 4;
+  const int64_t want = few ? 2048 : 1024, enough = few ? 1024 : 256;
+  int64_t n = items >= enough ? 1 : (want + items - 1) / items;
+  n = std::min(n, (blocks + p.min_blocks - 1) / p.min_blocks);
+  p.nsplit = (int)std::max<int64_t>(1, std::min(n, kMaxSplit));
+  return p;
+}
+
+int64_t workspace_for(const Plan& p, int64_t T, int64_t Hq) {
+  return p.nsplit > 1 ? p.nsplit * T * Hq * (int64_t)(msa::kD * sizeof(float) + sizeof(float2)) : 0;
+}
+
+template <int KK>
+hipError_t launch(const AttnParams& p, const Plan& plan, int64_t grid, hipStream_t s) {
+  hipError_t e;
+  const dim3 gr((unsigned)grid);
+  if (plan.rows == msa::kAttnRows)
+    e = p.blocks ? msa::launch_kernel(msa::attn_rows_kernel<KK, true>, gr, dim3(256), s, p)
+                 : msa::launch_kernel(msa::attn_rows_kernel<KK, false>, gr, dim3(256), s, p);
+  else if (plan.rows == 256)
+    e = msa::launch_kernel(msa::attn_tile_kernel<KK, 8>, gr, dim3(512), s, p);
+  else
+    e = msa::launch_kernel(msa::attn_tile_kernel<KK, 4>, gr, dim3(256), s, p);
+  if (e == hipSuccess && p.nsplit > 1)
+    e = msa::launch_kernel(msa::attn_join_kernel<KK>, dim3((unsigned)((p.T * p.Hq + 3) / 4)),
+                           dim3(256), s, p);
+  return e;
+}
+
+msa_status_t run(const msa_tensor_t* query, const msa_tensor_t* key, const msa_tensor_t* value,
+                 const int32_t* blocks, int64_t num_blocks, bool selected,
+                 const int32_t* block_table, int64_t max_blocks, const int32_t* cu_seqlens_q,
+                 const int32_t* kv_len, int32_t batch, int32_t block_size, int32_t layout,
+                 int32_t sparse_mode, float softmax_scale, void* out, float* lse, void* workspace,
+                 int64_t workspace_bytes, void* stream) {
+  if (!query || !key || !value || !cu_seqlens_q) return MSA_ERR_NULL;
+  if (batch > 0 && !kv_len) return MSA_ERR_NULL;
+  if (query->ndim == 3 && query->shape[0] > 0 && !out) return MSA_ERR_NULL;
+  if (layout != MSA_LAYOUT_TND && layout != MSA_LAYOUT_BBND && layout != MSA_LAYOUT_BNBD)
+    return MSA_ERR_LAYOUT;
+  const bool paged = layout != MSA_LAYOUT_TND;
+  if (query->dtype != MSA_DTYPE_F16 && query->dtype != MSA_DTYPE_BF16) return MSA_ERR_DTYPE;
+  if (key->dtype != query->dtype || value->dtype != query->dtype) return MSA_ERR_DTYPE;
+
+  // query [T, Hq, D]: rows of a wider projection's rows
+  if (query->ndim != 3) return MSA_ERR_SHAPE;
+  const int64_t T = query->shape[0], Hq = query->shape[1], D = query->shape[2];
+  if (T < 0 || Hq < 1 || D != msa::kD || block_size != msa::kP) return MSA_ERR_SHAPE;
+  const int64_t q_row = T > 1 ? query->stride[0] : Hq * D;
+  if (!msa::compact_axis(D, query->stride[2], 1) || !msa::compact_axis(Hq, query->stride[1], D) ||
+      q_row < Hq * D || (q_row * 2) % 16)
+    return MSA_ERR_STRIDE;
+
+  msa::CacheView kv, vv;
+  msa_status_t st = msa::cache_view(*key, layout, msa::kD, msa::kP, true, kv);
+  if (st != MSA_OK) return st;
+  st = msa::cache_view(*value, layout, msa::kD, msa::kP, true, vv);
+  if (st != MSA_OK) return st;
+  if (kv.pages != vv.pages || kv.heads != vv.heads || Hq % kv.heads) return MSA_ERR_SHAPE;
+  const int64_t Hkv = kv.heads;
+
+  if (max_blocks < 0 || batch < 0) return MSA_ERR_SHAPE;
+  if (paged) {
+    if (!block_table && batch > 0) return MSA_ERR_NULL;
+    if (max_blocks < 1) return MSA_ERR_SHAPE;
+  } else if (block_table) {
+    return MSA_ERR_SHAPE;   // packed keys take no block table
+  }
+  if (batch == 0 && T > 0) return MSA_ERR_SHAPE;
+  if (sparse_mode != 0 && sparse_mode != 3) return MSA_ERR_ATTR;
+  if (!(softmax_scale > 0.f) || !std::isfinite(softmax_scale * msa::kLog2e)) return MSA_ERR_ATTR;
+  if (selected) {
+    if (num_blocks < 1 || num_blocks > 64) return MSA_ERR_ATTR;
+    if (T > 0 && !blocks) return MSA_ERR_NULL;
+    if (reinterpret_cast<uintptr_t>(blocks) & 3u) return MSA_ERR_STRIDE;
+  }
+  // sizes the kernels index with 32-bit integers
+  if (max_blocks > (1 << 24) || Hq > (1 << 16) || batch > (1 << 30) || T > INT32_MAX)
+    return MSA_ERR_SHAPE;
+  if (!msa::aligned16(query->data) || !msa::aligned16(out) || !msa::aligned16(workspace) ||
+      (reinterpret_cast<uintptr_t>(lse) & 3u))
+    return MSA_ERR_STRIDE;
+  if (T == 0) return MSA_OK;
+
+  const Plan plan = plan_for(T, batch, Hq, Hkv, max_blocks, selected ? num_blocks : 0);
+  const int64_t need = workspace_for(plan, T, Hq);
+  if (need > 0 && (!workspace || workspace_bytes < need)) return MSA_ERR_WORKSPACE;
+  const int64_t grid = plan.ntiles * Hkv * plan.hchunks * plan.nsplit;
+  if (grid > INT32_MAX || T * Hq > (int64_t)INT32_MAX * 4) return MSA_ERR_SHAPE;
+
+  AttnParams p{};
+  p.q = static_cast<const uint8_t*>(query->data);
+  p.k = static_cast<const uint8_t*>(key->data);
+  p.v = static_cast<const uint8_t*>(value->data);
+  p.block_table = paged ? block_table : nullptr;
+  p.cu_q = cu_seqlens_q;
+  p.kv_len = kv_len;
+  p.blocks = selected ? blocks : nullptr;
+  p.out = static_cast<uint8_t*>(out);
+  p.lse = lse;
+  p.part_o = static_cast<float*>(workspace);
+  p.part_ml = reinterpret_cast<float2*>(static_cast<float*>(workspace) +
+                                        (need > 0 ? plan.nsplit * T * Hq * msa::kD : 0));
+  p.q_row_stride = q_row * 2;
+  p.k_page_stride = kv.page;
+  p.v_page_stride = vv.page;
+  p.k_row_stride = (int32_t)kv.row;
+  p.v_row_stride = (int32_t)vv.row;
+  p.k_head_stride = (int32_t)kv.head;
+  p.v_head_stride = (int32_t)vv.head;
+  p.keys = paged ? 0 : kv.pages;
+  p.T = T;
+  p.B = batch;
+  p.Hq = (int32_t)Hq;
+  p.Hkv = (int32_t)Hkv;
+  p.g = (int32_t)(Hq / Hkv);
+  p.MB = (int32_t)std::max<int64_t>(max_blocks, 1);
+  p.NP = paged ? (int32_t)kv.pages : 0;
+  p.nsel = selected ? (int32_t)num_blocks : 0;
+  p.paged = paged ? 1 : 0;
+  p.causal = sparse_mode == 3 ? 1 : 0;
+  p.c = softmax_scale * msa::kLog2e;
+  p.hpt = plan.hpt;
+  p.tpt = plan.tpt;
+  p.hchunks = plan.hchunks;
+  p.ntiles = (int32_t)plan.ntiles;
+  p.nsplit = plan.nsplit;
+  p.min_blocks = plan.min_blocks;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  const hipError_t e = query->dtype == MSA_DTYPE_BF16 ? launch<msa::KBF16>(p, plan, grid, s)
+                                                      : launch<msa::KF16>(p, plan, grid, s);
+  return e == hipSuccess ? MSA_OK : MSA_ERR_HIP;
+}
+
+}  // namespace
+
+extern "C" {
+
+msa_status_t msa_attention(const msa_tensor_t* query, const msa_tensor_t* key,
+                           const msa_tensor_t* value, const int32_t* block_table,
+                           int64_t max_blocks, const int32_t* cu_seqlens_q, const int32_t* kv_len,
+                           int32_t batch, int32_t block_size, int32_t layout, int32_t sparse_mode,
+                           float softmax_scale, void* out, float* lse, void* workspace,
+                           int64_t workspace_bytes, void* stream) {
+  return run(query, key, value, nullptr, 0, false, block_table, max_blocks, cu_seqlens_q, kv_len,
+             batch, block_size, layout, sparse_mode, softmax_scale, out, lse, workspace,
+             workspace_bytes, stream);
+}
+
+msa_status_t msa_block_attention(const msa_tensor_t* query, const msa_tensor_t* key,
+                                 const msa_tensor_t* value, const int32_t* blocks,
+                                 int32_t num_blocks, const int32_t* block_table,
+                                 int64_t max_blocks, const int32_t* cu_seqlens_q,
+                                 const int32_t* kv_len, int32_t batch, int32_t block_size,
+                                 int32_t layout, int32_t sparse_mode, float softmax_scale,
+                                 void* out, float* lse, void* workspace, int64_t workspace_bytes,
+                                 void* stream) {
+  return run(query, key, value, blocks, num_blocks, true, block_table, max_blocks, cu_seqlens_q,
+             kv_len, batch, block_size, layout, sparse_mode, softmax_scale, out, lse, workspace,
+             workspace_bytes, stream);
+}
+
+int64_t msa_attention_workspace(int64_t T, int32_t batch, int32_t Hq, int32_t Hkv,
+                                int64_t max_blocks, int32_t num_blocks) {
+  if (T < 1 || batch < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv || T > INT32_MAX || max_blocks < 0 ||
+      max_blocks > (1 << 24) || num_blocks < 0 || num_blocks > 64)
+    return 0;
+  return workspace_for(plan_for(T, batch, Hq, Hkv, max_blocks, num_blocks), T, Hq);
+}
+
+}  // extern "C"

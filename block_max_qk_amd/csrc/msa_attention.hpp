@@ -1,0 +1,717 @@
+// Attention kernels of the MSA layer (gfx950 only): dense attention of the new
+// tokens over a paged or packed cache (msa_attention) and attention over the
+// blocks that the top-k selection names (msa_block_attention).
+//
+//   S = c <q, k_j>, c = softmax_scale * log2(e), over the visible j
+//   m = max S,  l = sum 2^(S - m),  out = sum 2^(S - m) v_j / l,
+//   lse = ln 2 (m + log2 l)
+//
+// in one pass over the keys with the running m and l.  Both products are taken
+// transposed, with the keys (then the head elements) as the MFMA's M side and
+// the rows -- (query token, head) pairs of one KV head -- as its N side:
+// S^T = K Q^T leaves a lane with many keys of ONE row, so m and l are mostly
+// in-register reductions, and O^T = V^T P^T takes the lane's own weights as
+// its B operand without moving them: the order of the keys inside an MFMA's
+// contraction is free, so V is read (transposed, ds_read_b64_tr_b16) in the
+// order in which S^T left the keys.  The accumulators' columns are the rows
+// too, so a row's rescaling factor is already in the lane that needs it.
+// P is rounded to the operands' type (to nearest), which is what the MFMA
+// takes; m, l and both accumulators are float32.
+#pragma once
+
+#include "msa_device.hpp"
+
+namespace msa {
+
+struct AttnParams {
+  const uint8_t* q;            // query rows, q_row_stride bytes per token
+  const uint8_t* k;
+  const uint8_t* v;
+  const int32_t* block_table;  // [B, MB] (paged) or nullptr
+  const int32_t* cu_q;         // [B+1]
+  const int32_t* kv_len;       // [B]
+  const int32_t* blocks;       // [T, Hkv, nsel] selected blocks, or nullptr
+  uint8_t* out;                // [T, Hq, D], the query's type
+  float* lse;                  // [T, Hq] or nullptr
+  float* part_o;               // [nsplit, T, Hq, D], with nsplit > 1
+  float2* part_ml;             // [nsplit, T, Hq]: m and l
+  int64_t q_row_stride;        // bytes between query tokens
+  int64_t k_page_stride, v_page_stride;   // bytes between pages (paged)
+  int32_t k_row_stride, v_row_stride;     // bytes between key tokens
+  int32_t k_head_stride, v_head_stride;   // bytes between KV heads
+  int64_t keys;                // packed key tokens (T2)
+  int64_t T;
+  int32_t B, Hq, Hkv, g;
+  int32_t MB, NP, nsel;
+  int32_t paged, causal;
+  float c;                     // softmax_scale * log2(e)
+  int32_t hpt, tpt, hchunks, ntiles;      // as in Params
+  int32_t nsplit;              // parts that a tile's blocks are split into
+  int32_t min_blocks;          // blocks per part at least
+};
+
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kLn2 = 0.69314718055994530942f;
+
+// A tile of query tokens of one request.
+struct AttnTile {
+  int valid;
+  int t0, ntok, i0;            // first token, tokens, index of the first in the request
+  int b, Lq, L;                // request, its new tokens, its keys
+  int64_t koff;                // packed offset of the request's keys
+};
+
+// The tile-th tile of tpt tokens: a prefix sum of the requests' tile counts,
+// 64 requests at a time (every lane of the wave takes part).  Lengths that
+// break the rules (negative, past the tensors) are cut to what the tensors
+// hold, so that no address leaves them.
+__device__ __forceinline__ AttnTile attn_tile(const AttnParams& p, int tile) {
+  AttnTile w;
+  w.valid = 0;
+  const int l = lane_id();
+  int acc = 0;
+  int64_t kacc = 0;
+  for (int base = 0; base < p.B; base += 64) {
+    const int b = base + l;
+    int t0 = 0, lq = 0, kv = 0;
+    if (b < p.B) {
+      t0 = p.cu_q[b];
+      lq = max(p.cu_q[b + 1] - t0, 0);
+      kv = max(p.kv_len[b], 0);
+    }
+    const int n = (int)(((int64_t)lq + p.tpt - 1) / p.tpt);
+    const int incl = wave_incl_scan(n);
+    const int64_t kincl = wave_incl_scan((int64_t)kv);
+    const int total = lane_at(incl, 63);
+    if (tile < acc + total) {
+      const unsigned long long m = __ballot(acc + incl > tile);
+      const int src = __builtin_amdgcn_readfirstlane(__ffsll((long long)m) - 1);
+      const int tin = tile - (acc + lane_at(incl, src) - lane_at(n, src));
+      w.b = base + src;
+      w.Lq = lane_at(lq, src);
+      w.i0 = tin * p.tpt;
+      w.t0 = lane_at(t0, src) + w.i0;
+      const int64_t room = p.T - (int64_t)w.t0;
+      w.ntok = (int)min((int64_t)min(p.tpt, w.Lq - w.i0), w.t0 < 0 ? (int64_t)0 : room);
+      w.koff = kacc + lane_at(kincl, src) - lane_at(kv, src);
+      w.L = lane_at(kv, src);
+      if (p.paged)
+        w.L = (int)min((int64_t)w.L, (int64_t)p.MB * kP);
+      else
+        w.L = (int)max(min((int64_t)w.L, p.keys - w.koff), (int64_t)0);
+      w.valid = w.ntok > 0;
+      return w;
+    }
+    acc += total;
+    kacc += lane_at(kincl, 63);
+  }
+  return w;
+}
+
+// Last visible key of the request's i-th new token: kv_len - L_q + i under
+// the causal mode, the last key without it.  (The position comes from kv_len
+// as given; attn_tile has cut L to the keys that exist.)
+__device__ __forceinline__ int attn_last(const AttnParams& p, const AttnTile& w, int len, int i) {
+  return min(p.causal ? len - w.Lq + i : w.L - 1, w.L - 1);
+}
+
+// Two floats -> one register of two 16-bit operands, rounded to nearest.
+template <int KK>
+__device__ __forceinline__ int pack2(float a, float b) {
+  typedef __attribute__((ext_vector_type(2))) float f32x2;
+  typedef __attribute__((ext_vector_type(2))) __bf16 bf16x2;
+  const f32x2 v = {a, b};
+  if constexpr (KK == KBF16)
+    return __builtin_bit_cast(int, __builtin_convertvector(v, bf16x2));
+  else
+    return __builtin_bit_cast(int, __builtin_convertvector(v, f16x2));
+}
+
+// ds_read_b64_tr_b16: within each 16 lanes, lane i gives the address of
+// columns 4 (i % 4) .. + 3 of row i / 4 of a 4 x 16 block of 16-bit elements
+// and receives the four rows of column i.
+typedef __attribute__((ext_vector_type(4))) short s16x4;
+typedef __attribute__((ext_vector_type(2))) int i32x2;
+__device__ __forceinline__ i32x2 lds_read_tr(const uint8_t* p) {
+  return __builtin_bit_cast(
+      i32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)p));
+}
+
+__device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// x[l] + x[l ^ 32], x[l] + x[l ^ 16] (as max_xor32 and max_xor16)
+__device__ __forceinline__ float sum_xor32(float x) {
+  uint32_t a = __builtin_bit_cast(uint32_t, x), b = a;
+  asm volatile("s_nop 1\n\tv_permlane32_swap_b32 %0, %1\n\ts_nop 1\n\tv_add_f32 %0, %0, %1"
+               : "+v"(a), "+v"(b));
+  return __builtin_bit_cast(float, a);
+}
+__device__ __forceinline__ float sum_xor16(float x) {
+  uint32_t a = __builtin_bit_cast(uint32_t, x), b = a;
+  asm volatile("s_nop 1\n\tv_permlane16_swap_b32 %0, %1\n\ts_nop 1\n\tv_add_f32 %0, %0, %1"
+               : "+v"(a), "+v"(b));
+  return __builtin_bit_cast(float, a);
+}
+
+// Registers whose loads are waited for here, not at their first use inside a
+// loop, where the wait would count the loop's own copies.
+__device__ __forceinline__ void landed(i32x4& x) { asm volatile("" : "+v"(x)); }
+
+// The running maximum may lag the true one by this much (in powers of two)
+// before the accumulators are rescaled: weights then reach 2^8, exact in
+// range for both 16-bit types and float32 sums, and almost every stage after
+// the first skips the rescaling.
+constexpr float kMaxLag = 8.f;
+
+// ---------------------------------------------------------------------------
+// Few rows: 16 rows a tile, the keys split over waves and workgroups.
+//
+// A tile is tpt tokens x hpt heads (at most 16 rows) of one KV head.  Its
+// blocks -- all visible ones, or the token's selected ones -- are split into
+// nsplit parts, one workgroup each; within a workgroup wave w takes keys
+// 32w .. 32w + 31 of every block, with its own m, l and accumulators, and the
+// four waves' results are joined through LDS at the end.  The bound is the
+// reading of keys and values: each wave copies its 16 KB of a block straight
+// into its own part of the LDS, one block ahead, with no barrier in the loop.
+// ---------------------------------------------------------------------------
+
+constexpr int kAttnRows = 16;
+constexpr int kRowWaves = 4;
+constexpr int kRowStage = 16384;     // 32 keys' K and V rows
+
+template <int KK, bool SEL>
+__global__ __launch_bounds__(256, 1) void attn_rows_kernel(AttnParams p) {
+  __shared__ __attribute__((aligned(16))) uint8_t ring[kRowWaves][2][kRowStage];
+  const int item = blockIdx.x;
+  const int split = item % p.nsplit;
+  int rest = item / p.nsplit;
+  const int hc = rest % p.hchunks;
+  rest /= p.hchunks;
+  const int hk = rest % p.Hkv;
+  const AttnTile w = attn_tile(p, rest / p.Hkv);
+  if (!w.valid) return;
+
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int l = lane_id();
+  const int n = l & 15, G = l >> 4;
+  const int len = p.kv_len[w.b];
+
+  // this lane's row (column n of every MFMA result)
+  const int ti = n / p.hpt;
+  const int hg = hc * p.hpt + (n - ti * p.hpt);
+  const bool row_ok = ti < w.ntok && ti < p.tpt && hg < p.g;
+  const int lim = row_ok ? attn_last(p, w, len, w.i0 + ti) : -1;
+  const int lim_lo = attn_last(p, w, len, w.i0);
+  const int lim_hi = attn_last(p, w, len, w.i0 + w.ntok - 1);
+  const int nb = lim_hi >= 0 ? lim_hi / kP + 1 : 0;    // blocks with a visible key
+
+  // the part's blocks: [b0, b1) of the visible ones, or of the selected list
+  int sel = -1, total = nb;
+  if constexpr (SEL) {
+    // one entry per lane; entries outside the visible blocks and repeats of
+    // an earlier entry count as none; the rest move to the front.  (The top-k
+    // selection gives ascending entries in front of its -1 tail: nothing to
+    // look for then.)
+    int e = l < p.nsel ? p.blocks[((int64_t)w.t0 * p.Hkv + hk) * p.nsel + l] : -1;
+    bool ok = e >= 0 && e < nb;
+    const int prev = __shfl_up(e, 1);
+    const unsigned long long front = __ballot(ok);
+    if ((front & (front + 1)) || __ballot(ok && l > 0 && prev >= e)) {
+      for (int i = 0; i + 1 < p.nsel; ++i) ok = ok && !(l > i && e == lane_at(e, i));
+    }
+    const unsigned long long m = __ballot(ok);
+    total = __popcll(m);
+    // lane i receives the i-th entry: every kept lane sends its own to its rank
+    const int rank = __popcll(m & ((1ull << l) - 1));
+    sel = __builtin_amdgcn_ds_permute((ok ? rank : 63) << 2, e);
+    if (l >= total) sel = -1;
+  }
+  const int parts = max(1, min(p.nsplit, (total + p.min_blocks - 1) / p.min_blocks));
+  const int b0 = (int)((int64_t)total * split / parts);
+  const int b1 = split < parts ? (int)((int64_t)total * (split + 1) / parts) : b0;
+  const int nst = max(b1 - b0, 0);
+
+  const int64_t out_row = ((int64_t)(w.t0 + ti) * p.Hq + hk * p.g + hg);
+
+  // query fragments: k step s of group G is elements 32 s + 8 G .. + 7
+  i32x4 qv[4];
+#pragma unroll
+  for (int s = 0; s < 4; ++s) qv[s] = i32x4{0, 0, 0, 0};
+  if (row_ok) {
+    const uint8_t* qr = p.q + (int64_t)(w.t0 + ti) * p.q_row_stride + (hk * p.g + hg) * (2 * kD);
+#pragma unroll
+    for (int s = 0; s < 4; ++s) qv[s] = ld16(qr + 64 * s + 16 * G);
+  }
+
+  // page numbers, one per lane, 64 blocks at a time (-1: no page)
+  int pidx = -1, pbase = 0;
+  auto page_of = [&](int blk) -> int {
+    const int pg = p.block_table[(int64_t)w.b * p.MB + blk];
+    return pg >= 0 && pg < p.NP ? pg : -1;
+  };
+  auto load_pages = [&](int from) {
+    pbase = from;
+    const int i = b0 + from + l;
+    if constexpr (!SEL) {
+      pidx = consumed(p.paged && from + l < nst ? page_of(i) : -1);
+    }
+  };
+  if constexpr (SEL) {
+    // (selected blocks: at most 64, all at once)
+    if (l < total) pidx = p.paged ? page_of(sel) : -1;
+  } else {
+    load_pages(0);
+  }
+
+  // copies of one block's 32 keys: instruction i brings rows 4 i .. 4 i + 3
+  // (16 lanes to a row), the 16-byte chunks of row r permuted by the XORs
+  // that the reads below undo
+  const int cr = l >> 4, cc = l & 15;
+  uint8_t* const mine = &ring[wave][0][0];
+  struct Block { int beta, page; };
+  auto block_at = [&](int s) -> Block {
+    Block x;
+    if constexpr (SEL) {
+      x.beta = lane_at(sel, b0 + s);
+      x.page = lane_at(pidx, b0 + s);
+    } else {
+      x.beta = b0 + s;
+      x.page = lane_at(pidx, s - pbase);
+    }
+    return x;
+  };
+  auto copy = [&](uint8_t* dst, const Block& x) {
+    const int j0 = x.beta * kP + 32 * wave;
+    const bool there = !p.paged || x.page >= 0;
+    const int nvalid = __builtin_amdgcn_readfirstlane(there ? max(0, min(32, w.L - j0)) : 0);
+    const int64_t kb = p.paged ? (int64_t)max(x.page, 0) * p.k_page_stride +
+                                     (int64_t)(32 * wave) * p.k_row_stride
+                               : (w.koff + j0) * p.k_row_stride;
+    const int64_t vb = p.paged ? (int64_t)max(x.page, 0) * p.v_page_stride +
+                                     (int64_t)(32 * wave) * p.v_row_stride
+                               : (w.koff + j0) * p.v_row_stride;
+    const __amdgpu_buffer_rsrc_t kr = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<uint8_t*>(p.k + uniform64(kb + (int64_t)hk * p.k_head_stride)), 0,
+        nvalid * p.k_row_stride, kBufferWord3);
+    const __amdgpu_buffer_rsrc_t vr = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<uint8_t*>(p.v + uniform64(vb + (int64_t)hk * p.v_head_stride)), 0,
+        nvalid * p.v_row_stride, kBufferWord3);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int r = 4 * i + cr;
+      buffer_copy16_lds(kr, dst + 1024 * i, (uint32_t)(r * p.k_row_stride + 16 * (cc ^ (r & 15))));
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int r = 4 * i + cr;
+      buffer_copy16_lds(vr, dst + 8192 + 1024 * i,
+                        (uint32_t)(r * p.v_row_stride + 16 * (cc ^ ((r & 7) << 1))));
+    }
+  };
+
+  f32x4 o[8];
+#pragma unroll
+  for (int d = 0; d < 8; ++d) o[d] = f32x4{0.f, 0.f, 0.f, 0.f};
+  float m = -__builtin_inff(), lsum = 0.f;
+
+  // One block: its next one's copies into `dst`, then its own keys and values
+  // at kt.  (The two never overlap -- they are the ring's two halves -- and
+  // the parameters say so: reads of LDS that may alias a copy in flight would
+  // wait for all copies.)
+  auto step = [&](const uint8_t* __restrict kt, uint8_t* __restrict dst, const Block& cur,
+                  const Block& next, bool more) __attribute__((always_inline)) {
+    if (more) {
+      copy(dst, next);
+      asm volatile("s_waitcnt vmcnt(16)" ::: "memory");
+    } else {
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    }
+    const uint8_t* vt = kt + 8192;
+    const int j0 = cur.beta * kP + 32 * wave;
+    const bool there = !p.paged || cur.page >= 0;
+
+    // S^T: tile a holds keys j0 + 4 G + r, tile b keys j0 + 16 + 4 G + r of row n
+    f32x4 sa = {0.f, 0.f, 0.f, 0.f}, sb = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int ch = ((4 * k + G) ^ n) << 4;
+      sa = mfma16x16x32<KK>(*reinterpret_cast<const i32x4*>(kt + n * 256 + ch), qv[k], sa);
+      sb = mfma16x16x32<KK>(*reinterpret_cast<const i32x4*>(kt + (16 + n) * 256 + ch), qv[k], sb);
+    }
+    if (!there || j0 + 31 > lim_lo) {
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int j = j0 + 4 * G + r;
+        sa[r] = there && j <= lim ? sa[r] : -__builtin_inff();
+        sb[r] = there && j + 16 <= lim ? sb[r] : -__builtin_inff();
+      }
+    }
+    float mx = fmaxf(fmaxf(fmaxf(sa[0], sa[1]), fmaxf(sa[2], sa[3])),
+                     fmaxf(fmaxf(sb[0], sb[1]), fmaxf(sb[2], sb[3])));
+    mx = max_xor32(max_xor16(mx)) * p.c;
+    if (__ballot(mx > m + kMaxLag)) {
+      const float mn = fmaxf(m, mx);
+      const float alpha = exp2_hw(m - (mn == -__builtin_inff() ? 0.f : mn));
+      m = mn;
+      lsum *= alpha;
+#pragma unroll
+      for (int d = 0; d < 8; ++d) o[d] *= alpha;
+    }
+    const float ms = m == -__builtin_inff() ? 0.f : m;
+    float pa[4], pb[4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      pa[r] = exp2_hw(__builtin_fmaf(sa[r], p.c, -ms));
+      pb[r] = exp2_hw(__builtin_fmaf(sb[r], p.c, -ms));
+    }
+    lsum += ((pa[0] + pa[1]) + (pa[2] + pa[3])) + ((pb[0] + pb[1]) + (pb[2] + pb[3]));
+    const i32x4 pf = {pack2<KK>(pa[0], pa[1]), pack2<KK>(pa[2], pa[3]), pack2<KK>(pb[0], pb[1]),
+                      pack2<KK>(pb[2], pb[3])};
+#pragma unroll
+    for (int d = 0; d < 8; ++d) {
+      const int r = 4 * G + (n >> 2);
+      const int ch = ((2 * d + ((n >> 1) & 1)) ^ ((r & 7) << 1)) * 16 + (n & 1) * 8;
+      const i32x2 v0 = lds_read_tr(vt + r * 256 + ch);
+      const i32x2 v1 = lds_read_tr(vt + (r + 16) * 256 + ch);
+      o[d] = mfma16x16x32<KK>(i32x4{v0[0], v0[1], v1[0], v1[1]}, pf, o[d]);
+    }
+  };
+
+#pragma unroll
+  for (int s = 0; s < 4; ++s) landed(qv[s]);
+  Block cur{0, -1};
+  if (nst > 0) {
+    cur = block_at(0);
+    copy(mine, cur);
+  }
+  for (int s = 0; s < nst; ++s) {
+    Block next = cur;
+    if (s + 1 < nst) {
+      if (!SEL && s + 1 - pbase >= 64) load_pages(s + 1);
+      next = block_at(s + 1);
+    }
+    // (the reads of the half that is written next are done)
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    step(mine + (s & 1) * kRowStage, mine + ((s + 1) & 1) * kRowStage, cur, next, s + 1 < nst);
+    cur = next;
+  }
+
+  // join the four waves: each writes its accumulators, m and l, then wave w
+  // joins head elements 32 w .. 32 w + 31
+  lsum = sum_xor32(sum_xor16(lsum));
+  __syncthreads();
+  float* const ol = reinterpret_cast<float*>(&ring[0][0][0]);    // [wave][row][132]
+  constexpr int OS = 132;                                        // (row stride: no bank conflicts)
+  float* const mls = ol + kRowWaves * kAttnRows * OS;            // [wave][row][2]
+#pragma unroll
+  for (int d = 0; d < 8; ++d)
+    *reinterpret_cast<f32x4*>(ol + (wave * kAttnRows + n) * OS + 16 * d + 4 * G) = o[d];
+  if (G == 0) {
+    mls[(wave * kAttnRows + n) * 2] = m;
+    mls[(wave * kAttnRows + n) * 2 + 1] = lsum;
+  }
+  __syncthreads();
+  float mt = -__builtin_inff();
+#pragma unroll
+  for (int u = 0; u < kRowWaves; ++u) mt = fmaxf(mt, mls[(u * kAttnRows + n) * 2]);
+  const float ms = mt == -__builtin_inff() ? 0.f : mt;
+  float lt = 0.f;
+  f32x4 s0 = {0.f, 0.f, 0.f, 0.f}, s1 = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int u = 0; u < kRowWaves; ++u) {
+    const float a = exp2_hw(mls[(u * kAttnRows + n) * 2] - ms);
+    lt += a * mls[(u * kAttnRows + n) * 2 + 1];
+    const float* src = ol + (u * kAttnRows + n) * OS + 32 * wave + 8 * G;
+    s0 += a * *reinterpret_cast<const f32x4*>(src);
+    s1 += a * *reinterpret_cast<const f32x4*>(src + 4);
+  }
+  if (!row_ok) return;
+  if (p.nsplit > 1) {
+    const int64_t pr = (int64_t)split * p.T * p.Hq + out_row;
+    if (wave == 0 && G == 0) p.part_ml[pr] = float2{mt, lt};
+    if (nst > 0) {
+      float* dst = p.part_o + pr * kD + 32 * wave + 8 * G;
+      *reinterpret_cast<f32x4*>(dst) = s0;
+      *reinterpret_cast<f32x4*>(dst + 4) = s1;
+    }
+    return;
+  }
+  const float inv = lt == 0.f ? 0.f : 1.f / lt;
+  const i32x4 res = {pack2<KK>(s0[0] * inv, s0[1] * inv), pack2<KK>(s0[2] * inv, s0[3] * inv),
+                     pack2<KK>(s1[0] * inv, s1[1] * inv), pack2<KK>(s1[2] * inv, s1[3] * inv)};
+  *reinterpret_cast<i32x4*>(p.out + out_row * (2 * kD) + 64 * wave + 16 * G) = res;
+  if (p.lse && wave == 0 && G == 0)
+    p.lse[out_row] = lt == 0.f ? -__builtin_inff() : (mt + __log2f(lt)) * kLn2;
+}
+
+// ---------------------------------------------------------------------------
+// The join of a split tile's parts: one wave per row, two elements a lane.
+// Rows that no request holds are left as they are.
+// ---------------------------------------------------------------------------
+
+template <int KK>
+__global__ __launch_bounds__(256) void attn_join_kernel(AttnParams p) {
+  const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  const int l = lane_id();
+  const int64_t rows = p.T * p.Hq;
+  if (row >= rows || row >= (int64_t)max(p.cu_q[p.B], 0) * p.Hq ||
+      row < (int64_t)p.cu_q[0] * p.Hq)
+    return;
+  float2 ml = {-__builtin_inff(), 0.f};
+  if (l < p.nsplit) ml = p.part_ml[l * rows + row];
+  float mt = max_xor32(max_xor16(ml.x));
+  mt = fmaxf(mt, __shfl_xor(mt, 8));
+  mt = fmaxf(mt, __shfl_xor(mt, 4));
+  mt = fmaxf(mt, __shfl_xor(mt, 2));
+  mt = fmaxf(mt, __shfl_xor(mt, 1));
+  const float ms = mt == -__builtin_inff() ? 0.f : mt;
+  const float a = exp2_hw(ml.x - ms);
+  float lt = a * ml.y;
+  lt = sum_xor32(sum_xor16(lt));
+  lt += __shfl_xor(lt, 8);
+  lt += __shfl_xor(lt, 4);
+  lt += __shfl_xor(lt, 2);
+  lt += __shfl_xor(lt, 1);
+  float2 o = {0.f, 0.f};
+  for (int s = 0; s < p.nsplit; ++s) {
+    const float as = __builtin_bit_cast(float, lane_at(__builtin_bit_cast(int, a), s));
+    const float lp = __builtin_bit_cast(float, lane_at(__builtin_bit_cast(int, ml.y), s));
+    if (lp == 0.f) continue;      // a part without visible keys wrote no sums
+    const float2 x = *reinterpret_cast<const float2*>(p.part_o + (s * rows + row) * kD + 2 * l);
+    o.x += as * x.x;
+    o.y += as * x.y;
+  }
+  const float inv = lt == 0.f ? 0.f : 1.f / lt;
+  reinterpret_cast<int*>(p.out + row * (2 * kD))[l] = pack2<KK>(o.x * inv, o.y * inv);
+  if (p.lse && l == 0)
+    p.lse[row] = lt == 0.f ? -__builtin_inff() : (mt + __log2f(lt)) * kLn2;
+}
+
+// ---------------------------------------------------------------------------
+// Many rows: 32 rows a wave, NW waves a workgroup, every wave reading the same
+// stages of 64 keys from the LDS.
+//
+// The stages' K and V rows are copied straight into a two-deep LDS ring one
+// stage ahead, through raw buffers that end at the request's last key, so
+// rows past it read zeros (a stored NaN there cannot reach a sum).
+// ---------------------------------------------------------------------------
+
+constexpr int kTileKeys = 64;
+
+template <int KK, int NW>
+__global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 2) void attn_tile_kernel(AttnParams p) {
+  constexpr int SB = kTileKeys * 256;          // bytes of a stage's K (or V) rows
+  constexpr int NI = SB / 1024 / NW;           // copies of each per wave and stage
+  __shared__ __attribute__((aligned(16))) uint8_t ring[2][2 * SB];
+  // heavy tiles (the last tokens of a request see the most keys) first; the
+  // KV head changes fastest, so that with 8 XCDs taking workgroups in turn an
+  // XCD's L2 holds the keys of few heads
+  int rest = blockIdx.x;
+  const int split = rest % p.nsplit;
+  rest /= p.nsplit;
+  const int hc = rest % p.hchunks;
+  rest /= p.hchunks;
+  const int hk = rest % p.Hkv;
+  const AttnTile w = attn_tile(p, p.ntiles - 1 - rest / p.Hkv);
+  if (!w.valid) return;
+
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int l = lane_id();
+  const int n = l & 31, h = l >> 5;
+  const int len = p.kv_len[w.b];
+  const int row = wave * 32 + n;
+  const int ti = row / p.hpt;
+  const int hg = hc * p.hpt + (row - ti * p.hpt);
+  const bool row_ok = row < p.hpt * p.tpt && ti < w.ntok && hg < p.g;
+  const int lim = row_ok ? attn_last(p, w, len, w.i0 + ti) : -1;
+  const int lim_lo = attn_last(p, w, len, w.i0);
+  const int lim_hi = attn_last(p, w, len, w.i0 + w.ntok - 1);
+  const int total = lim_hi >= 0 ? lim_hi / kP + 1 : 0;
+  const int parts = max(1, min(p.nsplit, (total + p.min_blocks - 1) / p.min_blocks));
+  const int b0 = (int)((int64_t)total * split / parts);
+  const int b1 = split < parts ? (int)((int64_t)total * (split + 1) / parts) : b0;
+  const int s0 = 2 * b0;                                   // stages [s0, s1)
+  const int s1 = b1 > b0 ? min(2 * b1, lim_hi / kTileKeys + 1) : s0;
+
+  i32x4 qv[8];
+#pragma unroll
+  for (int s = 0; s < 8; ++s) qv[s] = i32x4{0, 0, 0, 0};
+  if (row_ok) {
+    const uint8_t* qr = p.q + (int64_t)(w.t0 + ti) * p.q_row_stride + (hk * p.g + hg) * (2 * kD);
+#pragma unroll
+    for (int s = 0; s < 8; ++s) qv[s] = ld16(qr + 16 * (2 * s + h));
+  }
+
+  int pidx = -1, pbase = b0;
+  auto load_pages = [&](int from) {
+    pbase = from;
+    pidx = -1;
+    if (p.paged && from + l < b1) {
+      const int pg = p.block_table[(int64_t)w.b * p.MB + from + l];
+      pidx = pg >= 0 && pg < p.NP ? pg : -1;
+    }
+    pidx = consumed(pidx);
+  };
+  load_pages(b0);
+
+  const int cr = l >> 4, cc = l & 15;
+  uint32_t kof[NI], vof[NI];
+#pragma unroll
+  for (int i = 0; i < NI; ++i) {
+    const int r = (wave * NI + i) * 4 + cr;
+    kof[i] = (uint32_t)(r * p.k_row_stride + 16 * (cc ^ (r & 15)));
+    vof[i] = (uint32_t)(r * p.v_row_stride + 16 * (cc ^ ((r & 3) << 2)));
+  }
+  auto copy = [&](uint8_t* dst, int s, int page) {
+    const int j0 = s * kTileKeys;
+    const bool there = !p.paged || page >= 0;
+    const int nvalid = __builtin_amdgcn_readfirstlane(there ? max(0, min(kTileKeys, w.L - j0)) : 0);
+    const int in = (s & 1) * kTileKeys;          // first row within the block
+    const int64_t kb = p.paged ? (int64_t)max(page, 0) * p.k_page_stride + (int64_t)in * p.k_row_stride
+                               : (w.koff + j0) * p.k_row_stride;
+    const int64_t vb = p.paged ? (int64_t)max(page, 0) * p.v_page_stride + (int64_t)in * p.v_row_stride
+                               : (w.koff + j0) * p.v_row_stride;
+    const __amdgpu_buffer_rsrc_t kr = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<uint8_t*>(p.k + uniform64(kb + (int64_t)hk * p.k_head_stride)), 0,
+        nvalid * p.k_row_stride, kBufferWord3);
+    const __amdgpu_buffer_rsrc_t vr = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<uint8_t*>(p.v + uniform64(vb + (int64_t)hk * p.v_head_stride)), 0,
+        nvalid * p.v_row_stride, kBufferWord3);
+#pragma unroll
+    for (int i = 0; i < NI; ++i)
+      buffer_copy16_lds(kr, dst + (wave * NI + i) * 1024, kof[i]);
+#pragma unroll
+    for (int i = 0; i < NI; ++i)
+      buffer_copy16_lds(vr, dst + SB + (wave * NI + i) * 1024, vof[i]);
+  };
+  auto page_at = [&](int s) -> int {
+    if ((s >> 1) - pbase >= 64) load_pages(s >> 1);
+    return lane_at(pidx, (s >> 1) - pbase);
+  };
+
+  f32x16 o[4];
+#pragma unroll
+  for (int d = 0; d < 4; ++d) o[d] = f32x16{};
+  float m = -__builtin_inff(), lsum = 0.f;
+
+  // One stage: the next one's copies into `dst`, then its own rows at kt (as in
+  // attn_rows_kernel, the parameters say that the two do not overlap).
+  auto stage = [&](const uint8_t* __restrict kt, uint8_t* __restrict dst, int s, int cur,
+                   int page, bool more) __attribute__((always_inline)) {
+    if (more) copy(dst, s + 1, page);
+    const uint8_t* vt = kt + SB;
+    const int j0 = s * kTileKeys;
+    const bool there = !p.paged || cur >= 0;
+
+    // S^T, two tiles of 32 keys: register r of tile t is key
+    // j0 + 32 t + 8 (r / 4) + 4 h + r % 4 of row n
+    f32x16 st[2] = {f32x16{}, f32x16{}};
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int jj = 32 * t + n;
+        st[t] = mfma32x32x16<KK>(
+            *reinterpret_cast<const i32x4*>(kt + jj * 256 + (((2 * k + h) ^ (jj & 15)) << 4)), qv[k],
+            st[t]);
+      }
+    if (!there || j0 + kTileKeys - 1 > lim_lo) {
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          const int j = j0 + 32 * t + 8 * (r >> 2) + 4 * h + (r & 3);
+          st[t][r] = there && j <= lim ? st[t][r] : -__builtin_inff();
+        }
+    }
+    float mx = st[0][0];
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) mx = fmaxf(mx, st[t][r]);
+    mx = max_xor32(mx) * p.c;
+    if (__ballot(mx > m + kMaxLag)) {
+      const float mn = fmaxf(m, mx);
+      const float alpha = exp2_hw(m - (mn == -__builtin_inff() ? 0.f : mn));
+      m = mn;
+      lsum *= alpha;
+#pragma unroll
+      for (int d = 0; d < 4; ++d) o[d] *= alpha;
+    }
+    const float ms = m == -__builtin_inff() ? 0.f : m;
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        st[t][r] = exp2_hw(__builtin_fmaf(st[t][r], p.c, -ms));
+        lsum += st[t][r];
+      }
+    // O^T += V^T P^T, 16 keys a step: registers 8 u .. 8 u + 7 of a tile are
+    // keys 16 u + 4 h + {0..3} and 16 u + 8 + 4 h + {0..3}
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        i32x4 pf;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          pf[e] = pack2<KK>(st[t][8 * u + 2 * e], st[t][8 * u + 2 * e + 1]);
+        const int i = l & 15;
+        const int r = 32 * t + 16 * u + 4 * h + (i >> 2);
+#pragma unroll
+        for (int d = 0; d < 4; ++d) {
+          const int ch = ((4 * d + 2 * ((l >> 4) & 1) + ((i >> 1) & 1)) ^ ((r & 3) << 2)) * 16 +
+                         (i & 1) * 8;
+          const i32x2 v0 = lds_read_tr(vt + r * 256 + ch);
+          const i32x2 v1 = lds_read_tr(vt + (r + 8) * 256 + ch);
+          o[d] = mfma32x32x16<KK>(i32x4{v0[0], v0[1], v1[0], v1[1]}, pf, o[d]);
+        }
+      }
+  };
+
+#pragma unroll
+  for (int s = 0; s < 8; ++s) landed(qv[s]);
+  int page = -1;
+  if (s0 < s1) {
+    page = page_at(s0);
+    copy(ring[s0 & 1], s0, page);
+  }
+  for (int s = s0; s < s1; ++s) {
+    const int cur = page;
+    if (s + 1 < s1) page = page_at(s + 1);
+    // this wave's copies of stage s have landed; after the barrier everyone's
+    // have, and everyone has read stage s - 1
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    stage(ring[s & 1], ring[(s + 1) & 1], s, cur, page, s + 1 < s1);
+  }
+
+  lsum = sum_xor32(lsum);
+  if (!row_ok) return;
+  const int64_t out_row = ((int64_t)(w.t0 + ti) * p.Hq + hk * p.g + hg);
+  // register r of o[d] is head element 32 d + 8 (r / 4) + 4 h + r % 4
+  if (p.nsplit > 1) {
+    const int64_t pr = (int64_t)split * p.T * p.Hq + out_row;
+    if (h == 0) p.part_ml[pr] = float2{m, lsum};
+    if (s0 < s1) {
+#pragma unroll
+      for (int d = 0; d < 4; ++d)
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          *reinterpret_cast<f32x4*>(p.part_o + pr * kD + 32 * d + 8 * q + 4 * h) =
+              f32x4{o[d][4 * q], o[d][4 * q + 1], o[d][4 * q + 2], o[d][4 * q + 3]};
+    }
+    return;
+  }
+  const float inv = lsum == 0.f ? 0.f : 1.f / lsum;
+#pragma unroll
+  for (int d = 0; d < 4; ++d)
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      *reinterpret_cast<i32x2*>(p.out + out_row * (2 * kD) + 2 * (32 * d + 8 * q + 4 * h)) =
+          i32x2{pack2<KK>(o[d][4 * q] * inv, o[d][4 * q + 1] * inv),
+                pack2<KK>(o[d][4 * q + 2] * inv, o[d][4 * q + 3] * inv)};
+  if (p.lse && h == 0)
+    p.lse[out_row] = lsum == 0.f ? -__builtin_inff() : (m + __log2f(lsum)) * kLn2;
+}
+
+}  // namespace msa

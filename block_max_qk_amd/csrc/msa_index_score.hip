@@ -11,30 +11,22 @@
 #include <algorithm>
 #include <atomic>
 #include <cstdint>
-#include <tuple>
 
+#include "msa_host.hpp"
 #include "msa_kernels.hpp"
 #include "msa_topk.hpp"
 
 namespace {
 
 using msa::Params;
+using msa::aligned16;
+using msa::compact_axis;
+using msa::elem_bytes;
+using msa::launch_kernel;
 
 int64_t round_up16(int64_t mb) {
   if (mb < 1) mb = 1;
   return (mb + 15) / 16 * 16;
-}
-
-int elem_bytes(int32_t dt) {
-  switch (dt) {
-    case MSA_DTYPE_F16:
-    case MSA_DTYPE_BF16: return 2;
-    case MSA_DTYPE_I8:
-    case MSA_DTYPE_F8E4M3:
-    case MSA_DTYPE_F8E5M2:
-    case MSA_DTYPE_MXFP4: return 1;   // MXFP4: a byte holds two elements
-    default: return 0;
-  }
 }
 
 // Supported (query, key) element pairs (guide to msa_index_score, section 七:
@@ -47,13 +39,6 @@ bool pair_ok(int32_t qd, int32_t kd) {
   if (qd == MSA_DTYPE_F8E5M2 && kd == MSA_DTYPE_F8E5M2) return true;
   if (qd == MSA_DTYPE_MXFP4 && kd == MSA_DTYPE_MXFP4) return true;
   return false;
-}
-
-bool aligned16(const void* ptr) { return (reinterpret_cast<uintptr_t>(ptr) & 15u) == 0; }
-
-// Extent-1 axes are never addressed, so their strides are not compared.
-bool compact_axis(int64_t extent, int64_t stride, int64_t want) {
-  return extent <= 1 || stride == want;
 }
 
 // Kernel family.  Prefill tiles (hundreds of rows sharing each key block
@@ -90,22 +75,6 @@ int32_t prefill_chunk_for(int32_t dflt, int64_t W, int64_t units_per_chunk, int6
   int64_t c = (W + want - 1) / want;
   c = (c + 3) / 4 * 4;
   return (int32_t)std::min<int64_t>(std::max<int64_t>(c, 4), dflt);
-}
-
-// Launch `kern` with these arguments (converted to its parameter types) and
-// return the status of this launch alone.  (hipGetLastError after a
-// triple-chevron launch would also return, and clear, an error left pending
-// by earlier unrelated HIP calls of the caller.)
-template <typename... KA, typename... A>
-hipError_t launch_kernel(void (*kern)(KA...), dim3 grid, dim3 block, hipStream_t s, A... a) {
-  static_assert(sizeof...(KA) == sizeof...(A), "one value per kernel parameter");
-  std::tuple<KA...> vals{static_cast<KA>(a)...};
-  void* ptrs[sizeof...(KA)];
-  std::apply([&](auto&... v) {
-    int i = 0;
-    ((ptrs[i++] = static_cast<void*>(&v)), ...);
-  }, vals);
-  return hipLaunchKernel(reinterpret_cast<const void*>(kern), grid, block, ptrs, 0, s);
 }
 
 // Decode: one round of workgroups, as many as fit on the device at once,
@@ -499,9 +468,10 @@ const char* msa_status_str(int32_t s) {
     case MSA_ERR_DTYPE: return "unsupported query/key element types";
     case MSA_ERR_SHAPE: return "inconsistent shapes";
     case MSA_ERR_STRIDE: return "non-compact or misaligned axis";
-    case MSA_ERR_SCALE: return "scale must be given exactly for int8 keys";
-    case MSA_ERR_ATTR: return "sparse_mode, init_blocks, local_blocks or family out of range";
+    case MSA_ERR_SCALE: return "scale must be given exactly for int8 (and MXFP4) tensors";
+    case MSA_ERR_ATTR: return "an attribute (mode, count, scale factor, family) is out of range";
     case MSA_ERR_HIP: return "HIP launch failed";
+    case MSA_ERR_WORKSPACE: return "the workspace is smaller than the call needs";
     default: return "unknown status";
   }
 }

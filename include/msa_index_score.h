@@ -48,12 +48,17 @@ typedef enum {
   MSA_ERR_SCALE = 6,   /* int8 key without scale, or scale with a non-int8 key */
   MSA_ERR_ATTR = 7,    /* sparse_mode not 0/3, init/local_blocks out of range, or
                           another attribute (family, local_mode, top-k k) invalid */
-  MSA_ERR_HIP = 8      /* a HIP runtime call or kernel launch failed */
+  MSA_ERR_HIP = 8,     /* a HIP runtime call or kernel launch failed */
+  MSA_ERR_WORKSPACE = 9 /* the workspace is smaller than the call needs */
 } msa_status_t;
 
 /* Key layouts (guide, section 四): packed [T2, Hkv, D]; paged
  * [NP, P, Hkv, D] (BBND) and [NP, Hkv, P, D] (BNBD). */
 typedef enum { MSA_LAYOUT_TND = 0, MSA_LAYOUT_BBND = 1, MSA_LAYOUT_BNBD = 2 } msa_layout_t;
+
+/* For msa_cache_append only: a destination [T, H, D] with one row per new
+ * token and head (rotated or encoded queries), not a cache. */
+#define MSA_LAYOUT_ROWS 3
 
 /* Where local_mask's window of local_blocks blocks ends.  PER_REQUEST: at
  * start_loc[b] for every token of request b (guide, section 二).  PER_QUERY:
@@ -271,6 +276,154 @@ msa_status_t msa_index_score_mxfp4_family(const msa_tensor_t* query, const uint8
  * misaligned one, MSA_ERR_HIP if the launch fails. */
 msa_status_t msa_block_topk(const float* scores, int64_t Hq, int64_t T, int64_t width,
                             int64_t num_valid, int32_t k, int32_t* out, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Around the index branch: the cache append that comes before the block score
+ * and the attention that comes after the selection.
+ *
+ * Shared by the entry points below.  Token t of request b (cu_seqlens_q[b] <=
+ * t < cu_seqlens_q[b+1]), the i-th of its L_q(b) new tokens, stands at
+ * position pos(t) = kv_len[b] - L_q(b) + i: kv_len counts the new tokens.
+ * cu_seqlens_q, kv_len, block_table, max_blocks, batch, block_size (128) and
+ * stream are as for msa_index_score, except that
+ *  - cu_seqlens_q[B] may be less than T: rows of tokens behind the last
+ *    request (a padded batch) are neither read nor written;
+ *  - a table entry outside [0, NP) names no page: nothing is written there,
+ *    and its keys are not visible;
+ *  - max_blocks <= 2^24, batch <= 2^30, T < 2^31, at most 2^16 heads, at most
+ *    2^31 - 1 pages or packed keys, and one 128-token block of one head spans
+ *    less than 2 GiB (MSA_ERR_SHAPE otherwise).
+ * Blocks at or past max_blocks, and packed keys past the tensor's end, are
+ * neither read nor written, whatever kv_len says.  All pointers are
+ * caller-owned, nothing is allocated or kept, calls may overlap as long as
+ * they write different memory, and they may be captured into HIP graphs (two
+ * graphs that may run at once need workspaces of their own).  T = 0 returns
+ * MSA_OK without launching anything.
+ * ------------------------------------------------------------------------ */
+
+/* One tensor of a msa_cache_append call. */
+typedef struct {
+  msa_tensor_t src;   /* [T, H, 128] f16 or bf16: any token and head strides of
+                         whole 16 bytes, the last axis compact */
+  msa_tensor_t dst;   /* where the rows go, see below */
+  void* scale;        /* the scales that an int8 or MXFP4 dst needs, else NULL */
+  int32_t layout;     /* msa_layout_t of a cache, or MSA_LAYOUT_ROWS */
+  int32_t rotate;     /* 1: the rows are rotated first; 0: stored as they are */
+} msa_append_item_t;
+
+#define MSA_APPEND_MAX_ITEMS 8
+
+/*
+ * Append new tokens' rows to caches, rotated by their positions and encoded as
+ * the cache holds them; and rotate or encode the queries in the same launch.
+ *
+ * For every item, token t and head h, y = src[t, h, :], rotated if asked for:
+ * with c = cos[pos, r], s = sin[pos, r] and the r-th pair (a, b) of the first
+ * rotary_dim elements -- elements (r, r + rotary_dim / 2), or (2r, 2r + 1)
+ * with interleaved = 1 --
+ *     a' = a c - b s,   b' = b c + a s;
+ * elements past rotary_dim stay as they are.  Then y is stored
+ *  - in a paged cache (BBND [NP, 128, H, D], BNBD [NP, H, 128, D], strides as
+ *    msa_index_score's key) in page block_table[b, pos / 128], slot pos % 128;
+ *  - in a packed cache (TND [T2, H, D]) at token sum_{b' < b} kv_len[b'] + pos;
+ *  - with MSA_LAYOUT_ROWS in dst[t, h, :] (strides as src; may be src itself).
+ * dst's type says how:
+ *  - src's own type: rounded to nearest even;
+ *  - F8E4M3, F8E5M2: rounded to nearest even, past the largest finite value to
+ *    that value, NaN kept;
+ *  - I8: scale = max |y| / 127 (float32), element = y / scale rounded to
+ *    nearest even.  scale: float32 [NP, H, 128] for both paged layouts,
+ *    [T2, H] packed, [T, H] rows;
+ *  - MXFP4 (last axis 64 bytes): per group of 32 elements E8M0 =
+ *    floor(log2 max |y|) - 2 + 127 (at least 0), elements y / 2^(E8M0 - 127)
+ *    rounded to the nearest E2M1 value, ties to the even code, past 6 to 6.
+ *    scale: uint8, dst's layout with a last axis of 4, compact, 4-byte aligned.
+ * The rotation for the last three is evaluated in float64, so that a value
+ * next to a rounding border falls on its own side; a zero row or group has
+ * scale 0 and zero elements; a row (I8) or group (MXFP4) that holds an
+ * infinity or NaN gets a NaN scale (E8M0 255) and zero elements.
+ *
+ * cos, sin     device float32 [positions, rotary_dim / 2], compact, 16-byte
+ *              aligned; may be NULL if no item is rotated.
+ * rotary_dim   a multiple of 16 in [16, 128] if any item is rotated.
+ * interleaved  0 or 1, how elements pair up.
+ * block_table  may be NULL if no item is a paged cache.
+ *
+ * A token before position 0, or (if any item is rotated) at or past
+ * `positions`, is skipped in every item.  A call must not write one place
+ * twice (two requests' tables naming one page for new tokens): which row
+ * stays is not defined.
+ * Returns MSA_ERR_ATTR for num_items outside [1, MSA_APPEND_MAX_ITEMS] or a
+ * bad rotate, rotary_dim or interleaved, MSA_ERR_SCALE for a scale given with
+ * a type that has none or missing, MSA_ERR_DTYPE, _LAYOUT, _SHAPE, _STRIDE,
+ * _NULL as msa_index_score does. */
+msa_status_t msa_cache_append(const msa_append_item_t* items, int32_t num_items,
+                              const float* cos, const float* sin, int64_t positions,
+                              int32_t rotary_dim, int32_t interleaved,
+                              const int32_t* block_table, int64_t max_blocks,
+                              const int32_t* cu_seqlens_q, const int32_t* kv_len, int32_t batch,
+                              int32_t block_size, void* stream);
+
+/*
+ * Attention of the new tokens: over a paged cache (a chunk of a prompt, one
+ * decode token, speculative tokens, or requests of each kind in one batch), or
+ * over packed keys (whole prompts of different lengths).
+ *
+ *   S[t,h,j] = softmax_scale <query[t,h,:], key[j, h/g, :]>
+ *   out[t,h,:] = sum_j exp(S - m) value[j, h/g, :] / sum_j exp(S - m)
+ *   lse[t,h] = log sum_j exp(S)
+ *
+ * over the visible j: j < kv_len[b] and, with sparse_mode 3, j <= pos(t).  A
+ * row that sees no key gets out 0 and lse -inf.  S, the softmax's maximum and
+ * sum and both products' sums are float32; the weights exp(S - m) are rounded
+ * to the query's type for the second product, and out once at the end.
+ * (A value row is multiplied by weight 0 for rows of its own request in the
+ * same tile that do not see it: infinities and NaN in keys or values past
+ * kv_len never reach out, but one in the value of a visible token may turn
+ * rows of earlier tokens of that request into NaN.)
+ *
+ * query        f16 or bf16 [T, Hq, 128], any token stride >= Hq * 128 of whole
+ *              16 bytes, other axes compact.
+ * key, value   the query's type, layouts as msa_index_score's key, each with a
+ *              page stride of its own; packed ones with any token stride >=
+ *              Hkv * 128 of whole 16 bytes.  Hq a multiple of Hkv.
+ * max_blocks   as for msa_index_score (packed: a bound on ceil(kv_len / 128);
+ *              it only steers how the work is split).
+ * softmax_scale  positive and finite (1 / sqrt(128) in most models).
+ * out          device [T, Hq, 128] of the query's type, compact, 16-byte
+ *              aligned.
+ * lse          device float32 [T, Hq], compact, or NULL.
+ * workspace    device memory of at least msa_attention_workspace(...) bytes,
+ *              16-byte aligned, for this call alone until it has run; may be
+ *              NULL if that is 0 (MSA_ERR_WORKSPACE if it is too small).
+ * The same call gives the same bits every time. */
+msa_status_t msa_attention(const msa_tensor_t* query, const msa_tensor_t* key,
+                           const msa_tensor_t* value, const int32_t* block_table,
+                           int64_t max_blocks, const int32_t* cu_seqlens_q, const int32_t* kv_len,
+                           int32_t batch, int32_t block_size, int32_t layout, int32_t sparse_mode,
+                           float softmax_scale, void* out, float* lse, void* workspace,
+                           int64_t workspace_bytes, void* stream);
+
+/* The same over selected blocks: j is visible to the heads of KV head h only
+ * if also floor(j / 128) is among blocks[t, h, 0:num_blocks] (device int32
+ * [T, Hkv, num_blocks], compact, num_blocks 1..64: msa_block_topk's output for
+ * one index head per KV head).  Entries may stand in any order; one outside the
+ * request's visible blocks (-1 among them) names nothing, and a block named
+ * twice counts once. */
+msa_status_t msa_block_attention(const msa_tensor_t* query, const msa_tensor_t* key,
+                                 const msa_tensor_t* value, const int32_t* blocks,
+                                 int32_t num_blocks, const int32_t* block_table,
+                                 int64_t max_blocks, const int32_t* cu_seqlens_q,
+                                 const int32_t* kv_len, int32_t batch, int32_t block_size,
+                                 int32_t layout, int32_t sparse_mode, float softmax_scale,
+                                 void* out, float* lse, void* workspace, int64_t workspace_bytes,
+                                 void* stream);
+
+/* Bytes of workspace that msa_attention (num_blocks = 0) or
+ * msa_block_attention needs for a call of these sizes; 0 if it needs none.
+ * Host-only. */
+int64_t msa_attention_workspace(int64_t T, int32_t batch, int32_t Hq, int32_t Hkv,
+                                int64_t max_blocks, int32_t num_blocks);
 
 /* Output width RoundUp(max(max_blocks, 1), 16) (guide, section 五: the last
  * axis is aligned to 16, and an all-empty packed batch clamps MB to 1). */
