@@ -32,18 +32,18 @@ struct Plan {
 Plan plan_for(int64_t T, int64_t B, int64_t Hq, int64_t Hkv, int64_t MB, int64_t nsel) {
   Plan p{};
   const int64_t g = Hq / Hkv;
-  const bool few = nsel > 0 || T * std::min<int64_t>(g, 16) <= 16 * B;
-  p.rows = few ? msa::kAttnRows : 128;
-  if (!few) {
+  const bool few = nsel > 0 ? T < 64 * B || T * Hkv < 2048 : T * std::min<int64_t>(g, 16) <= 16 * B;
+  p.rows = few ? msa::kAttnRows : nsel > 0 ? 256 : 128;
+  if (!few && nsel == 0) {
     const int64_t big = (T * std::min<int64_t>(g, 256) + 255) / 256 * Hkv;
     if (T * std::min<int64_t>(g, 256) >= 192 * B && big >= 128) p.rows = 256;
   }
   p.hpt = (int)std::min<int64_t>(g, p.rows);
-  p.tpt = nsel > 0 ? 1 : p.rows / p.hpt;
+  p.tpt = few && nsel > 0 ? 1 : p.rows / p.hpt;
   p.hchunks = (int)((g + p.hpt - 1) / p.hpt);
   p.ntiles = std::min<int64_t>(T, (T + B * (p.tpt - 1)) / p.tpt);
   const int64_t items = std::max<int64_t>(p.ntiles * Hkv * p.hchunks, 1);
-  const int64_t blocks = std::max<int64_t>(nsel > 0 ? std::min(nsel, MB) : MB, 1);
+  const int64_t blocks = std::max<int64_t>(few && nsel > 0 ? std::min(nsel, MB) : MB, 1);
   p.min_blocks = few ? 2 : 4;
   const int64_t want = few ? 2048 : 1024, enough = few ? 1024 : 256;
   int64_t n = items >= enough ? 1 : (want + items - 1) / items;
@@ -63,10 +63,12 @@ hipError_t launch(const AttnParams& p, const Plan& plan, int64_t grid, hipStream
   if (plan.rows == msa::kAttnRows)
     e = p.blocks ? msa::launch_kernel(msa::attn_rows_kernel<KK, true>, gr, dim3(256), s, p)
                  : msa::launch_kernel(msa::attn_rows_kernel<KK, false>, gr, dim3(256), s, p);
+  else if (p.blocks)
+    e = msa::launch_kernel(msa::attn_tile_kernel<KK, 8, true>, gr, dim3(512), s, p);
   else if (plan.rows == 256)
-    e = msa::launch_kernel(msa::attn_tile_kernel<KK, 8>, gr, dim3(512), s, p);
+    e = msa::launch_kernel(msa::attn_tile_kernel<KK, 8, false>, gr, dim3(512), s, p);
   else
-    e = msa::launch_kernel(msa::attn_tile_kernel<KK, 4>, gr, dim3(256), s, p);
+    e = msa::launch_kernel(msa::attn_tile_kernel<KK, 4, false>, gr, dim3(256), s, p);
   if (e == hipSuccess && p.nsplit > 1)
     e = msa::launch_kernel(msa::attn_join_kernel<KK>, dim3((unsigned)((p.T * p.Hq + 3) / 4)),
                            dim3(256), s, p);

@@ -19,6 +19,8 @@
 // takes; m, l and both accumulators are float32.
 #pragma once
 
+#include <type_traits>
+
 #include "msa_device.hpp"
 
 namespace msa {
@@ -160,8 +162,28 @@ __device__ __forceinline__ void landed(i32x4& x) { asm volatile("" : "+v"(x)); }
 // The running maximum may lag the true one by this much (in powers of two)
 // before the accumulators are rescaled: weights then reach 2^8, exact in
 // range for both 16-bit types and float32 sums, and almost every stage after
-// the first skips the rescaling.
+// the first skips the rescaling.  (A row's own scores alone decide when its
+// maximum moves, so its bits do not depend on the rows it shares a tile with.)
 constexpr float kMaxLag = 8.f;
+
+// NI copies each of a stage's K and V rows: a wave's lanes' pieces at the byte
+// offsets kof and vof of two raw buffers, 1 KB a copy, the V rows `vat` bytes
+// behind the K rows.
+template <int NI>
+__device__ __forceinline__ void copy_stage(uint8_t* dst, int vat, const uint8_t* k,
+                                           const uint8_t* v, int kbytes, int vbytes,
+                                           const uint32_t* kof, const uint32_t* vof) {
+  const __amdgpu_buffer_rsrc_t kr =
+      __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(k), 0, kbytes, kBufferWord3);
+  const __amdgpu_buffer_rsrc_t vr =
+      __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(v), 0, vbytes, kBufferWord3);
+#pragma unroll
+  for (int i = 0; i < NI; ++i) buffer_copy16_lds(kr, dst + 1024 * i, kof[i]);
+#pragma unroll
+  for (int i = 0; i < NI; ++i) buffer_copy16_lds(vr, dst + vat + 1024 * i, vof[i]);
+}
+constexpr int kSelBits = 131072;       // (token, block) marks of a workgroup
+constexpr int kSelSpan = 4096;         // blocks marked at a time, at most
 
 // ---------------------------------------------------------------------------
 // Few rows: 16 rows a tile, the keys split over waves and workgroups.
@@ -280,51 +302,44 @@ __global__ __launch_bounds__(256, 1) void attn_rows_kernel(AttnParams p) {
     }
     return x;
   };
-  auto copy = [&](uint8_t* dst, const Block& x) {
+  struct Rows { const uint8_t *k, *v; int n; };
+  auto rows_of = [&](const Block& x) -> Rows {
     const int j0 = x.beta * kP + 32 * wave;
     const bool there = !p.paged || x.page >= 0;
-    const int nvalid = __builtin_amdgcn_readfirstlane(there ? max(0, min(32, w.L - j0)) : 0);
-    const int64_t kb = p.paged ? (int64_t)max(x.page, 0) * p.k_page_stride +
-                                     (int64_t)(32 * wave) * p.k_row_stride
+    const int64_t pg = max(x.page, 0);
+    const int64_t kb = p.paged ? pg * p.k_page_stride + (int64_t)(32 * wave) * p.k_row_stride
                                : (w.koff + j0) * p.k_row_stride;
-    const int64_t vb = p.paged ? (int64_t)max(x.page, 0) * p.v_page_stride +
-                                     (int64_t)(32 * wave) * p.v_row_stride
+    const int64_t vb = p.paged ? pg * p.v_page_stride + (int64_t)(32 * wave) * p.v_row_stride
                                : (w.koff + j0) * p.v_row_stride;
-    const __amdgpu_buffer_rsrc_t kr = __builtin_amdgcn_make_buffer_rsrc(
-        const_cast<uint8_t*>(p.k + uniform64(kb + (int64_t)hk * p.k_head_stride)), 0,
-        nvalid * p.k_row_stride, kBufferWord3);
-    const __amdgpu_buffer_rsrc_t vr = __builtin_amdgcn_make_buffer_rsrc(
-        const_cast<uint8_t*>(p.v + uniform64(vb + (int64_t)hk * p.v_head_stride)), 0,
-        nvalid * p.v_row_stride, kBufferWord3);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int r = 4 * i + cr;
-      buffer_copy16_lds(kr, dst + 1024 * i, (uint32_t)(r * p.k_row_stride + 16 * (cc ^ (r & 15))));
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int r = 4 * i + cr;
-      buffer_copy16_lds(vr, dst + 8192 + 1024 * i,
-                        (uint32_t)(r * p.v_row_stride + 16 * (cc ^ ((r & 7) << 1))));
-    }
+    return Rows{p.k + uniform64(kb + (int64_t)hk * p.k_head_stride),
+                p.v + uniform64(vb + (int64_t)hk * p.v_head_stride),
+                __builtin_amdgcn_readfirstlane(there ? max(0, min(32, lim_hi + 1 - j0)) : 0)};
   };
+  uint32_t kof[8], vof[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int r = 4 * i + cr;
+    kof[i] = (uint32_t)(r * p.k_row_stride + 16 * (cc ^ (r & 15)));
+    vof[i] = (uint32_t)(r * p.v_row_stride + 16 * (cc ^ ((r & 7) << 1)));
+  }
 
   f32x4 o[8];
-#pragma unroll
-  for (int d = 0; d < 8; ++d) o[d] = f32x4{0.f, 0.f, 0.f, 0.f};
-  float m = -__builtin_inff(), lsum = 0.f;
+  float m, lsum;
 
-  // One block: its next one's copies into `dst`, then its own keys and values
-  // at kt.  (The two never overlap -- they are the ring's two halves -- and
-  // the parameters say so: reads of LDS that may alias a copy in flight would
-  // wait for all copies.)
+  // One block's keys and values at kt; with CAREFUL as in attn_tile_kernel.
+  // (kt is one half of the ring while copies into the other are in flight, and
+  // the parameters say that the two do not overlap: reads of LDS that may
+  // alias a copy in flight would wait for all copies.)
   auto step = [&](const uint8_t* __restrict kt, uint8_t* __restrict dst, const Block& cur,
-                  const Block& next, bool more) __attribute__((always_inline)) {
-    if (more) {
-      copy(dst, next);
-      asm volatile("s_waitcnt vmcnt(16)" ::: "memory");
-    } else {
-      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+                  const Rows& next, bool more, auto careful) __attribute__((always_inline)) {
+    if constexpr (!decltype(careful)::value) {
+      if (more) {
+        copy_stage<8>(dst, 8192, next.k, next.v, next.n * p.k_row_stride,
+                      next.n * p.v_row_stride, kof, vof);
+        asm volatile("s_waitcnt vmcnt(16)" ::: "memory");
+      } else {
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+      }
     }
     const uint8_t* vt = kt + 8192;
     const int j0 = cur.beta * kP + 32 * wave;
@@ -350,7 +365,7 @@ __global__ __launch_bounds__(256, 1) void attn_rows_kernel(AttnParams p) {
                      fmaxf(fmaxf(sb[0], sb[1]), fmaxf(sb[2], sb[3])));
     mx = max_xor32(max_xor16(mx)) * p.c;
     if (__ballot(mx > m + kMaxLag)) {
-      const float mn = fmaxf(m, mx);
+      const float mn = mx > m + kMaxLag ? mx : m;
       const float alpha = exp2_hw(m - (mn == -__builtin_inff() ? 0.f : mn));
       m = mn;
       lsum *= alpha;
@@ -367,33 +382,87 @@ __global__ __launch_bounds__(256, 1) void attn_rows_kernel(AttnParams p) {
     lsum += ((pa[0] + pa[1]) + (pa[2] + pa[3])) + ((pb[0] + pb[1]) + (pb[2] + pb[3]));
     const i32x4 pf = {pack2<KK>(pa[0], pa[1]), pack2<KK>(pa[2], pa[3]), pack2<KK>(pb[0], pb[1]),
                       pack2<KK>(pb[2], pb[3])};
-#pragma unroll
-    for (int d = 0; d < 8; ++d) {
+    auto value = [&](int d) -> i32x4 {
       const int r = 4 * G + (n >> 2);
       const int ch = ((2 * d + ((n >> 1) & 1)) ^ ((r & 7) << 1)) * 16 + (n & 1) * 8;
       const i32x2 v0 = lds_read_tr(vt + r * 256 + ch);
       const i32x2 v1 = lds_read_tr(vt + (r + 16) * 256 + ch);
-      o[d] = mfma16x16x32<KK>(i32x4{v0[0], v0[1], v1[0], v1[1]}, pf, o[d]);
+      return i32x4{v0[0], v0[1], v1[0], v1[1]};
+    };
+    if constexpr (!decltype(careful)::value) {
+#pragma unroll
+      for (int d = 0; d < 8; ++d) o[d] = mfma16x16x32<KK>(value(d), pf, o[d]);
+    } else {
+      for (int tk = 0; tk < w.ntok; ++tk) {
+        const int end = attn_last(p, w, len, w.i0 + tk);
+#pragma unroll
+        for (int d = 0; d < 8; ++d) {
+          i32x4 v = value(d);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int j = j0 + 16 * (e >> 1) + 4 * G + 2 * (e & 1);
+            v[e] = j + 1 <= end ? v[e] : j <= end ? v[e] & 0xFFFF : 0;
+          }
+          const f32x4 x = mfma16x16x32<KK>(v, pf, o[d]);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) o[d][r] = ti == tk ? x[r] : o[d][r];
+        }
+      }
     }
   };
 
 #pragma unroll
   for (int s = 0; s < 4; ++s) landed(qv[s]);
-  Block cur{0, -1};
-  if (nst > 0) {
-    cur = block_at(0);
-    copy(mine, cur);
-  }
-  for (int s = 0; s < nst; ++s) {
-    Block next = cur;
-    if (s + 1 < nst) {
-      if (!SEL && s + 1 - pbase >= 64) load_pages(s + 1);
-      next = block_at(s + 1);
+  auto pass = [&](auto careful) __attribute__((always_inline)) {
+#pragma unroll
+    for (int d = 0; d < 8; ++d) o[d] = f32x4{0.f, 0.f, 0.f, 0.f};
+    m = -__builtin_inff();
+    lsum = 0.f;
+    if (nst <= 0) return;
+    if (!SEL && pbase > 0) load_pages(0);
+    Block cur = block_at(0);
+    Rows r = rows_of(cur);
+    if constexpr (!decltype(careful)::value)
+      copy_stage<8>(mine, 8192, r.k, r.v, r.n * p.k_row_stride, r.n * p.v_row_stride, kof, vof);
+    for (int s = 0; s < nst; ++s) {
+      Block next = cur;
+      if constexpr (decltype(careful)::value) {
+        if (!SEL && s - pbase >= 64) load_pages(s);
+        cur = block_at(s);
+        r = rows_of(cur);
+        wave_lds_sync();
+        for (int i = 0; i < 8; ++i) {
+          const bool ok = 4 * i + cr < r.n;
+          const i32x4 zero = {0, 0, 0, 0};
+          *reinterpret_cast<i32x4*>(mine + 1024 * i + 16 * l) = ok ? ld16(r.k + kof[i]) : zero;
+          *reinterpret_cast<i32x4*>(mine + 8192 + 1024 * i + 16 * l) =
+              ok ? ld16(r.v + vof[i]) : zero;
+        }
+        wave_lds_sync();
+        step(mine, mine + kRowStage, cur, r, false, careful);
+      } else {
+        if (s + 1 < nst) {
+          if (!SEL && s + 1 - pbase >= 64) load_pages(s + 1);
+          next = block_at(s + 1);
+          r = rows_of(next);
+        }
+        // (the reads of the half that is written next are done)
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        step(mine + (s & 1) * kRowStage, mine + ((s + 1) & 1) * kRowStage, cur, r, s + 1 < nst,
+             careful);
+        cur = next;
+      }
     }
-    // (the reads of the half that is written next are done)
-    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-    step(mine + (s & 1) * kRowStage, mine + ((s + 1) & 1) * kRowStage, cur, next, s + 1 < nst);
-    cur = next;
+  };
+
+  pass(std::false_type{});
+  if (w.ntok > 1) {
+    float odd = 0.f;
+#pragma unroll
+    for (int d = 0; d < 8; ++d)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) odd += o[d][r] - o[d][r];
+    if (__ballot(row_ok && odd != 0.f)) pass(std::true_type{});
   }
 
   // join the four waves: each writes its accumulators, m and l, then wave w
@@ -492,17 +561,41 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnParams p) {
 // stages of 64 keys from the LDS.
 //
 // The stages' K and V rows are copied straight into a two-deep LDS ring one
-// stage ahead, through raw buffers that end at the request's last key, so
+// stage ahead, through raw buffers that end at the tile's last visible key, so
 // rows past it read zeros (a stored NaN there cannot reach a sum).
+//
+// With selected blocks (SEL) the tile's tokens have lists of their own.  The
+// workgroup walks the union of its tokens' blocks in ascending order: a block
+// is copied once for all of them, a wave none of whose tokens selected it
+// skips its products, and a row of another token gets weight 0.  The bound of
+// one workgroup per token is the copying (64 KB per token, KV head and
+// selected block out of the L2); neighbouring tokens share most of their
+// blocks, and even unrelated lists share them once the tile's tokens name
+// more blocks than there are.
+//
+// A weight of 0 does not hide an infinity or NaN in the value of a key that
+// only other rows of the tile see.  So a tile that ends with an accumulator
+// that is not finite is taken again with the second product formed token by
+// token, from values with the unseen rows cleared (CAREFUL); a tile of finite
+// inputs costs only the look at its accumulators.
 // ---------------------------------------------------------------------------
 
 constexpr int kTileKeys = 64;
 
-template <int KK, int NW>
-__global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 2) void attn_tile_kernel(AttnParams p) {
+template <int KK, int NW, bool SEL>
+__global__ __launch_bounds__(64 * NW, 2) void attn_tile_kernel(AttnParams p) {
   constexpr int SB = kTileKeys * 256;          // bytes of a stage's K (or V) rows
   constexpr int NI = SB / 1024 / NW;           // copies of each per wave and stage
-  __shared__ __attribute__((aligned(16))) uint8_t ring[2][2 * SB];
+  // One LDS object, cut up by hand: with several, the compiler attaches alias
+  // scopes to the copies into the ring and then waits for them before every
+  // read of it.
+  constexpr int kMarksAt = 4 * SB, kNamedAt = kMarksAt + (SEL ? kSelBits / 8 : 0);
+  constexpr int kFlagAt = kNamedAt + (SEL ? 2 * kSelSpan : 0);
+  __shared__ __attribute__((aligned(16))) uint8_t lds[kFlagAt + 16];
+  uint8_t* const ring = lds;                                        // [2][K rows, V rows]
+  uint32_t* const marks = reinterpret_cast<uint32_t*>(lds + kMarksAt);   // [token][block of the span]
+  uint16_t* const named = reinterpret_cast<uint16_t*>(lds + kNamedAt);   // the span's blocks, ascending
+  int* const flag = reinterpret_cast<int*>(lds + kFlagAt);
   // heavy tiles (the last tokens of a request see the most keys) first; the
   // KV head changes fastest, so that with 8 XCDs taking workgroups in turn an
   // XCD's L2 holds the keys of few heads
@@ -515,7 +608,8 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 2) void attn_tile_kernel(Att
   const AttnTile w = attn_tile(p, p.ntiles - 1 - rest / p.Hkv);
   if (!w.valid) return;
 
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int tid = threadIdx.x;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int l = lane_id();
   const int n = l & 31, h = l >> 5;
   const int len = p.kv_len[w.b];
@@ -530,8 +624,6 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 2) void attn_tile_kernel(Att
   const int parts = max(1, min(p.nsplit, (total + p.min_blocks - 1) / p.min_blocks));
   const int b0 = (int)((int64_t)total * split / parts);
   const int b1 = split < parts ? (int)((int64_t)total * (split + 1) / parts) : b0;
-  const int s0 = 2 * b0;                                   // stages [s0, s1)
-  const int s1 = b1 > b0 ? min(2 * b1, lim_hi / kTileKeys + 1) : s0;
 
   i32x4 qv[8];
 #pragma unroll
@@ -542,17 +634,31 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 2) void attn_tile_kernel(Att
     for (int s = 0; s < 8; ++s) qv[s] = ld16(qr + 16 * (2 * s + h));
   }
 
-  int pidx = -1, pbase = b0;
-  auto load_pages = [&](int from) {
+  // The blocks come as a list of `count` entries: the part's own ones in
+  // order, or a span's marked ones.  Their numbers and pages are held one per
+  // lane, 64 entries at a time (page -1: none).
+  int base = b0, count = b1 - b0;
+  const int span = SEL ? min(kSelSpan, kSelBits / p.tpt & ~31) : 0;
+  int bidx = 0, pidx = -1, pbase = 0;
+  auto load_entries = [&](int from) {
     pbase = from;
     pidx = -1;
-    if (p.paged && from + l < b1) {
-      const int pg = p.block_table[(int64_t)w.b * p.MB + from + l];
-      pidx = pg >= 0 && pg < p.NP ? pg : -1;
+    bidx = base + from + l;
+    if (from + l < count) {
+      if constexpr (SEL) bidx = base + named[from + l];
+      if (p.paged) {
+        const int pg = p.block_table[(int64_t)w.b * p.MB + bidx];
+        pidx = pg >= 0 && pg < p.NP ? pg : -1;
+      }
     }
+    bidx = consumed(bidx);
     pidx = consumed(pidx);
   };
-  load_pages(b0);
+  struct Entry { int beta, page; };
+  auto entry_at = [&](int e) -> Entry {
+    if (e - pbase >= 64) load_entries(e);
+    return Entry{lane_at(bidx, e - pbase), lane_at(pidx, e - pbase)};
+  };
 
   const int cr = l >> 4, cc = l & 15;
   uint32_t kof[NI], vof[NI];
@@ -562,46 +668,49 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 2) void attn_tile_kernel(Att
     kof[i] = (uint32_t)(r * p.k_row_stride + 16 * (cc ^ (r & 15)));
     vof[i] = (uint32_t)(r * p.v_row_stride + 16 * (cc ^ ((r & 3) << 2)));
   }
-  auto copy = [&](uint8_t* dst, int s, int page) {
-    const int j0 = s * kTileKeys;
-    const bool there = !p.paged || page >= 0;
-    const int nvalid = __builtin_amdgcn_readfirstlane(there ? max(0, min(kTileKeys, w.L - j0)) : 0);
-    const int in = (s & 1) * kTileKeys;          // first row within the block
-    const int64_t kb = p.paged ? (int64_t)max(page, 0) * p.k_page_stride + (int64_t)in * p.k_row_stride
+  // Where the keys of half `in` of a block lie, and how many of them there are
+  // to the tile's last visible one.
+  struct Rows { const uint8_t *k, *v; int n; };
+  auto rows_of = [&](const Entry& x, int in) -> Rows {
+    const int j0 = x.beta * kP + in * kTileKeys;
+    const bool there = !p.paged || x.page >= 0;
+    const int64_t pg = max(x.page, 0);
+    const int64_t kb = p.paged ? pg * p.k_page_stride + (int64_t)(in * kTileKeys) * p.k_row_stride
                                : (w.koff + j0) * p.k_row_stride;
-    const int64_t vb = p.paged ? (int64_t)max(page, 0) * p.v_page_stride + (int64_t)in * p.v_row_stride
+    const int64_t vb = p.paged ? pg * p.v_page_stride + (int64_t)(in * kTileKeys) * p.v_row_stride
                                : (w.koff + j0) * p.v_row_stride;
-    const __amdgpu_buffer_rsrc_t kr = __builtin_amdgcn_make_buffer_rsrc(
-        const_cast<uint8_t*>(p.k + uniform64(kb + (int64_t)hk * p.k_head_stride)), 0,
-        nvalid * p.k_row_stride, kBufferWord3);
-    const __amdgpu_buffer_rsrc_t vr = __builtin_amdgcn_make_buffer_rsrc(
-        const_cast<uint8_t*>(p.v + uniform64(vb + (int64_t)hk * p.v_head_stride)), 0,
-        nvalid * p.v_row_stride, kBufferWord3);
-#pragma unroll
-    for (int i = 0; i < NI; ++i)
-      buffer_copy16_lds(kr, dst + (wave * NI + i) * 1024, kof[i]);
-#pragma unroll
-    for (int i = 0; i < NI; ++i)
-      buffer_copy16_lds(vr, dst + SB + (wave * NI + i) * 1024, vof[i]);
+    return Rows{p.k + uniform64(kb + (int64_t)hk * p.k_head_stride),
+                p.v + uniform64(vb + (int64_t)hk * p.v_head_stride),
+                __builtin_amdgcn_readfirstlane(there ? max(0, min(kTileKeys, lim_hi + 1 - j0)) : 0)};
   };
-  auto page_at = [&](int s) -> int {
-    if ((s >> 1) - pbase >= 64) load_pages(s >> 1);
-    return lane_at(pidx, (s >> 1) - pbase);
+  // a stage's rows through registers, for the careful pass (whose copies need
+  // not overlap anything)
+  auto copy_plain = [&](uint8_t* dst, const Entry& x, int in) {
+    const Rows r = rows_of(x, in);
+    for (int i = 0; i < NI; ++i) {
+      const bool ok = (wave * NI + i) * 4 + cr < r.n;
+      const int at = (wave * NI + i) * 1024 + 16 * l;
+      const i32x4 zero = {0, 0, 0, 0};
+      *reinterpret_cast<i32x4*>(dst + at) = ok ? ld16(r.k + kof[i]) : zero;
+      *reinterpret_cast<i32x4*>(dst + SB + at) = ok ? ld16(r.v + vof[i]) : zero;
+    }
   };
 
   f32x16 o[4];
-#pragma unroll
-  for (int d = 0; d < 4; ++d) o[d] = f32x16{};
-  float m = -__builtin_inff(), lsum = 0.f;
+  float m, lsum;
 
-  // One stage: the next one's copies into `dst`, then its own rows at kt (as in
-  // attn_rows_kernel, the parameters say that the two do not overlap).
-  auto stage = [&](const uint8_t* __restrict kt, uint8_t* __restrict dst, int s, int cur,
-                   int page, bool more) __attribute__((always_inline)) {
-    if (more) copy(dst, s + 1, page);
+  // One stage: the copies of the next one's rows into `dst`, then its own at kt
+  // (as in attn_rows_kernel, the parameters say that the two do not overlap).
+  // `mine`: this lane's row's token selected the block.
+  auto stage = [&](const uint8_t* __restrict kt, uint8_t* __restrict dst, const Entry& cur, int in,
+                   const Rows& next, bool mine, auto careful) __attribute__((always_inline)) {
+    if constexpr (!decltype(careful)::value)
+      copy_stage<NI>(dst + wave * NI * 1024, SB, next.k, next.v, next.n * p.k_row_stride,
+                     next.n * p.v_row_stride, kof, vof);
+    if (SEL && !__ballot(mine && row_ok)) return;
     const uint8_t* vt = kt + SB;
-    const int j0 = s * kTileKeys;
-    const bool there = !p.paged || cur >= 0;
+    const int j0 = cur.beta * kP + in * kTileKeys;
+    const bool there = !p.paged || cur.page >= 0;
 
     // S^T, two tiles of 32 keys: register r of tile t is key
     // j0 + 32 t + 8 (r / 4) + 4 h + r % 4 of row n
@@ -630,8 +739,9 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 2) void attn_tile_kernel(Att
 #pragma unroll
       for (int r = 0; r < 16; ++r) mx = fmaxf(mx, st[t][r]);
     mx = max_xor32(mx) * p.c;
+    if constexpr (SEL) mx = mine ? mx : -__builtin_inff();
     if (__ballot(mx > m + kMaxLag)) {
-      const float mn = fmaxf(m, mx);
+      const float mn = mx > m + kMaxLag ? mx : m;
       const float alpha = exp2_hw(m - (mn == -__builtin_inff() ? 0.f : mn));
       m = mn;
       lsum *= alpha;
@@ -639,50 +749,166 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 2) void attn_tile_kernel(Att
       for (int d = 0; d < 4; ++d) o[d] *= alpha;
     }
     const float ms = m == -__builtin_inff() ? 0.f : m;
+    float add = 0.f;
 #pragma unroll
     for (int t = 0; t < 2; ++t)
 #pragma unroll
       for (int r = 0; r < 16; ++r) {
         st[t][r] = exp2_hw(__builtin_fmaf(st[t][r], p.c, -ms));
-        lsum += st[t][r];
+        add += st[t][r];
+      }
+    lsum += !SEL || mine ? add : 0.f;
+    i32x4 pf[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int pk = pack2<KK>(st[u >> 1][8 * (u & 1) + 2 * e], st[u >> 1][8 * (u & 1) + 2 * e + 1]);
+        pf[u][e] = !SEL || mine ? pk : 0;
       }
     // O^T += V^T P^T, 16 keys a step: registers 8 u .. 8 u + 7 of a tile are
     // keys 16 u + 4 h + {0..3} and 16 u + 8 + 4 h + {0..3}
+    const int vi = l & 15;
+    auto value = [&](int u, int d) -> i32x4 {
+      const int r = 16 * u + 4 * h + (vi >> 2);
+      const int ch = ((4 * d + 2 * ((l >> 4) & 1) + ((vi >> 1) & 1)) ^ ((r & 3) << 2)) * 16 +
+                     (vi & 1) * 8;
+      const i32x2 v0 = lds_read_tr(vt + r * 256 + ch);
+      const i32x2 v1 = lds_read_tr(vt + (r + 8) * 256 + ch);
+      return i32x4{v0[0], v0[1], v1[0], v1[1]};
+    };
+    if constexpr (!decltype(careful)::value) {
 #pragma unroll
-    for (int t = 0; t < 2; ++t)
+      for (int u = 0; u < 4; ++u)
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        i32x4 pf;
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          pf[e] = pack2<KK>(st[t][8 * u + 2 * e], st[t][8 * u + 2 * e + 1]);
-        const int i = l & 15;
-        const int r = 32 * t + 16 * u + 4 * h + (i >> 2);
+        for (int d = 0; d < 4; ++d) o[d] = mfma32x32x16<KK>(value(u, d), pf[u], o[d]);
+    } else {
+      // token by token: the values of keys that it does not see cleared, its
+      // rows' sums kept
+      const int first = wave * 32 / p.hpt, last = min((wave * 32 + 31) / p.hpt, w.ntok - 1);
+      for (int tk = first; tk <= last; ++tk) {
+        const unsigned long long its = __ballot(row_ok && ti == tk && mine);
+        if (!its) continue;
+        const int end = attn_last(p, w, len, w.i0 + tk);
 #pragma unroll
         for (int d = 0; d < 4; ++d) {
-          const int ch = ((4 * d + 2 * ((l >> 4) & 1) + ((i >> 1) & 1)) ^ ((r & 3) << 2)) * 16 +
-                         (i & 1) * 8;
-          const i32x2 v0 = lds_read_tr(vt + r * 256 + ch);
-          const i32x2 v1 = lds_read_tr(vt + (r + 8) * 256 + ch);
-          o[d] = mfma32x32x16<KK>(i32x4{v0[0], v0[1], v1[0], v1[1]}, pf, o[d]);
+          f32x16 x = o[d];
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            i32x4 v = value(u, d);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int j = j0 + 16 * u + 8 * (e >> 1) + 4 * h + 2 * (e & 1);
+              v[e] = j + 1 <= end ? v[e] : j <= end ? v[e] & 0xFFFF : 0;
+            }
+            x = mfma32x32x16<KK>(v, pf[u], x);
+          }
+#pragma unroll
+          for (int r = 0; r < 16; ++r) o[d][r] = ti == tk ? x[r] : o[d][r];
         }
       }
+    }
+  };
+
+  // the list's stages, two per block
+  auto walk = [&](auto careful) __attribute__((always_inline)) {
+    if (count <= 0) return;
+    load_entries(0);
+    Entry x = entry_at(0);
+    const int stages = 2 * count;
+    auto selected = [&](const Entry& e) -> bool {
+      if constexpr (!SEL) return true;
+      const int at = e.beta - base;
+      return row_ok && (marks[ti * (span >> 5) + (at >> 5)] >> (at & 31)) & 1;
+    };
+    if constexpr (decltype(careful)::value) {
+      for (int s = 0; s < stages; ++s) {
+        x = entry_at(s >> 1);
+        __syncthreads();
+        copy_plain(ring, x, s & 1);
+        __syncthreads();
+        stage(ring, ring + 2 * SB, x, s & 1, Rows{}, selected(x), careful);
+      }
+    } else {
+      Rows r = rows_of(x, 0);
+      copy_stage<NI>(ring + wave * NI * 1024, SB, r.k, r.v, r.n * p.k_row_stride,
+                     r.n * p.v_row_stride, kof, vof);
+      for (int s = 0; s < stages; ++s) {
+        const Entry cur = x;
+        if (s + 1 < stages) {
+          if (s & 1) x = entry_at((s + 1) >> 1);
+          r = rows_of(x, (s + 1) & 1);
+        } else {
+          r.n = 0;       // (nothing is read: the last copies bring zeros)
+        }
+        const bool mine = selected(cur);
+        // this wave's copies of stage s have landed; after the barrier
+        // everyone's have, and everyone has read stage s - 1
+        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        stage(ring + (s & 1) * 2 * SB, ring + (~s & 1) * 2 * SB, cur, s & 1, r, mine, careful);
+      }
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    }
+  };
+
+  auto pass = [&](auto careful) __attribute__((always_inline)) {
+#pragma unroll
+    for (int d = 0; d < 4; ++d) o[d] = f32x16{};
+    m = -__builtin_inff();
+    lsum = 0.f;
+    if constexpr (!SEL) {
+      walk(careful);
+    } else {
+      const int words = span >> 5;
+      for (base = b0; base < b1; base += span) {
+        const int end = min(base + span, b1);
+        __syncthreads();
+        for (int i = tid; i < w.ntok * words; i += 64 * NW) marks[i] = 0;
+        __syncthreads();
+        for (int i = tid; i < w.ntok * p.nsel; i += 64 * NW) {
+          const int tk = i / p.nsel;
+          const int e = p.blocks[((int64_t)(w.t0 + tk) * p.Hkv + hk) * p.nsel + (i - tk * p.nsel)];
+          if (e >= base && e < end && (int64_t)e * kP <= attn_last(p, w, len, w.i0 + tk))
+            atomicOr(&marks[tk * words + ((e - base) >> 5)], 1u << ((e - base) & 31));
+        }
+        __syncthreads();
+        if (wave == 0) {
+          // two words a lane, then the marked blocks' places by a prefix sum
+          int n0 = 0;
+          for (int wd = 0; wd < words; wd += 64) {
+            uint32_t u = 0;
+            if (wd + l < words)
+              for (int tk = 0; tk < w.ntok; ++tk) u |= marks[tk * words + wd + l];
+            const int incl = wave_incl_scan((int)__popc(u));
+            int at = n0 + incl - __popc(u);
+            for (; u; u &= u - 1) named[at++] = (uint16_t)(32 * (wd + l) + __ffs(u) - 1);
+            n0 += lane_at(incl, 63);
+          }
+          if (l == 0) *flag = n0;
+        }
+        __syncthreads();
+        count = __builtin_amdgcn_readfirstlane(*flag);
+        walk(careful);
+      }
+    }
   };
 
 #pragma unroll
   for (int s = 0; s < 8; ++s) landed(qv[s]);
-  int page = -1;
-  if (s0 < s1) {
-    page = page_at(s0);
-    copy(ring[s0 & 1], s0, page);
-  }
-  for (int s = s0; s < s1; ++s) {
-    const int cur = page;
-    if (s + 1 < s1) page = page_at(s + 1);
-    // this wave's copies of stage s have landed; after the barrier everyone's
-    // have, and everyone has read stage s - 1
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-    stage(ring[s & 1], ring[(s + 1) & 1], s, cur, page, s + 1 < s1);
+  pass(std::false_type{});
+  if (w.ntok > 1) {
+    // (x - x is 0 for a finite x only; the products add no rounding of their own)
+    float odd = 0.f;
+#pragma unroll
+    for (int d = 0; d < 4; ++d)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) odd += o[d][r] - o[d][r];
+    __syncthreads();
+    if (tid == 0) *flag = 0;
+    __syncthreads();
+    if (row_ok && odd != 0.f) *flag = 1;
+    __syncthreads();
+    if (*flag) pass(std::true_type{});
   }
 
   lsum = sum_xor32(lsum);
@@ -692,7 +918,7 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 2) void attn_tile_kernel(Att
   if (p.nsplit > 1) {
     const int64_t pr = (int64_t)split * p.T * p.Hq + out_row;
     if (h == 0) p.part_ml[pr] = float2{m, lsum};
-    if (s0 < s1) {
+    if (b0 < b1) {
 #pragma unroll
       for (int d = 0; d < 4; ++d)
 #pragma unroll

@@ -377,10 +377,7 @@ msa_status_t msa_cache_append(const msa_append_item_t* items, int32_t num_items,
  * row that sees no key gets out 0 and lse -inf.  S, the softmax's maximum and
  * sum and both products' sums are float32; the weights exp(S - m) are rounded
  * to the query's type for the second product, and out once at the end.
- * (A value row is multiplied by weight 0 for rows of its own request in the
- * same tile that do not see it: infinities and NaN in keys or values past
- * kv_len never reach out, but one in the value of a visible token may turn
- * rows of earlier tokens of that request into NaN.)
+ * Infinities and NaN in keys or values that a row does not see never reach it.
  *
  * query        f16 or bf16 [T, Hq, 128], any token stride >= Hq * 128 of whole
  *              16 bytes, other axes compact.

@@ -216,6 +216,35 @@ def test_nonfinite_keys_behind_the_last(q_lens, kv, bad, dev):
     check(c, out, lse, ref)
 
 
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+@pytest.mark.parametrize("q_lens,kv,Hq,Hkv,k", [
+    ([3], [300], 4, 1, 0), ([5, 1], [40, 9], 6, 3, 0), ([90], [300], 8, 2, 0),
+    ([700], [700], 16, 2, 0), ([2, 33], [300, 700], 300, 1, 0), ([40], [3333], 16, 2, 0),
+    ([70, 90], [1000, 513], 16, 2, 5), ([2100], [2200], 8, 2, 4)])
+def test_nonfinite_values_that_a_row_does_not_see(bad, q_lens, kv, Hq, Hkv, k, dev):
+    """The last token's key and value hold no numbers: rows of earlier tokens
+    (in the same tile) and of tokens that did not select its block are as they
+    would be without."""
+    log("unseen", bad, q_lens, Hq, k)
+    c = lc.attention_case(q_lens, kv, Hq, Hkv, k=k, seed=22)
+    page, slot = int(c["table"][0, (kv[0] - 1) // 128]), (kv[0] - 1) % 128
+    n = q_lens[0]
+    full = dict(c, k=c["k"].clone(), v=c["v"].clone())
+    full["v"][page, slot, :, 3:90] = bad
+    full["k"][page, slot, 0, 5] = bad
+    out, lse = (x.cpu() for x in call(to(full, dev)))
+    torch.cuda.synchronize()
+    clean_out, clean_lse = (x.cpu() for x in call(to(c, dev)))
+    see = torch.zeros(c["q"].shape[0], Hkv, dtype=torch.bool)
+    see[n - 1] = True
+    if k:
+        see &= (c["blocks"] == (kv[0] - 1) // 128).any(-1)
+    rows = see.repeat_interleave(Hq // Hkv, 1)
+    assert torch.equal(out[~rows], clean_out[~rows]) and torch.equal(lse[~rows], clean_lse[~rows])
+    if rows.any():
+        assert not torch.isfinite(out[rows][:, 3:90]).any()
+
+
 def test_large_and_small_scores(dev):
     """Scores far apart (weights that underflow, a maximum that grows along the
     keys) and a scale of its own."""
@@ -234,6 +263,66 @@ def test_selected(dtype, layout, k, Hq, Hkv, dev):
     log("selected", dtype, layout, k, Hq, Hkv)
     run(lc.attention_case([1, 3, 0, 30], [1, 2000, 55, 999], Hq, Hkv, layout, dtype, k=k,
                           seed=k), dev)
+
+
+def check_tokens(c, out, lse, tokens):
+    """Compare some tokens' rows, each as a request of its own (causal mode)."""
+    out, lse = out.cpu(), lse.cpu()
+    where = {t: (b, pos) for t, b, pos in layer.positions(c["cu"], c["kv"], c["q"].shape[0])}
+    for t in tokens:
+        b, pos = where[t]
+        first = int(c["kv"][:b].clamp(min=0).sum())
+        one = dict(c, q=c["q"][t:t + 1], cu=torch.tensor([0, 1], dtype=torch.int32),
+                   kv=torch.tensor([pos + 1], dtype=torch.int32))
+        if c["layout"] == "TND":
+            one["k"], one["v"] = (c[x][first:first + pos + 1] for x in "kv")
+        else:
+            one["table"] = c["table"][b:b + 1]
+        if c["blocks"] is not None:
+            one["blocks"] = c["blocks"][t:t + 1]
+        check(one, out[t:t + 1], lse[t:t + 1])
+
+
+@pytest.mark.parametrize("Hq,Hkv", [(8, 1), (16, 8), (40, 2), (4, 4), (300, 1)])
+@pytest.mark.parametrize("layout", ["BBND", "BNBD", "TND"])
+def test_selected_long_chunks(layout, Hq, Hkv, dev):
+    """Long enough for the tiles that walk the union of their tokens' blocks."""
+    log("selected chunks", layout, Hq, Hkv)
+    q_lens, kv = ([250, 131], [1000, 131]) if Hkv > 2 else ([900, 1170], [2000, 1170])
+    if Hq == 300:
+        q_lens, kv = [2050], [2300]
+    c = lc.attention_case(q_lens, kv, Hq, Hkv, layout, FP if Hq == 16 else BF, k=5, seed=Hq)
+    out, lse = call(to(c, dev))
+    torch.cuda.synchronize()
+    assert torch.isfinite(out).all()
+    T, gen = sum(q_lens), torch.Generator().manual_seed(Hq)
+    some = {0, 1, 5, 6, 7, 31, 32, 255, T - 1, T - 2, q_lens[0] - 1, q_lens[0] % T}
+    some |= set(torch.randint(0, T, (20,), generator=gen).tolist())
+    check_tokens(c, out, lse, sorted(x for x in some if x < T))
+
+
+def test_selected_chunk_any_order_and_wide_spans(dev):
+    """Lists out of order, with repeats and entries that name nothing, over more
+    blocks than a workgroup marks at a time."""
+    gen = torch.Generator().manual_seed(33)
+    T, Hkv, k, nb = 2100, 2, 9, 5000
+    c = lc.attention_case([T], [T + 300], 4, Hkv, k=k, seed=34)
+    c["blocks"] = torch.randint(-3, 25, (T, Hkv, k), generator=gen, dtype=torch.int32)
+    c["blocks"][::7, :, 2] = 2 ** 31 - 1
+    c["blocks"][::5, :, 1] = -2 ** 31
+    out, lse = call(to(c, dev))
+    torch.cuda.synchronize()
+    check_tokens(c, out, lse, range(0, T, 29))
+    # 5000 blocks behind few pages
+    c = lc.attention_case([T], [T], 4, Hkv, k=k, seed=35)
+    last = nb * 128 - 60
+    c["table"] = (torch.arange(nb) % c["k"].shape[0]).int()[None]
+    c["kv"] = torch.tensor([last], dtype=torch.int32)
+    c["blocks"] = torch.randint(0, nb, (T, Hkv, k), generator=gen, dtype=torch.int32)
+    c["blocks"][..., 0] = ((last - T + torch.arange(T)) // 128)[:, None]
+    out, lse = call(to(c, dev))
+    torch.cuda.synchronize()
+    check_tokens(c, out, lse, (0, 63, 1000, T - 1))
 
 
 def test_selected_any_order_and_repeats(dev):
