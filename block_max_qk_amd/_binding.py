@@ -113,7 +113,7 @@ def load_library(path: Optional[str] = None):
         # layout, sparse_mode, softmax_scale, out, lse, workspace,
         # workspace_bytes, stream
         tail = [ptr, i64, ptr, ptr, i32, i32, i32, i32, ctypes.c_float, ptr, ptr, ptr, i64, ptr]
-        three = [ctypes.POINTER(MsaTensor)] * 3
+        three = [ptr] * 3                # descriptors, as packed bytes or byref()
         lib.msa_attention.argtypes = three + tail
         lib.msa_attention.restype = ctypes.c_int
         lib.msa_block_attention.argtypes = three + [ptr, i32] + tail
@@ -443,44 +443,57 @@ class CacheItem(NamedTuple):
     rotate: bool = False
 
 
-# msa_append_item_t: two msa_tensor_t (data, dtype, ndim, shape[4], stride[4]),
-# scale, layout, rotate
-_ITEM = struct.Struct("<Qii4q4qQii4q4qQii")
+# msa_tensor_t packed by hand (data, dtype, ndim, shape[4], stride[4]): a step
+# of small calls is bound by the host, and filling a ctypes structure field by
+# field costs several times as much as packing its bytes
+_PACK = {n: struct.Struct("<Qii%dq%dx%dq%dx" % (n, 32 - 8 * n, n, 32 - 8 * n))
+         for n in range(1, 5)}
+_ITEM_TAIL = struct.Struct("<Qii")       # scale, layout, rotate of msa_append_item_t
 
 
-def _dims(t: torch.Tensor):
-    n = t.dim()
-    if n > 4:
-        raise ValueError(f"a tensor of {n} axes: at most 4 are taken")
-    pad = (0,) * (4 - n)
-    return (t.data_ptr(), DTYPE_CODE.get(t.dtype, -1), n, *t.shape, *pad, *t.stride(), *pad)
+def _packed(t: torch.Tensor) -> bytes:
+    shape = t.shape
+    n = len(shape)
+    if not 1 <= n <= 4:
+        raise ValueError(f"a tensor of {n} axes: 1 to 4 are taken")
+    return _PACK[n].pack(t.data_ptr(), DTYPE_CODE.get(t.dtype, -1), n, *shape, *t.stride())
 
 
-def _on_device(dev, named):
+def _address(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+def _on_device(index, *named):
+    """Every (name, tensor) on the device of this index (-1: the host)."""
     for name, t in named:
-        if t is not None and t.device != dev:
-            raise ValueError(f"{name} is on {t.device}, the call's first tensor on {dev}")
+        if t is not None and t.get_device() != index:
+            raise ValueError(f"{name} is on {t.device}, the call's first tensor on "
+                             f"{'cpu' if index < 0 else 'cuda:%d' % index}")
 
 
 def _check_lengths(cu_seqlens_q, kv_len, block_table, max_blocks, paged) -> int:
     """The request count B, from tensors whose extents the C ABI takes on trust."""
-    for name, t in (("cu_seqlens_q", cu_seqlens_q), ("kv_len", kv_len),
-                    ("block_table", block_table)):
-        if t is not None and (t.dtype != torch.int32 or not t.is_contiguous()):
-            raise ValueError(f"{name} must be a contiguous int32 tensor")
+    i32 = torch.int32
+    if cu_seqlens_q.dtype != i32 or not cu_seqlens_q.is_contiguous():
+        raise ValueError("cu_seqlens_q must be a contiguous int32 tensor")
+    if kv_len.dtype != i32 or not kv_len.is_contiguous():
+        raise ValueError("kv_len must be a contiguous int32 tensor")
     if kv_len.dim() != 1:
         raise ValueError("kv_len must be 1-D [B] (per-request lengths)")
     B = kv_len.shape[0]
     if cu_seqlens_q.dim() != 1 or cu_seqlens_q.shape[0] != B + 1:
         raise ValueError(f"cu_seqlens_q must be [B+1] = [{B + 1}], got "
                          f"{tuple(cu_seqlens_q.shape)}")
-    if paged:
-        if block_table is None:
+    if block_table is None:
+        if paged:
             raise ValueError("paged layouts need a block_table")
-        if (block_table.dim() != 2 or block_table.shape[0] < B or
-                block_table.shape[1] != max_blocks):
-            raise ValueError(f"block_table must be [>= {B}, max_blocks = {max_blocks}], got "
-                             f"{tuple(block_table.shape)}")
+        return B
+    if block_table.dtype != i32 or not block_table.is_contiguous():
+        raise ValueError("block_table must be a contiguous int32 tensor")
+    shape = block_table.shape
+    if paged and (len(shape) != 2 or shape[0] < B or shape[1] != max_blocks):
+        raise ValueError(f"block_table must be [>= {B}, max_blocks = {max_blocks}], got "
+                         f"{tuple(shape)}")
     return B
 
 
@@ -495,11 +508,12 @@ class _On:
     """The device of a call, and its stream's handle (a stream of another
     device than the current one is launched on with its own made current)."""
 
-    def __init__(self, dev, stream):
+    def __init__(self, t, stream):
         self.guard = None
-        if dev.type == "cuda" and torch.cuda.current_device() != dev.index:
-            self.guard = torch.cuda.device(dev)
-        self.handle = _stream_handle(stream, dev)
+        index = t.get_device()
+        if index >= 0 and torch.cuda.current_device() != index:
+            self.guard = torch.cuda.device(index)
+        self.handle = _stream_handle(stream, index if index >= 0 else t.device)
 
     def __enter__(self):
         if self.guard is not None:
@@ -529,49 +543,51 @@ def msa_cache_append(items: Sequence[CacheItem], cos: Optional[torch.Tensor],
     ``cos`` and ``sin`` [positions, rotary_dim / 2] float32 may be None if no
     item is rotated, ``block_table`` [>= B, MB] int32 if no item is paged;
     ``kv_len`` counts the new tokens."""
-    lib = load_library()
+    lib = _lib or load_library()
     if not 1 <= len(items) <= APPEND_MAX_ITEMS:
         raise ValueError(f"1 to {APPEND_MAX_ITEMS} items, got {len(items)}")
-    dev = items[0].src.device
-    _on_device(dev, (("cos", cos), ("sin", sin), ("block_table", block_table),
-                     ("cu_seqlens_q", cu_seqlens_q), ("kv_len", kv_len)))
-    max_blocks = 0 if block_table is None or block_table.dim() != 2 else block_table.shape[1]
-    B = _check_lengths(cu_seqlens_q, kv_len, block_table, max_blocks, block_table is not None)
+    index = items[0].src.get_device()
+    _on_device(index, ("cos", cos), ("sin", sin), ("block_table", block_table),
+               ("cu_seqlens_q", cu_seqlens_q), ("kv_len", kv_len))
+    paged = block_table is not None
+    max_blocks = block_table.shape[-1] if paged else 0
+    B = _check_lengths(cu_seqlens_q, kv_len, block_table, max_blocks, paged)
     positions = rotary = 0
-    if cos is not None or sin is not None:
-        if cos is None or sin is None or cos.shape != sin.shape or cos.dim() != 2:
+    if cos is not None and sin is not None:
+        if cos.shape != sin.shape or cos.dim() != 2:
             raise ValueError("cos and sin must both be [positions, rotary_dim / 2]")
         for name, t in (("cos", cos), ("sin", sin)):
             if t.dtype != torch.float32 or not t.is_contiguous():
                 raise ValueError(f"{name} must be a contiguous float32 tensor")
         positions, rotary = cos.shape[0], 2 * cos.shape[1]
-    elif any(it.rotate for it in items):
-        raise ValueError("rotated items need cos and sin")
-    buf = bytearray(_ITEM.size * len(items))
-    for i, it in enumerate(items):
-        src, dst, scale = it.src, it.dst, it.scale
-        _on_device(dev, (("src", src), ("dst", dst), ("scale", scale)))
-        lay = _item_layout(it.layout)
-        sp = 0
+    elif cos is not None or sin is not None or any(it[4] for it in items):
+        raise ValueError("rotated items need both cos and sin")
+    packed = []
+    for i, (src, dst, layout, scale, rotate) in enumerate(items):
+        lay = _item_layout(layout)
+        if src.get_device() != index or dst.get_device() != index:
+            raise ValueError(f"item {i}: src is on {src.device}, dst on {dst.device}")
+        if lay in (1, 2) and not paged:
+            raise ValueError(f"item {i}: paged layouts need a block_table")
+        at = 0
         if scale is not None:
             i8 = dst.dtype == torch.int8
             want = torch.float32 if i8 else torch.uint8
             n = dst.numel() // (128 if i8 else 16)
-            if scale.dtype != want or not scale.is_contiguous() or scale.numel() != n:
+            if (scale.dtype != want or not scale.is_contiguous() or scale.numel() != n or
+                    scale.get_device() != index):
                 raise ValueError(f"item {i}: scale must be a contiguous {want} tensor of {n} "
-                                 f"elements, got {scale.dtype} {tuple(scale.shape)}")
-            sp = scale.data_ptr()
-        if lay in (1, 2) and block_table is None:
-            raise ValueError(f"item {i}: paged layouts need a block_table")
-        _ITEM.pack_into(buf, i * _ITEM.size, *_dims(src), *_dims(dst), sp, lay,
-                        int(bool(it.rotate)))
-    arr = (ctypes.c_char * len(buf)).from_buffer(buf)
-    with _On(dev, stream) as handle:
-        st = lib.msa_cache_append(ctypes.addressof(arr), len(items), _ptr(cos), _ptr(sin),
-                                  positions, rotary, int(bool(interleaved)), _ptr(block_table),
-                                  max_blocks, _ptr(cu_seqlens_q), _ptr(kv_len), B,
-                                  int(block_size), handle)
-    _raise_status(st)
+                                 f"elements beside dst, got {scale.dtype} "
+                                 f"{tuple(scale.shape)} on {scale.device}")
+            at = scale.data_ptr()
+        packed += (_packed(src), _packed(dst), _ITEM_TAIL.pack(at, lay, 1 if rotate else 0))
+    with _On(items[0].src, stream) as handle:
+        st = lib.msa_cache_append(b"".join(packed), len(items), _address(cos), _address(sin),
+                                  positions, rotary, 1 if interleaved else 0,
+                                  _address(block_table), max_blocks, cu_seqlens_q.data_ptr(),
+                                  kv_len.data_ptr(), B, int(block_size), handle)
+    if st:
+        _raise_status(st)
 
 
 def msa_attention_workspace(T: int, batch: int, Hq: int, Hkv: int, max_blocks: int,
@@ -584,21 +600,22 @@ def msa_attention_workspace(T: int, batch: int, Hq: int, Hkv: int, max_blocks: i
 
 def _attention(query, key, value, blocks, block_table, cu_seqlens_q, kv_len, layout, sparse_mode,
                softmax_scale, out, lse, max_blocks, workspace, stream, block_size):
-    lib = load_library()
-    dev = query.device
-    _on_device(dev, (("key", key), ("value", value), ("blocks", blocks), ("out", out),
-                     ("lse", lse), ("block_table", block_table), ("cu_seqlens_q", cu_seqlens_q),
-                     ("kv_len", kv_len), ("workspace", workspace)))
+    lib = _lib or load_library()
+    index = query.get_device()
+    _on_device(index, ("key", key), ("value", value), ("blocks", blocks), ("out", out),
+               ("lse", lse), ("block_table", block_table), ("cu_seqlens_q", cu_seqlens_q),
+               ("kv_len", kv_len), ("workspace", workspace))
     lay = _layout_code(layout)
     max_blocks = int(max_blocks)
     B = _check_lengths(cu_seqlens_q, kv_len, block_table, max_blocks, lay in (1, 2))
-    if query.dim() != 3:
-        raise ValueError(f"query must be [T, Hq, 128], got {tuple(query.shape)}")
-    T, Hq = query.shape[0], query.shape[1]
-    if out.dtype != query.dtype or not out.is_contiguous() or out.shape != query.shape:
-        raise ValueError(f"out must be a contiguous {query.dtype} {tuple(query.shape)} tensor")
-    if lse is not None and (lse.dtype != torch.float32 or not lse.is_contiguous() or
-                            tuple(lse.shape) != (T, Hq)):
+    shape = query.shape
+    if len(shape) != 3:
+        raise ValueError(f"query must be [T, Hq, 128], got {tuple(shape)}")
+    T, Hq, D = shape
+    if out.dtype != query.dtype or out.shape != shape or not out.is_contiguous():
+        raise ValueError(f"out must be a contiguous {query.dtype} {tuple(shape)} tensor")
+    if lse is not None and (lse.dtype != torch.float32 or lse.shape != shape[:2] or
+                            not lse.is_contiguous()):
         raise ValueError(f"lse must be a contiguous float32 [{T}, {Hq}] tensor")
     kr = _key_rows(key, lay)
     Hkv = kr[1] if kr is not None else 0
@@ -611,28 +628,28 @@ def _attention(query, key, value, blocks, block_table, cu_seqlens_q, kv_len, lay
         k = blocks.shape[2]
     if workspace is not None and not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous")
-    scale = 1.0 / math.sqrt(query.shape[2]) if softmax_scale is None else float(softmax_scale)
-    qd, kd, vd = describe(query), describe(key), describe(value)
-    with _On(dev, stream) as handle:
+    scale = 1.0 / math.sqrt(D) if softmax_scale is None else float(softmax_scale)
+    with _On(query, stream) as handle:
         need = lib.msa_attention_workspace(T, B, Hq, Hkv, max_blocks, k)
         if need and workspace is None:
             # memory of the stream that the kernels run on, so that it is
             # handed on only behind them
             if stream is None:
-                workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+                workspace = query.new_empty(need, dtype=torch.uint8)
             else:
-                with torch.cuda.stream(_stream_of(handle, dev)):
-                    workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+                with torch.cuda.stream(_stream_of(handle, query.device)):
+                    workspace = query.new_empty(need, dtype=torch.uint8)
         wb = 0 if workspace is None else workspace.numel() * workspace.element_size()
-        tail = (_ptr(block_table), max_blocks, _ptr(cu_seqlens_q), _ptr(kv_len), B,
-                int(block_size), lay, int(sparse_mode), scale, _ptr(out), _ptr(lse),
-                _ptr(workspace), wb, handle)
-        head = (ctypes.byref(qd), ctypes.byref(kd), ctypes.byref(vd))
+        tail = (_address(block_table), max_blocks, cu_seqlens_q.data_ptr(), kv_len.data_ptr(), B,
+                int(block_size), lay, int(sparse_mode), scale, out.data_ptr(), _address(lse),
+                _address(workspace), wb, handle)
         if blocks is None:
-            st = lib.msa_attention(*head, *tail)
+            st = lib.msa_attention(_packed(query), _packed(key), _packed(value), *tail)
         else:
-            st = lib.msa_block_attention(*head, _ptr(blocks), k, *tail)
-    _raise_status(st)
+            st = lib.msa_block_attention(_packed(query), _packed(key), _packed(value),
+                                         blocks.data_ptr(), k, *tail)
+    if st:
+        _raise_status(st)
     return out
 
 
@@ -678,9 +695,8 @@ def _allocated(query, key, block_table, layout, max_blocks, return_lse, stream):
             max_blocks = (key.shape[0] + 127) // 128   # packed: no more than all keys
 
     def make():
-        out = torch.empty(query.shape, dtype=query.dtype, device=query.device)
-        lse = (torch.empty(query.shape[:2], dtype=torch.float32, device=query.device)
-               if return_lse else None)
+        out = query.new_empty(query.shape)
+        lse = query.new_empty(query.shape[:2], dtype=torch.float32) if return_lse else None
         return out, lse, max_blocks
 
     if stream is None or query.device.type != "cuda":

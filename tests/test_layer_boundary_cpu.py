@@ -3,17 +3,19 @@ rejected with its status (or the binding's error) before anything is launched,
 and the workspace sizes hold together.  No call here reaches a launch: each
 fails validation or has T = 0."""
 import ctypes
+import struct
 
 import pytest
 import torch
 
 import block_max_qk_amd as m
-from block_max_qk_amd._binding import _ITEM, MsaTensor
+from block_max_qk_amd._binding import MsaTensor
 
 OK, NULL, LAYOUT, DTYPE, SHAPE, STRIDE, SCALE, ATTR, HIP, WORKSPACE = range(10)
 TND, BBND, BNBD, ROWS = 0, 1, 2, 3
 F16, BF16, I8, E4M3, E5M2, MX = range(6)
 FAKE = 0x10000          # never dereferenced
+ITEM = struct.Struct("<Qii4q4qQii4q4qQii")       # msa_append_item_t
 
 
 def desc(shape, stride=None, dtype=F16, addr=FAKE):
@@ -152,12 +154,12 @@ DST = dims((6, 128, 2, 128))
 
 
 def item(src=SRC, dst=DST, scale=0, layout=BBND, rotate=1):
-    return _ITEM.pack(*src, *dst, scale, layout, rotate)
+    return ITEM.pack(*src, *dst, scale, layout, rotate)
 
 
 def append(*items, cos=FAKE, sin=FAKE, pos=64, rot=128, pairs=0, table=FAKE, mb=4, cu=FAKE,
            kv=FAKE, B=1, bs=128, n=None, null=False):
-    buf = ctypes.create_string_buffer(b"".join(items) or b"\0" * _ITEM.size)
+    buf = ctypes.create_string_buffer(b"".join(items) or b"\0" * ITEM.size)
     return m.load_library().msa_cache_append(
         None if null else ctypes.addressof(buf), len(items) if n is None else n, cos, sin, pos,
         rot, pairs, table, mb, cu, kv, B, bs, None)
