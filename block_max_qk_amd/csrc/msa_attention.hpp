@@ -635,29 +635,44 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tile_kernel(AttnParams p) {
   }
 
   // The blocks come as a list of `count` entries: the part's own ones in
-  // order, or a span's marked ones.  Their numbers and pages are held one per
-  // lane, 64 entries at a time (page -1: none).
+  // order, or a span's marked ones.  Their numbers (kNoPage: on no page) and
+  // the places of their rows are held one per lane, 64 entries at a time, so
+  // that a stage takes a few readlanes and no address arithmetic (scalar
+  // multiplications per stage held up every wave for hundreds of cycles).
+  constexpr int kNoPage = 1 << 30;
   int base = b0, count = b1 - b0;
   const int span = SEL ? min(kSelSpan, kSelBits / p.tpt & ~31) : 0;
-  int bidx = 0, pidx = -1, pbase = 0;
+  int bidx = 0, pbase = 0;
+  int64_t kat = 0, vat = 0;
   auto load_entries = [&](int from) {
     pbase = from;
-    pidx = -1;
-    bidx = base + from + l;
+    bidx = kNoPage;
+    kat = vat = 0;
     if (from + l < count) {
+      bidx = base + from + l;
       if constexpr (SEL) bidx = base + named[from + l];
       if (p.paged) {
         const int pg = p.block_table[(int64_t)w.b * p.MB + bidx];
-        pidx = pg >= 0 && pg < p.NP ? pg : -1;
+        if (pg >= 0 && pg < p.NP) {
+          kat = pg * p.k_page_stride;
+          vat = pg * p.v_page_stride;
+        } else {
+          bidx |= kNoPage;
+        }
+      } else {
+        kat = (w.koff + (int64_t)bidx * kP) * p.k_row_stride;
+        vat = (w.koff + (int64_t)bidx * kP) * p.v_row_stride;
       }
     }
     bidx = consumed(bidx);
-    pidx = consumed(pidx);
+    kat += (int64_t)hk * p.k_head_stride;
+    vat += (int64_t)hk * p.v_head_stride;
   };
-  struct Entry { int beta, page; };
+  struct Entry { int beta; bool there; int64_t k, v; };
   auto entry_at = [&](int e) -> Entry {
     if (e - pbase >= 64) load_entries(e);
-    return Entry{lane_at(bidx, e - pbase), lane_at(pidx, e - pbase)};
+    const int x = lane_at(bidx, e - pbase);
+    return Entry{x & (kNoPage - 1), x < kNoPage, lane_at(kat, e - pbase), lane_at(vat, e - pbase)};
   };
 
   const int cr = l >> 4, cc = l & 15;
@@ -668,31 +683,27 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tile_kernel(AttnParams p) {
     kof[i] = (uint32_t)(r * p.k_row_stride + 16 * (cc ^ (r & 15)));
     vof[i] = (uint32_t)(r * p.v_row_stride + 16 * (cc ^ ((r & 3) << 2)));
   }
-  // Where the keys of half `in` of a block lie, and how many of them there are
-  // to the tile's last visible one.
-  struct Rows { const uint8_t *k, *v; int n; };
+  // Where the keys of half `in` of a block lie, and how many bytes of them
+  // there are to the tile's last visible one.
+  struct Rows { const uint8_t *k, *v; int kb, vb; };
   auto rows_of = [&](const Entry& x, int in) -> Rows {
-    const int j0 = x.beta * kP + in * kTileKeys;
-    const bool there = !p.paged || x.page >= 0;
-    const int64_t pg = max(x.page, 0);
-    const int64_t kb = p.paged ? pg * p.k_page_stride + (int64_t)(in * kTileKeys) * p.k_row_stride
-                               : (w.koff + j0) * p.k_row_stride;
-    const int64_t vb = p.paged ? pg * p.v_page_stride + (int64_t)(in * kTileKeys) * p.v_row_stride
-                               : (w.koff + j0) * p.v_row_stride;
-    return Rows{p.k + uniform64(kb + (int64_t)hk * p.k_head_stride),
-                p.v + uniform64(vb + (int64_t)hk * p.v_head_stride),
-                __builtin_amdgcn_readfirstlane(there ? max(0, min(kTileKeys, lim_hi + 1 - j0)) : 0)};
+    const int left = x.there ? max(0, min(kTileKeys, lim_hi + 1 - x.beta * kP - in * kTileKeys)) : 0;
+    return Rows{p.k + x.k + in * kTileKeys * p.k_row_stride,
+                p.v + x.v + in * kTileKeys * p.v_row_stride,
+                __builtin_amdgcn_readfirstlane(left * p.k_row_stride),
+                __builtin_amdgcn_readfirstlane(left * p.v_row_stride)};
   };
   // a stage's rows through registers, for the careful pass (whose copies need
   // not overlap anything)
   auto copy_plain = [&](uint8_t* dst, const Entry& x, int in) {
     const Rows r = rows_of(x, in);
     for (int i = 0; i < NI; ++i) {
-      const bool ok = (wave * NI + i) * 4 + cr < r.n;
+      const int row = (wave * NI + i) * 4 + cr;
       const int at = (wave * NI + i) * 1024 + 16 * l;
       const i32x4 zero = {0, 0, 0, 0};
-      *reinterpret_cast<i32x4*>(dst + at) = ok ? ld16(r.k + kof[i]) : zero;
-      *reinterpret_cast<i32x4*>(dst + SB + at) = ok ? ld16(r.v + vof[i]) : zero;
+      *reinterpret_cast<i32x4*>(dst + at) = row * p.k_row_stride < r.kb ? ld16(r.k + kof[i]) : zero;
+      *reinterpret_cast<i32x4*>(dst + SB + at) =
+          row * p.v_row_stride < r.vb ? ld16(r.v + vof[i]) : zero;
     }
   };
 
@@ -705,12 +716,11 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tile_kernel(AttnParams p) {
   auto stage = [&](const uint8_t* __restrict kt, uint8_t* __restrict dst, const Entry& cur, int in,
                    const Rows& next, bool mine, auto careful) __attribute__((always_inline)) {
     if constexpr (!decltype(careful)::value)
-      copy_stage<NI>(dst + wave * NI * 1024, SB, next.k, next.v, next.n * p.k_row_stride,
-                     next.n * p.v_row_stride, kof, vof);
+      copy_stage<NI>(dst + wave * NI * 1024, SB, next.k, next.v, next.kb, next.vb, kof, vof);
     if (SEL && !__ballot(mine && row_ok)) return;
     const uint8_t* vt = kt + SB;
     const int j0 = cur.beta * kP + in * kTileKeys;
-    const bool there = !p.paged || cur.page >= 0;
+    const bool there = cur.there;
 
     // S^T, two tiles of 32 keys: register r of tile t is key
     // j0 + 32 t + 8 (r / 4) + 4 h + r % 4 of row n
@@ -831,21 +841,23 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tile_kernel(AttnParams p) {
       }
     } else {
       Rows r = rows_of(x, 0);
-      copy_stage<NI>(ring + wave * NI * 1024, SB, r.k, r.v, r.n * p.k_row_stride,
-                     r.n * p.v_row_stride, kof, vof);
-      for (int s = 0; s < stages; ++s) {
+      copy_stage<NI>(ring + wave * NI * 1024, SB, r.k, r.v, r.kb, r.vb, kof, vof);
+      for (int e = 0; e < count; ++e) {
         const Entry cur = x;
-        if (s + 1 < stages) {
-          if (s & 1) x = entry_at((s + 1) >> 1);
-          r = rows_of(x, (s + 1) & 1);
-        } else {
-          r.n = 0;       // (nothing is read: the last copies bring zeros)
-        }
         const bool mine = selected(cur);
-        // this wave's copies of stage s have landed; after the barrier
-        // everyone's have, and everyone has read stage s - 1
+        // at each half: this wave's copies of the stage have landed; after the
+        // barrier everyone's have, and everyone has read the stage before
+        r = rows_of(cur, 1);
         asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-        stage(ring + (s & 1) * 2 * SB, ring + (~s & 1) * 2 * SB, cur, s & 1, r, mine, careful);
+        stage(ring, ring + 2 * SB, cur, 0, r, mine, careful);
+        if (e + 1 < count) {
+          x = entry_at(e + 1);
+          r = rows_of(x, 0);
+        } else {
+          r.kb = r.vb = 0;       // (nothing is read: the last copies bring zeros)
+        }
+        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        stage(ring + 2 * SB, ring, cur, 1, r, mine, careful);
       }
       asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     }
