@@ -725,23 +725,33 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tile_kernel(AttnParams p) {
     // S^T, two tiles of 32 keys: register r of tile t is key
     // j0 + 32 t + 8 (r / 4) + 4 h + r % 4 of row n
     f32x16 st[2] = {f32x16{}, f32x16{}};
+    // (K fragments are read KLEAD ahead of their MFMAs and pinned there: left to
+    // itself the compiler read each right before its use, and every MFMA waited
+    // for the LDS)
+    constexpr int KLEAD = 4;
+    i32x4 kf[16];
+    auto key_frag = [&](int i) -> i32x4 {
+      const int jj = 32 * (i >> 3) + n;
+      return *reinterpret_cast<const i32x4*>(kt + jj * 256 +
+                                             (((2 * (i & 7) + h) ^ (jj & 15)) << 4));
+    };
 #pragma unroll
-    for (int t = 0; t < 2; ++t)
+    for (int i = 0; i < KLEAD; ++i) kf[i] = key_frag(i);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const int jj = 32 * t + n;
-        st[t] = mfma32x32x16<KK>(
-            *reinterpret_cast<const i32x4*>(kt + jj * 256 + (((2 * k + h) ^ (jj & 15)) << 4)), qv[k],
-            st[t]);
-      }
+    for (int i = 0; i < 16; ++i) {
+      if (i + KLEAD < 16) kf[i + KLEAD] = key_frag(i + KLEAD);
+      st[i >> 3] = mfma32x32x16<KK>(kf[i], qv[i & 7], st[i >> 3]);
+      __builtin_amdgcn_sched_barrier(0);
+    }
     if (!there || j0 + kTileKeys - 1 > lim_lo) {
+      // (compared as constants against one value per lane: the keys' numbers
+      // themselves would take 32 registers through the whole loop)
+      const int rel = there ? lim - j0 - 4 * h : -1;
 #pragma unroll
       for (int t = 0; t < 2; ++t)
 #pragma unroll
-        for (int r = 0; r < 16; ++r) {
-          const int j = j0 + 32 * t + 8 * (r >> 2) + 4 * h + (r & 3);
-          st[t][r] = there && j <= lim ? st[t][r] : -__builtin_inff();
-        }
+        for (int r = 0; r < 16; ++r)
+          st[t][r] = 32 * t + 8 * (r >> 2) + (r & 3) <= rel ? st[t][r] : -__builtin_inff();
     }
     float mx = st[0][0];
 #pragma unroll
