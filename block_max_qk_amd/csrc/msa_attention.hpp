@@ -166,22 +166,17 @@ __device__ __forceinline__ void landed(i32x4& x) { asm volatile("" : "+v"(x)); }
 // maximum moves, so its bits do not depend on the rows it shares a tile with.)
 constexpr float kMaxLag = 8.f;
 
-// NI copies each of a stage's K and V rows: a wave's lanes' pieces at the byte
-// offsets kof and vof of two raw buffers, 1 KB a copy, the V rows `vat` bytes
-// behind the K rows.
+// NI copies of 1 KB, a wave's lanes' pieces at the byte offsets `of` of a raw
+// buffer of `bytes`.
 template <int NI>
-__device__ __forceinline__ void copy_stage(uint8_t* dst, int vat, const uint8_t* k,
-                                           const uint8_t* v, int kbytes, int vbytes,
-                                           const uint32_t* kof, const uint32_t* vof) {
-  const __amdgpu_buffer_rsrc_t kr =
-      __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(k), 0, kbytes, kBufferWord3);
-  const __amdgpu_buffer_rsrc_t vr =
-      __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(v), 0, vbytes, kBufferWord3);
+__device__ __forceinline__ void copy_rows(uint8_t* dst, const uint8_t* src, int bytes,
+                                          const uint32_t* of) {
+  const __amdgpu_buffer_rsrc_t rs =
+      __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(src), 0, bytes, kBufferWord3);
 #pragma unroll
-  for (int i = 0; i < NI; ++i) buffer_copy16_lds(kr, dst + 1024 * i, kof[i]);
-#pragma unroll
-  for (int i = 0; i < NI; ++i) buffer_copy16_lds(vr, dst + vat + 1024 * i, vof[i]);
+  for (int i = 0; i < NI; ++i) buffer_copy16_lds(rs, dst + 1024 * i, of[i]);
 }
+
 constexpr int kSelBits = 131072;       // (token, block) marks of a workgroup
 constexpr int kSelSpan = 4096;         // blocks marked at a time, at most
 
@@ -334,8 +329,8 @@ __global__ __launch_bounds__(256, 1) void attn_rows_kernel(AttnParams p) {
                   const Rows& next, bool more, auto careful) __attribute__((always_inline)) {
     if constexpr (!decltype(careful)::value) {
       if (more) {
-        copy_stage<8>(dst, 8192, next.k, next.v, next.n * p.k_row_stride,
-                      next.n * p.v_row_stride, kof, vof);
+        copy_rows<8>(dst, next.k, next.n * p.k_row_stride, kof);
+        copy_rows<8>(dst + 8192, next.v, next.n * p.v_row_stride, vof);
         asm volatile("s_waitcnt vmcnt(16)" ::: "memory");
       } else {
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
@@ -422,8 +417,10 @@ __global__ __launch_bounds__(256, 1) void attn_rows_kernel(AttnParams p) {
     if (!SEL && pbase > 0) load_pages(0);
     Block cur = block_at(0);
     Rows r = rows_of(cur);
-    if constexpr (!decltype(careful)::value)
-      copy_stage<8>(mine, 8192, r.k, r.v, r.n * p.k_row_stride, r.n * p.v_row_stride, kof, vof);
+    if constexpr (!decltype(careful)::value) {
+      copy_rows<8>(mine, r.k, r.n * p.k_row_stride, kof);
+      copy_rows<8>(mine + 8192, r.v, r.n * p.v_row_stride, vof);
+    }
     for (int s = 0; s < nst; ++s) {
       Block next = cur;
       if constexpr (decltype(careful)::value) {
@@ -592,7 +589,8 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tile_kernel(AttnParams p) {
   constexpr int kMarksAt = 4 * SB, kNamedAt = kMarksAt + (SEL ? kSelBits / 8 : 0);
   constexpr int kFlagAt = kNamedAt + (SEL ? 2 * kSelSpan : 0);
   __shared__ __attribute__((aligned(16))) uint8_t lds[kFlagAt + 16];
-  uint8_t* const ring = lds;                                        // [2][K rows, V rows]
+  uint8_t* const kring = lds;                                       // [2][64 K rows]
+  uint8_t* const vring = lds + 2 * SB;                              // [2][64 V rows]
   uint32_t* const marks = reinterpret_cast<uint32_t*>(lds + kMarksAt);   // [token][block of the span]
   uint16_t* const named = reinterpret_cast<uint16_t*>(lds + kNamedAt);   // the span's blocks, ascending
   int* const flag = reinterpret_cast<int*>(lds + kFlagAt);
@@ -695,14 +693,14 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tile_kernel(AttnParams p) {
   };
   // a stage's rows through registers, for the careful pass (whose copies need
   // not overlap anything)
-  auto copy_plain = [&](uint8_t* dst, const Entry& x, int in) {
+  auto copy_plain = [&](const Entry& x, int in) {
     const Rows r = rows_of(x, in);
     for (int i = 0; i < NI; ++i) {
       const int row = (wave * NI + i) * 4 + cr;
       const int at = (wave * NI + i) * 1024 + 16 * l;
       const i32x4 zero = {0, 0, 0, 0};
-      *reinterpret_cast<i32x4*>(dst + at) = row * p.k_row_stride < r.kb ? ld16(r.k + kof[i]) : zero;
-      *reinterpret_cast<i32x4*>(dst + SB + at) =
+      *reinterpret_cast<i32x4*>(kring + at) = row * p.k_row_stride < r.kb ? ld16(r.k + kof[i]) : zero;
+      *reinterpret_cast<i32x4*>(vring + at) =
           row * p.v_row_stride < r.vb ? ld16(r.v + vof[i]) : zero;
     }
   };
@@ -710,21 +708,15 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tile_kernel(AttnParams p) {
   f32x16 o[4];
   float m, lsum;
 
-  // One stage: the copies of the next one's rows into `dst`, then its own at kt
-  // (as in attn_rows_kernel, the parameters say that the two do not overlap).
-  // `mine`: this lane's row's token selected the block.
-  auto stage = [&](const uint8_t* __restrict kt, uint8_t* __restrict dst, const Entry& cur, int in,
-                   const Rows& next, bool mine, auto careful) __attribute__((always_inline)) {
-    if constexpr (!decltype(careful)::value)
-      copy_stage<NI>(dst + wave * NI * 1024, SB, next.k, next.v, next.kb, next.vb, kof, vof);
-    if (SEL && !__ballot(mine && row_ok)) return;
-    const uint8_t* vt = kt + SB;
-    const int j0 = cur.beta * kP + in * kTileKeys;
-    const bool there = cur.there;
-
+  // A stage in two parts: its scores from the K rows at kt, and what follows
+  // from them with the V rows at vt.  `mine`: this lane's row's token selected
+  // the block.  (The copies that may be in flight go to other parts of the
+  // rings, and the parameters say so, as in attn_rows_kernel.)
+  f32x16 st[2];
+  auto scores = [&](const uint8_t* __restrict kt) __attribute__((always_inline)) {
     // S^T, two tiles of 32 keys: register r of tile t is key
     // j0 + 32 t + 8 (r / 4) + 4 h + r % 4 of row n
-    f32x16 st[2] = {f32x16{}, f32x16{}};
+    st[0] = st[1] = f32x16{};
     // (K fragments are read KLEAD ahead of their MFMAs and pinned there: left to
     // itself the compiler read each right before its use, and every MFMA waited
     // for the LDS)
@@ -743,6 +735,11 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tile_kernel(AttnParams p) {
       st[i >> 3] = mfma32x32x16<KK>(kf[i], qv[i & 7], st[i >> 3]);
       __builtin_amdgcn_sched_barrier(0);
     }
+  };
+  auto absorb = [&](const uint8_t* __restrict vt, const Entry& cur, int in, bool mine, auto careful)
+      __attribute__((always_inline)) {
+    const int j0 = cur.beta * kP + in * kTileKeys;
+    const bool there = cur.there;
     if (!there || j0 + kTileKeys - 1 > lim_lo) {
       // (compared as constants against one value per lane: the keys' numbers
       // themselves would take 32 registers through the whole loop)
@@ -770,41 +767,49 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tile_kernel(AttnParams p) {
     }
     const float ms = m == -__builtin_inff() ? 0.f : m;
     float add = 0.f;
-#pragma unroll
-    for (int t = 0; t < 2; ++t)
-#pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        st[t][r] = exp2_hw(__builtin_fmaf(st[t][r], p.c, -ms));
-        add += st[t][r];
-      }
-    lsum += !SEL || mine ? add : 0.f;
     i32x4 pf[4];
-#pragma unroll
-    for (int u = 0; u < 4; ++u)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int pk = pack2<KK>(st[u >> 1][8 * (u & 1) + 2 * e], st[u >> 1][8 * (u & 1) + 2 * e + 1]);
-        pf[u][e] = !SEL || mine ? pk : 0;
-      }
+    // weights 2 i and 2 i + 1 of this lane's 32, rounded and packed
+    auto weigh = [&](int i) __attribute__((always_inline)) {
+      const float a = exp2_hw(__builtin_fmaf(st[i >> 3][2 * (i & 7)], p.c, -ms));
+      const float b = exp2_hw(__builtin_fmaf(st[i >> 3][2 * (i & 7) + 1], p.c, -ms));
+      add += a + b;
+      const int pk = pack2<KK>(a, b);
+      pf[i >> 2][i & 3] = !SEL || mine ? pk : 0;
+    };
     // O^T += V^T P^T, 16 keys a step: registers 8 u .. 8 u + 7 of a tile are
     // keys 16 u + 4 h + {0..3} and 16 u + 8 + 4 h + {0..3}
     const int vi = l & 15;
-    auto value = [&](int u, int d) -> i32x4 {
-      const int r = 16 * u + 4 * h + (vi >> 2);
-      const int ch = ((4 * d + 2 * ((l >> 4) & 1) + ((vi >> 1) & 1)) ^ ((r & 3) << 2)) * 16 +
+    auto value = [&](int i) __attribute__((always_inline)) -> i32x4 {
+      const int r = 16 * (i >> 2) + 4 * h + (vi >> 2);
+      const int ch = ((4 * (i & 3) + 2 * ((l >> 4) & 1) + ((vi >> 1) & 1)) ^ ((r & 3) << 2)) * 16 +
                      (vi & 1) * 8;
       const i32x2 v0 = lds_read_tr(vt + r * 256 + ch);
       const i32x2 v1 = lds_read_tr(vt + (r + 8) * 256 + ch);
       return i32x4{v0[0], v0[1], v1[0], v1[1]};
     };
     if constexpr (!decltype(careful)::value) {
+      // (a step's MFMAs run beside the next step's weights, each with one pair
+      // of them and the read of a later operand, pinned)
+      constexpr int VLEAD = 3;
+      i32x4 vf[16];
 #pragma unroll
-      for (int u = 0; u < 4; ++u)
+      for (int i = 0; i < VLEAD; ++i) vf[i] = value(i);
 #pragma unroll
-        for (int d = 0; d < 4; ++d) o[d] = mfma32x32x16<KK>(value(u, d), pf[u], o[d]);
+      for (int i = 0; i < 4; ++i) weigh(i);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        if (i + VLEAD < 16) vf[i + VLEAD] = value(i + VLEAD);
+        o[i & 3] = mfma32x32x16<KK>(vf[i], pf[i >> 2], o[i & 3]);
+        if (i < 12) weigh(i + 4);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      lsum += !SEL || mine ? add : 0.f;
     } else {
       // token by token: the values of keys that it does not see cleared, its
       // rows' sums kept
+#pragma unroll
+      for (int i = 0; i < 16; ++i) weigh(i);
+      lsum += !SEL || mine ? add : 0.f;
       const int first = wave * 32 / p.hpt, last = min((wave * 32 + 31) / p.hpt, w.ntok - 1);
       for (int tk = first; tk <= last; ++tk) {
         const unsigned long long its = __ballot(row_ok && ti == tk && mine);
@@ -815,7 +820,7 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tile_kernel(AttnParams p) {
           f32x16 x = o[d];
 #pragma unroll
           for (int u = 0; u < 4; ++u) {
-            i32x4 v = value(u, d);
+            i32x4 v = value(4 * u + d);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               const int j = j0 + 16 * u + 8 * (e >> 1) + 4 * h + 2 * (e & 1);
@@ -834,43 +839,62 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tile_kernel(AttnParams p) {
   auto walk = [&](auto careful) __attribute__((always_inline)) {
     if (count <= 0) return;
     load_entries(0);
-    Entry x = entry_at(0);
-    const int stages = 2 * count;
     auto selected = [&](const Entry& e) -> bool {
       if constexpr (!SEL) return true;
       const int at = e.beta - base;
       return row_ok && (marks[ti * (span >> 5) + (at >> 5)] >> (at & 31)) & 1;
     };
+    auto some = [&](bool mine) -> bool { return !SEL || __ballot(mine && row_ok) != 0; };
     if constexpr (decltype(careful)::value) {
-      for (int s = 0; s < stages; ++s) {
-        x = entry_at(s >> 1);
+      for (int s = 0; s < 2 * count; ++s) {
+        const Entry x = entry_at(s >> 1);
         __syncthreads();
-        copy_plain(ring, x, s & 1);
+        copy_plain(x, s & 1);
         __syncthreads();
-        stage(ring, ring + 2 * SB, x, s & 1, Rows{}, selected(x), careful);
-      }
-    } else {
-      Rows r = rows_of(x, 0);
-      copy_stage<NI>(ring + wave * NI * 1024, SB, r.k, r.v, r.kb, r.vb, kof, vof);
-      for (int e = 0; e < count; ++e) {
-        const Entry cur = x;
-        const bool mine = selected(cur);
-        // at each half: this wave's copies of the stage have landed; after the
-        // barrier everyone's have, and everyone has read the stage before
-        r = rows_of(cur, 1);
-        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-        stage(ring, ring + 2 * SB, cur, 0, r, mine, careful);
-        if (e + 1 < count) {
-          x = entry_at(e + 1);
-          r = rows_of(x, 0);
-        } else {
-          r.kb = r.vb = 0;       // (nothing is read: the last copies bring zeros)
+        const bool mine = selected(x);
+        if (some(mine)) {
+          scores(kring);
+          absorb(vring, x, s & 1, mine, careful);
         }
-        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-        stage(ring + 2 * SB, ring, cur, 1, r, mine, careful);
       }
-      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+      return;
     }
+    Entry x = entry_at(0);
+    Rows r = rows_of(x, 0);
+    // one half of an entry: the copies of the next into `kd` and `vd`, then its
+    // own work on the rows at kt and vt
+    auto half = [&](const uint8_t* __restrict kt, const uint8_t* __restrict vt,
+                    uint8_t* __restrict kd, uint8_t* __restrict vd, int in, bool mine, bool any)
+        __attribute__((always_inline)) {
+      copy_rows<NI>(kd + wave * NI * 1024, r.k, r.kb, kof);
+      copy_rows<NI>(vd + wave * NI * 1024, r.v, r.vb, vof);
+      if (any) {
+        scores(kt);
+        absorb(vt, x, in, mine, careful);
+      }
+    };
+    copy_rows<NI>(kring + wave * NI * 1024, r.k, r.kb, kof);
+    copy_rows<NI>(vring + wave * NI * 1024, r.v, r.vb, vof);
+    for (int e = 0; e < count; ++e) {
+      const bool mine = selected(x);
+      const bool any = some(mine);
+      // at each half: this wave's copies of the stage have landed; after the
+      // barrier everyone's have, and everyone has read the stage before
+      r = rows_of(x, 1);
+      asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+      half(kring, vring, kring + SB, vring + SB, 0, mine, any);
+      Entry xn = x;
+      if (e + 1 < count) {
+        xn = entry_at(e + 1);
+        r = rows_of(xn, 0);
+      } else {
+        r.kb = r.vb = 0;       // (nothing is read: the last copies bring zeros)
+      }
+      asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+      half(kring + SB, vring + SB, kring, vring, 1, mine, any);
+      x = xn;
+    }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
   };
 
   auto pass = [&](auto careful) __attribute__((always_inline)) {
