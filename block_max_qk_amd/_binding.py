@@ -7,6 +7,7 @@ library is missing the call raises: there is no fallback implementation.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
@@ -463,14 +464,6 @@ def _address(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
 
 
-def _on_device(index, *named):
-    """Every (name, tensor) on the device of this index (-1: the host)."""
-    for name, t in named:
-        if t is not None and t.get_device() != index:
-            raise ValueError(f"{name} is on {t.device}, the call's first tensor on "
-                             f"{'cpu' if index < 0 else 'cuda:%d' % index}")
-
-
 def _check_lengths(cu_seqlens_q, kv_len, block_table, max_blocks, paged) -> int:
     """The request count B, from tensors whose extents the C ABI takes on trust."""
     i32 = torch.int32
@@ -504,25 +497,14 @@ def _stream_of(handle, dev):
     return torch.cuda.ExternalStream(handle, device=dev)
 
 
-class _On:
-    """The device of a call, and its stream's handle (a stream of another
-    device than the current one is launched on with its own made current)."""
+def _guard(index: int):
+    """Makes the tensors' device current for a launch, where it is not."""
+    if index < 0 or torch.cuda.current_device() == index:
+        return _NO_GUARD
+    return torch.cuda.device(index)
 
-    def __init__(self, t, stream):
-        self.guard = None
-        index = t.get_device()
-        if index >= 0 and torch.cuda.current_device() != index:
-            self.guard = torch.cuda.device(index)
-        self.handle = _stream_handle(stream, index if index >= 0 else t.device)
 
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-        return self.handle
-
-    def __exit__(self, *e):
-        if self.guard is not None:
-            self.guard.__exit__(*e)
+_NO_GUARD = contextlib.nullcontext()
 
 
 def _item_layout(layout) -> int:
@@ -547,8 +529,9 @@ def msa_cache_append(items: Sequence[CacheItem], cos: Optional[torch.Tensor],
     if not 1 <= len(items) <= APPEND_MAX_ITEMS:
         raise ValueError(f"1 to {APPEND_MAX_ITEMS} items, got {len(items)}")
     index = items[0].src.get_device()
-    _on_device(index, ("cos", cos), ("sin", sin), ("block_table", block_table),
-               ("cu_seqlens_q", cu_seqlens_q), ("kv_len", kv_len))
+    for t in (cos, sin, block_table, cu_seqlens_q, kv_len):
+        if t is not None and t.get_device() != index:
+            raise ValueError(f"tensors are on {t.device} and {items[0].src.device}")
     paged = block_table is not None
     max_blocks = block_table.shape[-1] if paged else 0
     B = _check_lengths(cu_seqlens_q, kv_len, block_table, max_blocks, paged)
@@ -581,7 +564,8 @@ def msa_cache_append(items: Sequence[CacheItem], cos: Optional[torch.Tensor],
                                  f"{tuple(scale.shape)} on {scale.device}")
             at = scale.data_ptr()
         packed += (_packed(src), _packed(dst), _ITEM_TAIL.pack(at, lay, 1 if rotate else 0))
-    with _On(items[0].src, stream) as handle:
+    handle = _stream_handle(stream, index)
+    with _guard(index):
         st = lib.msa_cache_append(b"".join(packed), len(items), _address(cos), _address(sin),
                                   positions, rotary, 1 if interleaved else 0,
                                   _address(block_table), max_blocks, cu_seqlens_q.data_ptr(),
@@ -602,9 +586,12 @@ def _attention(query, key, value, blocks, block_table, cu_seqlens_q, kv_len, lay
                softmax_scale, out, lse, max_blocks, workspace, stream, block_size):
     lib = _lib or load_library()
     index = query.get_device()
-    _on_device(index, ("key", key), ("value", value), ("blocks", blocks), ("out", out),
-               ("lse", lse), ("block_table", block_table), ("cu_seqlens_q", cu_seqlens_q),
-               ("kv_len", kv_len), ("workspace", workspace))
+    for t in (key, value, out, cu_seqlens_q, kv_len):
+        if t.get_device() != index:
+            raise ValueError(f"tensors are on {t.device} and {query.device}")
+    for t in (block_table, lse, blocks, workspace):
+        if t is not None and t.get_device() != index:
+            raise ValueError(f"tensors are on {t.device} and {query.device}")
     lay = _layout_code(layout)
     max_blocks = int(max_blocks)
     B = _check_lengths(cu_seqlens_q, kv_len, block_table, max_blocks, lay in (1, 2))
@@ -629,7 +616,8 @@ def _attention(query, key, value, blocks, block_table, cu_seqlens_q, kv_len, lay
     if workspace is not None and not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous")
     scale = 1.0 / math.sqrt(D) if softmax_scale is None else float(softmax_scale)
-    with _On(query, stream) as handle:
+    handle = _stream_handle(stream, index)
+    with _guard(index):
         need = lib.msa_attention_workspace(T, B, Hq, Hkv, max_blocks, k)
         if need and workspace is None:
             # memory of the stream that the kernels run on, so that it is

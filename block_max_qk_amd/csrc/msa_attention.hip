@@ -45,8 +45,8 @@ Plan plan_for(int64_t T, int64_t B, int64_t Hq, int64_t Hkv, int64_t MB, int64_t
   const int64_t items = std::max<int64_t>(p.ntiles * Hkv * p.hchunks, 1);
   const int64_t blocks = std::max<int64_t>(few && nsel > 0 ? std::min(nsel, MB) : MB, 1);
   p.min_blocks = few ? 2 : 4;
-  const int64_t want = few ? 2048 : 1024, enough = few ? 1024 : 256;
-  int64_t n = items >= enough ? 1 : (want + items - 1) / items;
+  const int64_t want = nsel > 0 && few ? 256 : few ? 1536 : 512;
+  int64_t n = items >= want ? 1 : (want + items - 1) / items;
   n = std::min(n, (blocks + p.min_blocks - 1) / p.min_blocks);
   p.nsplit = (int)std::max<int64_t>(1, std::min(n, kMaxSplit));
   return p;

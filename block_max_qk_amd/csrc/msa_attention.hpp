@@ -59,7 +59,8 @@ constexpr float kLn2 = 0.69314718055994530942f;
 struct AttnTile {
   int valid;
   int t0, ntok, i0;            // first token, tokens, index of the first in the request
-  int b, Lq, L;                // request, its new tokens, its keys
+  int b, Lq, L;                // request, its new tokens, its keys that exist
+  int len;                     // kv_len of the request (positions follow from it)
   int64_t koff;                // packed offset of the request's keys
 };
 
@@ -96,7 +97,7 @@ __device__ __forceinline__ AttnTile attn_tile(const AttnParams& p, int tile) {
       const int64_t room = p.T - (int64_t)w.t0;
       w.ntok = (int)min((int64_t)min(p.tpt, w.Lq - w.i0), w.t0 < 0 ? (int64_t)0 : room);
       w.koff = kacc + lane_at(kincl, src) - lane_at(kv, src);
-      w.L = lane_at(kv, src);
+      w.L = w.len = lane_at(kv, src);
       if (p.paged)
         w.L = (int)min((int64_t)w.L, (int64_t)p.MB * kP);
       else
@@ -111,10 +112,9 @@ __device__ __forceinline__ AttnTile attn_tile(const AttnParams& p, int tile) {
 }
 
 // Last visible key of the request's i-th new token: kv_len - L_q + i under
-// the causal mode, the last key without it.  (The position comes from kv_len
-// as given; attn_tile has cut L to the keys that exist.)
-__device__ __forceinline__ int attn_last(const AttnParams& p, const AttnTile& w, int len, int i) {
-  return min(p.causal ? len - w.Lq + i : w.L - 1, w.L - 1);
+// the causal mode, the last key without it.
+__device__ __forceinline__ int attn_last(const AttnParams& p, const AttnTile& w, int i) {
+  return min(p.causal ? w.len - w.Lq + i : w.L - 1, w.L - 1);
 }
 
 // Two floats -> one register of two 16-bit operands, rounded to nearest.
@@ -211,15 +211,14 @@ __global__ __launch_bounds__(256, 1) void attn_rows_kernel(AttnParams p) {
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l = lane_id();
   const int n = l & 15, G = l >> 4;
-  const int len = p.kv_len[w.b];
 
   // this lane's row (column n of every MFMA result)
   const int ti = n / p.hpt;
   const int hg = hc * p.hpt + (n - ti * p.hpt);
   const bool row_ok = ti < w.ntok && ti < p.tpt && hg < p.g;
-  const int lim = row_ok ? attn_last(p, w, len, w.i0 + ti) : -1;
-  const int lim_lo = attn_last(p, w, len, w.i0);
-  const int lim_hi = attn_last(p, w, len, w.i0 + w.ntok - 1);
+  const int lim = row_ok ? attn_last(p, w, w.i0 + ti) : -1;
+  const int lim_lo = attn_last(p, w, w.i0);
+  const int lim_hi = attn_last(p, w, w.i0 + w.ntok - 1);
   const int nb = lim_hi >= 0 ? lim_hi / kP + 1 : 0;    // blocks with a visible key
 
   // the part's blocks: [b0, b1) of the visible ones, or of the selected list
@@ -389,7 +388,7 @@ __global__ __launch_bounds__(256, 1) void attn_rows_kernel(AttnParams p) {
       for (int d = 0; d < 8; ++d) o[d] = mfma16x16x32<KK>(value(d), pf, o[d]);
     } else {
       for (int tk = 0; tk < w.ntok; ++tk) {
-        const int end = attn_last(p, w, len, w.i0 + tk);
+        const int end = attn_last(p, w, w.i0 + tk);
 #pragma unroll
         for (int d = 0; d < 8; ++d) {
           i32x4 v = value(d);
@@ -610,14 +609,13 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tile_kernel(AttnParams p) {
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int l = lane_id();
   const int n = l & 31, h = l >> 5;
-  const int len = p.kv_len[w.b];
   const int row = wave * 32 + n;
   const int ti = row / p.hpt;
   const int hg = hc * p.hpt + (row - ti * p.hpt);
   const bool row_ok = row < p.hpt * p.tpt && ti < w.ntok && hg < p.g;
-  const int lim = row_ok ? attn_last(p, w, len, w.i0 + ti) : -1;
-  const int lim_lo = attn_last(p, w, len, w.i0);
-  const int lim_hi = attn_last(p, w, len, w.i0 + w.ntok - 1);
+  const int lim = row_ok ? attn_last(p, w, w.i0 + ti) : -1;
+  const int lim_lo = attn_last(p, w, w.i0);
+  const int lim_hi = attn_last(p, w, w.i0 + w.ntok - 1);
   const int total = lim_hi >= 0 ? lim_hi / kP + 1 : 0;
   const int parts = max(1, min(p.nsplit, (total + p.min_blocks - 1) / p.min_blocks));
   const int b0 = (int)((int64_t)total * split / parts);
@@ -814,7 +812,7 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tile_kernel(AttnParams p) {
       for (int tk = first; tk <= last; ++tk) {
         const unsigned long long its = __ballot(row_ok && ti == tk && mine);
         if (!its) continue;
-        const int end = attn_last(p, w, len, w.i0 + tk);
+        const int end = attn_last(p, w, w.i0 + tk);
 #pragma unroll
         for (int d = 0; d < 4; ++d) {
           f32x16 x = o[d];
@@ -914,7 +912,7 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tile_kernel(AttnParams p) {
         for (int i = tid; i < w.ntok * p.nsel; i += 64 * NW) {
           const int tk = i / p.nsel;
           const int e = p.blocks[((int64_t)(w.t0 + tk) * p.Hkv + hk) * p.nsel + (i - tk * p.nsel)];
-          if (e >= base && e < end && (int64_t)e * kP <= attn_last(p, w, len, w.i0 + tk))
+          if (e >= base && e < end && (int64_t)e * kP <= attn_last(p, w, w.i0 + tk))
             atomicOr(&marks[tk * words + ((e - base) >> 5)], 1u << ((e - base) & 31));
         }
         __syncthreads();
