@@ -586,12 +586,14 @@ def _attention(query, key, value, blocks, block_table, cu_seqlens_q, kv_len, lay
                softmax_scale, out, lse, max_blocks, workspace, stream, block_size):
     lib = _lib or load_library()
     index = query.get_device()
-    for t in (key, value, out, cu_seqlens_q, kv_len):
-        if t.get_device() != index:
-            raise ValueError(f"tensors are on {t.device} and {query.device}")
-    for t in (block_table, lse, blocks, workspace):
-        if t is not None and t.get_device() != index:
-            raise ValueError(f"tensors are on {t.device} and {query.device}")
+    if (key.get_device() != index or value.get_device() != index or
+            cu_seqlens_q.get_device() != index or kv_len.get_device() != index or
+            out.get_device() != index or
+            (block_table is not None and block_table.get_device() != index) or
+            (lse is not None and lse.get_device() != index) or
+            (blocks is not None and blocks.get_device() != index) or
+            (workspace is not None and workspace.get_device() != index)):
+        raise ValueError(f"every tensor must be on the query's device, {query.device}")
     lay = _layout_code(layout)
     max_blocks = int(max_blocks)
     B = _check_lengths(cu_seqlens_q, kv_len, block_table, max_blocks, lay in (1, 2))
@@ -683,7 +685,7 @@ def _allocated(query, key, block_table, layout, max_blocks, return_lse, stream):
             max_blocks = (key.shape[0] + 127) // 128   # packed: no more than all keys
 
     def make():
-        out = query.new_empty(query.shape)
+        out = torch.empty_like(query, memory_format=torch.contiguous_format)
         lse = query.new_empty(query.shape[:2], dtype=torch.float32) if return_lse else None
         return out, lse, max_blocks
 

@@ -33,7 +33,7 @@ Plan plan_for(int64_t T, int64_t B, int64_t Hq, int64_t Hkv, int64_t MB, int64_t
   Plan p{};
   const int64_t g = Hq / Hkv;
   const bool few = nsel > 0 ? T < 64 * B || T * Hkv < 2048 : T * std::min<int64_t>(g, 16) <= 16 * B;
-  p.rows = few ? msa::kAttnRows : nsel > 0 ? 256 : 128;
+  p.rows = few ? msa::kAttnRows : 128;
   if (!few && nsel == 0) {
     const int64_t big = (T * std::min<int64_t>(g, 256) + 255) / 256 * Hkv;
     if (T * std::min<int64_t>(g, 256) >= 192 * B && big >= 128) p.rows = 256;
@@ -64,7 +64,7 @@ hipError_t launch(const AttnParams& p, const Plan& plan, int64_t grid, hipStream
     e = p.blocks ? msa::launch_kernel(msa::attn_rows_kernel<KK, true>, gr, dim3(256), s, p)
                  : msa::launch_kernel(msa::attn_rows_kernel<KK, false>, gr, dim3(256), s, p);
   else if (p.blocks)
-    e = msa::launch_kernel(msa::attn_tile_kernel<KK, 8, true>, gr, dim3(512), s, p);
+    e = msa::launch_kernel(msa::attn_tile_kernel<KK, 4, true>, gr, dim3(256), s, p);
   else if (plan.rows == 256)
     e = msa::launch_kernel(msa::attn_tile_kernel<KK, 8, false>, gr, dim3(512), s, p);
   else

@@ -177,9 +177,6 @@ __device__ __forceinline__ void copy_rows(uint8_t* dst, const uint8_t* src, int 
   for (int i = 0; i < NI; ++i) buffer_copy16_lds(rs, dst + 1024 * i, of[i]);
 }
 
-constexpr int kSelBits = 131072;       // (token, block) marks of a workgroup
-constexpr int kSelSpan = 4096;         // blocks marked at a time, at most
-
 // ---------------------------------------------------------------------------
 // Few rows: 16 rows a tile, the keys split over waves and workgroups.
 //
@@ -582,6 +579,8 @@ template <int KK, int NW, bool SEL>
 __global__ __launch_bounds__(64 * NW, 2) void attn_tile_kernel(AttnParams p) {
   constexpr int SB = kTileKeys * 256;          // bytes of a stage's K (or V) rows
   constexpr int NI = SB / 1024 / NW;           // copies of each per wave and stage
+  constexpr int kSelBits = 16384 * NW;         // (token, block) marks of a workgroup
+  constexpr int kSelSpan = 512 * NW;           // blocks marked at a time, at most
   // One LDS object, cut up by hand: with several, the compiler attaches alias
   // scopes to the copies into the ring and then waits for them before every
   // read of it.
