@@ -447,9 +447,11 @@ class CacheItem(NamedTuple):
 # msa_tensor_t packed by hand (data, dtype, ndim, shape[4], stride[4]): a step
 # of small calls is bound by the host, and filling a ctypes structure field by
 # field costs several times as much as packing its bytes
-_PACK = {n: struct.Struct("<Qii%dq%dx%dq%dx" % (n, 32 - 8 * n, n, 32 - 8 * n))
-         for n in range(1, 5)}
-_ITEM_TAIL = struct.Struct("<Qii")       # scale, layout, rotate of msa_append_item_t
+_FIELDS = {n: "Qii%dq%dx%dq%dx" % (n, 32 - 8 * n, n, 32 - 8 * n) for n in range(1, 5)}
+_PACK = {n: struct.Struct("<" + f).pack for n, f in _FIELDS.items()}
+# msa_append_item_t: src, dst, scale, layout, rotate
+_PACK_ITEM = {(i, j): struct.Struct("<" + f + g + "Qii").pack
+              for i, f in _FIELDS.items() for j, g in _FIELDS.items()}
 
 
 def _packed(t: torch.Tensor) -> bytes:
@@ -457,7 +459,7 @@ def _packed(t: torch.Tensor) -> bytes:
     n = len(shape)
     if not 1 <= n <= 4:
         raise ValueError(f"a tensor of {n} axes: 1 to 4 are taken")
-    return _PACK[n].pack(t.data_ptr(), DTYPE_CODE.get(t.dtype, -1), n, *shape, *t.stride())
+    return _PACK[n](t.data_ptr(), DTYPE_CODE.get(t.dtype, -1), n, *shape, *t.stride())
 
 
 def _address(t: Optional[torch.Tensor]):
@@ -507,9 +509,12 @@ def _guard(index: int):
 _NO_GUARD = contextlib.nullcontext()
 
 
+_ITEM_LAYOUT = {**LAYOUT_CODE, "ROWS": ROWS}
+
+
 def _item_layout(layout) -> int:
     if isinstance(layout, str):
-        return ROWS if layout.upper() == "ROWS" else LAYOUT_CODE.get(layout.upper(), -1)
+        return _ITEM_LAYOUT.get(layout.upper(), -1)
     return int(layout)
 
 
@@ -545,9 +550,11 @@ def msa_cache_append(items: Sequence[CacheItem], cos: Optional[torch.Tensor],
         positions, rotary = cos.shape[0], 2 * cos.shape[1]
     elif cos is not None or sin is not None or any(it[4] for it in items):
         raise ValueError("rotated items need both cos and sin")
-    packed = []
+    packed, code = [], DTYPE_CODE.get
     for i, (src, dst, layout, scale, rotate) in enumerate(items):
-        lay = _item_layout(layout)
+        lay = _ITEM_LAYOUT.get(layout)
+        if lay is None:
+            lay = _item_layout(layout)
         if src.get_device() != index or dst.get_device() != index:
             raise ValueError(f"item {i}: src is on {src.device}, dst on {dst.device}")
         if lay in (1, 2) and not paged:
@@ -563,7 +570,13 @@ def msa_cache_append(items: Sequence[CacheItem], cos: Optional[torch.Tensor],
                                  f"elements beside dst, got {scale.dtype} "
                                  f"{tuple(scale.shape)} on {scale.device}")
             at = scale.data_ptr()
-        packed += (_packed(src), _packed(dst), _ITEM_TAIL.pack(at, lay, 1 if rotate else 0))
+        m, n = len(src.shape), len(dst.shape)
+        if not (1 <= m <= 4 and 1 <= n <= 4):
+            raise ValueError(f"item {i}: src has {m} axes, dst {n}: 1 to 4 are taken")
+        packed.append(_PACK_ITEM[m, n](
+            src.data_ptr(), code(src.dtype, -1), m, *src.shape, *src.stride(),
+            dst.data_ptr(), code(dst.dtype, -1), n, *dst.shape, *dst.stride(),
+            at, lay, 1 if rotate else 0))
     handle = _stream_handle(stream, index)
     with _guard(index):
         st = lib.msa_cache_append(b"".join(packed), len(items), _address(cos), _address(sin),
@@ -676,25 +689,22 @@ def msa_block_attention(query: torch.Tensor, key: torch.Tensor, value: torch.Ten
                       block_size)
 
 
-def _allocated(query, key, block_table, layout, max_blocks, return_lse, stream):
-    """(out, lse, max_blocks) of a call that leaves them to the binding."""
-    if max_blocks is None:
-        if block_table is not None:
-            max_blocks = block_table.shape[-1]
-        else:
-            max_blocks = (key.shape[0] + 127) // 128   # packed: no more than all keys
+def _outputs(query, return_lse, stream):
+    """out and lse of a call that leaves them to the binding; those of a call on
+    a given stream belong to that stream, as its workspace does."""
+    if stream is not None and query.is_cuda:
+        with torch.cuda.stream(_stream_of(_stream_handle(stream, query.device), query.device)):
+            return _outputs(query, return_lse, None)
+    out = torch.empty_like(query, memory_format=torch.contiguous_format)
+    if not return_lse:
+        return out, None
+    return out, query.new_empty(query.shape[:2], dtype=torch.float32)
 
-    def make():
-        out = torch.empty_like(query, memory_format=torch.contiguous_format)
-        lse = query.new_empty(query.shape[:2], dtype=torch.float32) if return_lse else None
-        return out, lse, max_blocks
 
-    if stream is None or query.device.type != "cuda":
-        return make()
-    # results of a call on a given stream belong to that stream, as its
-    # workspace does
-    with torch.cuda.stream(_stream_of(_stream_handle(stream, query.device), query.device)):
-        return make()
+def _default_blocks(key, block_table) -> int:
+    """max_blocks where the caller leaves it out: the table's width, or as many
+    as all packed keys would fill."""
+    return block_table.shape[-1] if block_table is not None else (key.shape[0] + 127) // 128
 
 
 def attention(query: torch.Tensor, key: torch.Tensor, value: torch.Tensor,
@@ -704,9 +714,11 @@ def attention(query: torch.Tensor, key: torch.Tensor, value: torch.Tensor,
               return_lse: bool = False, stream=None):
     """Allocate ``out`` (and ``lse``) and fill them with ``msa_attention``;
     returns ``out`` or ``(out, lse)``."""
-    out, lse, mb = _allocated(query, key, block_table, layout, max_blocks, return_lse, stream)
-    msa_attention(query, key, value, block_table, cu_seqlens_q, kv_len, layout, sparse_mode,
-                  softmax_scale, out, mb, lse=lse, stream=stream)
+    out, lse = _outputs(query, return_lse, stream)
+    if max_blocks is None:
+        max_blocks = _default_blocks(key, block_table)
+    _attention(query, key, value, None, block_table, cu_seqlens_q, kv_len, layout, sparse_mode,
+               softmax_scale, out, lse, max_blocks, None, stream, BLOCK_SIZE)
     return (out, lse) if return_lse else out
 
 
@@ -717,7 +729,11 @@ def block_attention(query: torch.Tensor, key: torch.Tensor, value: torch.Tensor,
                     max_blocks: Optional[int] = None, return_lse: bool = False, stream=None):
     """Allocate ``out`` (and ``lse``) and fill them with
     ``msa_block_attention``; returns ``out`` or ``(out, lse)``."""
-    out, lse, mb = _allocated(query, key, block_table, layout, max_blocks, return_lse, stream)
-    msa_block_attention(query, key, value, blocks, block_table, cu_seqlens_q, kv_len, layout,
-                        sparse_mode, softmax_scale, out, mb, lse=lse, stream=stream)
+    if blocks is None:
+        raise ValueError("blocks is required")
+    out, lse = _outputs(query, return_lse, stream)
+    if max_blocks is None:
+        max_blocks = _default_blocks(key, block_table)
+    _attention(query, key, value, blocks, block_table, cu_seqlens_q, kv_len, layout, sparse_mode,
+               softmax_scale, out, lse, max_blocks, None, stream, BLOCK_SIZE)
     return (out, lse) if return_lse else out

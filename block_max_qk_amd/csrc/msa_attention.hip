@@ -44,7 +44,7 @@ Plan plan_for(int64_t T, int64_t B, int64_t Hq, int64_t Hkv, int64_t MB, int64_t
   p.ntiles = std::min<int64_t>(T, (T + B * (p.tpt - 1)) / p.tpt);
   const int64_t items = std::max<int64_t>(p.ntiles * Hkv * p.hchunks, 1);
   const int64_t blocks = std::max<int64_t>(few && nsel > 0 ? std::min(nsel, MB) : MB, 1);
-  p.min_blocks = few ? 2 : 4;
+  p.min_blocks = few ? 2 : 8;
   const int64_t want = nsel > 0 && few ? 256 : few ? 1536 : 512;
   int64_t n = items >= want ? 1 : (want + items - 1) / items;
   n = std::min(n, (blocks + p.min_blocks - 1) / p.min_blocks);
