@@ -6,7 +6,7 @@
 // four head rows of one item, 16 lanes to a row and 8 elements to a lane
 // (16-byte loads, whole lines per row).  The step's item is the same for the
 // whole wave, so its type, layout and pointers are scalars and nothing
-// diverges.  The next step's rows are loaded before a step is computed.
+// diverges.  Loads run three steps ahead.
 #pragma once
 
 #include "msa_device.hpp"
@@ -155,23 +155,32 @@ __global__ __launch_bounds__(64 * kAppendWaves) void append_kernel(AppendParams 
   const bool rot_lane = i < 2 * hc;
   const int partner = (l & 48) | (rot_lane ? (i < hc ? i + hc : i - hc) : i);
 
-  // the step's item, and its first head in it
-  int it = 0, first = 0;
-  while (step >= first + p.item[it].steps) first += p.item[it++].steps;
-  auto load = [&](int item, int st) -> i32x4 {
-    const AppendItem& a = p.item[item];
-    const int h = 4 * st + rr;
-    if (h >= a.heads) return i32x4{0, 0, 0, 0};
-    return ld16(a.src + t * a.src_row + (int64_t)h * a.src_head + 16 * i);
+  // a step's item and its first step: kept once for the step at work and once
+  // for the loads, which run DEPTH steps ahead
+  constexpr int DEPTH = 3;
+  struct Place { int item, first; };
+  auto move_to = [&](Place& at, int st) {
+    while (st >= at.first + p.item[at.item].steps) at.first += p.item[at.item++].steps;
   };
-  i32x4 next = load(it, step - first);
+  Place at{0, 0}, ahead{0, 0};
+  auto load = [&](int st) -> i32x4 {
+    const i32x4 none = {0, 0, 0, 0};
+    if (st >= step_end) return none;
+    move_to(ahead, st);
+    const AppendItem& a = p.item[ahead.item];
+    const int h = 4 * (st - ahead.first) + rr;
+    return h < a.heads ? ld16(a.src + t * a.src_row + (int64_t)h * a.src_head + 16 * i) : none;
+  };
+  i32x4 next[DEPTH];
+#pragma unroll
+  for (int k = 0; k < DEPTH; ++k) next[k] = load(step + k);
   for (; step < step_end; ++step) {
-    const int cur = it, st = step - first;
-    i32x4 raw = next;
-    if (step + 1 < step_end) {
-      while (step + 1 >= first + p.item[it].steps) first += p.item[it++].steps;
-      next = load(it, step + 1 - first);
-    }
+    move_to(at, step);
+    const int cur = at.item, st = step - at.first;
+    i32x4 raw = next[0];
+#pragma unroll
+    for (int k = 0; k + 1 < DEPTH; ++k) next[k] = next[k + 1];
+    next[DEPTH - 1] = load(step + DEPTH);
     const AppendItem& a = p.item[cur];
     const int h = 4 * st + rr;
     int64_t off, soff;
@@ -266,15 +275,15 @@ __global__ __launch_bounds__(64 * kAppendWaves) void append_kernel(AppendParams 
       if (ok) *reinterpret_cast<int2*>(dst + 8 * i) = int2{w[0], w[1]};
       continue;
     }
-    double top = 0.0;
-    bool odd = false;                  // an infinity or NaN
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const double m = fabs(y[k]);
-      odd = odd || !(m < __builtin_inf());
-      top = fmax(top, m);
-    }
     if (a.kind == KI8) {
+      double top = 0.0;
+      bool odd = false;                // an infinity or NaN
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const double m = fabs(y[k]);
+        odd = odd || !(m < __builtin_inf());
+        top = fmax(top, m);
+      }
       odd = lanes_any<16>(odd);
       top = lanes_max<16>(top);
       const float sc = (float)(top / 127.0);
@@ -292,11 +301,22 @@ __global__ __launch_bounds__(64 * kAppendWaves) void append_kernel(AppendParams 
       }
       continue;
     }
-    // MXFP4: groups of 32 elements are 4 lanes
-    odd = lanes_any<4>(odd);
-    top = lanes_max<4>(top);
-    const int ex = (int)((__builtin_bit_cast(uint64_t, top) >> 52) & 2047) - 1023;
-    const int e8 = top == 0.0 ? 0 : min(max(ex - 2 + 127, 0), 254);
+    // MXFP4: groups of 32 elements are 4 lanes.  In integer steps on the
+    // float64's bits but for one addition: floor(log2) of the group's largest
+    // magnitude is the exponent field of the largest high word, dividing by
+    // the power of two lowers the exponent field, and adding 1.5 * 2^52 steps
+    // of the E2M1 grid leaves the value's steps, rounded to nearest even, in the
+    // low bits.
+    uint32_t hi[8], top = 0;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      hi[k] = (uint32_t)(__builtin_bit_cast(uint64_t, y[k]) >> 32);
+      top = max(top, hi[k] & 0x7FFFFFFFu);
+    }
+    top = max(top, (uint32_t)__shfl_xor((int)top, 1));
+    top = max(top, (uint32_t)__shfl_xor((int)top, 2));
+    const bool odd = top >= 0x7FF00000u;
+    const int e8 = top == 0 ? 0 : min(max((int)(top >> 20) - 1023 - 2 + 127, 0), 254);
     const double inv = __builtin_bit_cast(double, (uint64_t)(127 - e8 + 1023) << 52);
     uint32_t w = 0;
     if (!odd) {
@@ -304,9 +324,13 @@ __global__ __launch_bounds__(64 * kAppendWaves) void append_kernel(AppendParams 
       for (int k = 0; k < 8; ++k) {
         // E2M1: steps of 1/2 below 2, 1 below 4, 2 above; codes 0..4, 4..6, 6..7
         const double m = fabs(y[k]) * inv;
-        const double r = m < 2.0 ? rint(2.0 * m) : m < 4.0 ? rint(m) + 2.0 : rint(0.5 * m) + 4.0;
-        uint32_t code = (uint32_t)(int)fmin(r, 7.0);
-        if (code && y[k] < 0.0) code |= 8;
+        const uint32_t mh = (uint32_t)(__builtin_bit_cast(uint64_t, m) >> 32);
+        const int seg = mh < 0x40000000u ? 0 : mh < 0x40100000u ? 1 : 2;   // below 2, below 4
+        // 1.5 * 2^52 * (1/2, 1, 2)
+        const double grid = __builtin_bit_cast(double, (uint64_t)(0x43280000u + (seg << 20)) << 32);
+        const uint32_t r = (uint32_t)__builtin_bit_cast(uint64_t, m + grid);
+        uint32_t code = min((r & 15u) + 2 * seg, 7u);
+        if (code) code |= (hi[k] >> 28) & 8u;
         w |= code << (4 * k);
       }
     }

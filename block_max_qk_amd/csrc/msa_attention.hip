@@ -22,30 +22,47 @@ struct Plan {
   int hpt, tpt, hchunks;
   int64_t ntiles;
   int nsplit, min_blocks;
+  bool once;         // no two workgroups read the same rows of keys
 };
 
-// Tiles of 16 rows when the requests' new tokens fill no more on average (or
-// each token has blocks of its own); else 128 rows, or 256 where the batch
-// holds enough of them.  Few tiles are split over the keys until the parts
-// cover the chip's 256 CUs several times; a part takes at least min_blocks
-// blocks, whatever the table's width.
+// The tile and the split, from the sizes alone.
+//
+// Dense: tiles of 16 rows where the requests' new tokens fill no more on
+// average, 128 rows otherwise, and 256 where requests average three quarters
+// of that and there are 128 such tiles (2048 tokens over 32768 keys, 8 heads a
+// group: 911 us with 256 rows, 951 with 128, 3130 with 16; 9 requests of 2 to
+// 258 tokens: 84, 75 and 163 us).
+// Selected blocks: one workgroup per token and KV head (16 rows), or tiles of
+// 128 rows that walk the union of their tokens' blocks once tokens can share
+// them and fill the chip (16 blocks of 16000 keys, 4 KV heads: 60 tokens 21 us
+// against 34, 200 tokens 67 against 52, 1600 tokens 411 against 168; 64
+// requests of 2 tokens 83 against 79).
+//
+// Few tiles are split over the keys until there are about `want` parts, of
+// min_blocks blocks at least; a split pays a second kernel and the traffic of
+// its partial sums.  (64 requests x 8 KV heads, up to 64 blocks: 199 us in
+// 1536 parts, 208 in 1024, 221 unsplit; 64 x 4 with 16 selected blocks: 44 us
+// unsplit, 52 in two parts; 512 tokens over 8000 keys, 128 rows: 87 us in 512
+// parts, 96 in 256, 149 unsplit; one prompt of 1000 tokens: 27 us unsplit, 39
+// in two parts of 4 blocks.)
 Plan plan_for(int64_t T, int64_t B, int64_t Hq, int64_t Hkv, int64_t MB, int64_t nsel) {
   Plan p{};
   const int64_t g = Hq / Hkv;
-  const bool few = nsel > 0 ? T < 64 * B || T * Hkv < 2048 : T * std::min<int64_t>(g, 16) <= 16 * B;
+  const bool few = nsel > 0 ? T < 8 * B || T * Hkv < 640 : T * std::min<int64_t>(g, 16) <= 16 * B;
   p.rows = few ? msa::kAttnRows : 128;
   if (!few && nsel == 0) {
-    const int64_t big = (T * std::min<int64_t>(g, 256) + 255) / 256 * Hkv;
-    if (T * std::min<int64_t>(g, 256) >= 192 * B && big >= 128) p.rows = 256;
+    const int64_t rows = T * std::min<int64_t>(g, 256);
+    if (rows >= 192 * B && (rows + 255) / 256 * Hkv >= 128) p.rows = 256;
   }
   p.hpt = (int)std::min<int64_t>(g, p.rows);
   p.tpt = few && nsel > 0 ? 1 : p.rows / p.hpt;
   p.hchunks = (int)((g + p.hpt - 1) / p.hpt);
   p.ntiles = std::min<int64_t>(T, (T + B * (p.tpt - 1)) / p.tpt);
+  p.once = p.hchunks == 1 && (nsel == 0 || T <= 2 * B);
   const int64_t items = std::max<int64_t>(p.ntiles * Hkv * p.hchunks, 1);
   const int64_t blocks = std::max<int64_t>(few && nsel > 0 ? std::min(nsel, MB) : MB, 1);
   p.min_blocks = few ? 2 : 8;
-  const int64_t want = nsel > 0 && few ? 256 : few ? 1536 : 512;
+  const int64_t want = !few ? 512 : nsel > 0 ? 128 : 1536;
   int64_t n = items >= want ? 1 : (want + items - 1) / items;
   n = std::min(n, (blocks + p.min_blocks - 1) / p.min_blocks);
   p.nsplit = (int)std::max<int64_t>(1, std::min(n, kMaxSplit));
@@ -60,15 +77,19 @@ template <int KK>
 hipError_t launch(const AttnParams& p, const Plan& plan, int64_t grid, hipStream_t s) {
   hipError_t e;
   const dim3 gr((unsigned)grid);
-  if (plan.rows == msa::kAttnRows)
-    e = p.blocks ? msa::launch_kernel(msa::attn_rows_kernel<KK, true>, gr, dim3(256), s, p)
-                 : msa::launch_kernel(msa::attn_rows_kernel<KK, false>, gr, dim3(256), s, p);
-  else if (p.blocks)
+  if (plan.rows == msa::kAttnRows) {
+    auto kern = p.blocks ? (plan.once ? msa::attn_rows_kernel<KK, true, true>
+                                      : msa::attn_rows_kernel<KK, true, false>)
+                         : (plan.once ? msa::attn_rows_kernel<KK, false, true>
+                                      : msa::attn_rows_kernel<KK, false, false>);
+    e = msa::launch_kernel(kern, gr, dim3(256), s, p);
+  } else if (p.blocks) {
     e = msa::launch_kernel(msa::attn_tile_kernel<KK, 4, true>, gr, dim3(256), s, p);
-  else if (plan.rows == 256)
+  } else if (plan.rows == 256) {
     e = msa::launch_kernel(msa::attn_tile_kernel<KK, 8, false>, gr, dim3(512), s, p);
-  else
+  } else {
     e = msa::launch_kernel(msa::attn_tile_kernel<KK, 4, false>, gr, dim3(256), s, p);
+  }
   if (e == hipSuccess && p.nsplit > 1)
     e = msa::launch_kernel(msa::attn_join_kernel<KK>, dim3((unsigned)((p.T * p.Hq + 3) / 4)),
                            dim3(256), s, p);

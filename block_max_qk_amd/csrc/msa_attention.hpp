@@ -167,14 +167,17 @@ __device__ __forceinline__ void landed(i32x4& x) { asm volatile("" : "+v"(x)); }
 constexpr float kMaxLag = 8.f;
 
 // NI copies of 1 KB, a wave's lanes' pieces at the byte offsets `of` of a raw
-// buffer of `bytes`.
-template <int NI>
+// buffer of `bytes`; ONCE: rows that nobody else reads (the nontemporal hint).
+template <int NI, bool ONCE = false>
 __device__ __forceinline__ void copy_rows(uint8_t* dst, const uint8_t* src, int bytes,
                                           const uint32_t* of) {
   const __amdgpu_buffer_rsrc_t rs =
       __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(src), 0, bytes, kBufferWord3);
 #pragma unroll
-  for (int i = 0; i < NI; ++i) buffer_copy16_lds(rs, dst + 1024 * i, of[i]);
+  for (int i = 0; i < NI; ++i)
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(
+        rs, (__attribute__((address_space(3))) void*)(dst + 1024 * i), 16, of[i], 0, 0,
+        ONCE ? 2 : 0);
 }
 
 // ---------------------------------------------------------------------------
@@ -187,13 +190,17 @@ __device__ __forceinline__ void copy_rows(uint8_t* dst, const uint8_t* src, int 
 // four waves' results are joined through LDS at the end.  The bound is the
 // reading of keys and values: each wave copies its 16 KB of a block straight
 // into its own part of the LDS, one block ahead, with no barrier in the loop.
+// ONCE: no other workgroup reads the same rows, and the copies say so (64
+// requests of up to 8192 keys, 8 KV heads: 219 us without the hint, 199 with
+// it, 1.17 GB; where tokens share their selected blocks the hint costs as much
+// as it gains here).  Stages of 16 keys with two workgroups a CU instead: 207 us.
 // ---------------------------------------------------------------------------
 
 constexpr int kAttnRows = 16;
 constexpr int kRowWaves = 4;
 constexpr int kRowStage = 16384;     // 32 keys' K and V rows
 
-template <int KK, bool SEL>
+template <int KK, bool SEL, bool ONCE>
 __global__ __launch_bounds__(256, 1) void attn_rows_kernel(AttnParams p) {
   __shared__ __attribute__((aligned(16))) uint8_t ring[kRowWaves][2][kRowStage];
   const int item = blockIdx.x;
@@ -325,8 +332,8 @@ __global__ __launch_bounds__(256, 1) void attn_rows_kernel(AttnParams p) {
                   const Rows& next, bool more, auto careful) __attribute__((always_inline)) {
     if constexpr (!decltype(careful)::value) {
       if (more) {
-        copy_rows<8>(dst, next.k, next.n * p.k_row_stride, kof);
-        copy_rows<8>(dst + 8192, next.v, next.n * p.v_row_stride, vof);
+        copy_rows<8, ONCE>(dst, next.k, next.n * p.k_row_stride, kof);
+        copy_rows<8, ONCE>(dst + 8192, next.v, next.n * p.v_row_stride, vof);
         asm volatile("s_waitcnt vmcnt(16)" ::: "memory");
       } else {
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
@@ -414,8 +421,8 @@ __global__ __launch_bounds__(256, 1) void attn_rows_kernel(AttnParams p) {
     Block cur = block_at(0);
     Rows r = rows_of(cur);
     if constexpr (!decltype(careful)::value) {
-      copy_rows<8>(mine, r.k, r.n * p.k_row_stride, kof);
-      copy_rows<8>(mine + 8192, r.v, r.n * p.v_row_stride, vof);
+      copy_rows<8, ONCE>(mine, r.k, r.n * p.k_row_stride, kof);
+      copy_rows<8, ONCE>(mine + 8192, r.v, r.n * p.v_row_stride, vof);
     }
     for (int s = 0; s < nst; ++s) {
       Block next = cur;
