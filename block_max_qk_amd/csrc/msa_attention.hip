@@ -18,7 +18,8 @@ using msa::AttnParams;
 constexpr int64_t kMaxSplit = 64;      // one lane per part in the join
 
 struct Plan {
-  int rows;          // rows per tile: 16 (attn_rows_kernel), 128 or 256 (attn_tile_kernel)
+  int rows;          // rows per tile: 16 (attn_rows_kernel), 128 or 256 (attn_tile_kernel;
+                     // 128 with selected blocks: attn_union_kernel)
   int hpt, tpt, hchunks;
   int64_t ntiles;
   int nsplit, min_blocks;
@@ -35,16 +36,18 @@ struct Plan {
 // Selected blocks: one workgroup per token and KV head (16 rows), or tiles of
 // 128 rows that walk the union of their tokens' blocks once tokens can share
 // them and fill the chip (16 blocks of 16000 keys, 4 KV heads: 60 tokens 21 us
-// against 34, 200 tokens 67 against 52, 1600 tokens 411 against 168; 64
-// requests of 2 tokens 83 against 79).
+// against 43, 200 tokens 69 against 60, 1600 tokens 411 against 152; 64
+// requests of 2 tokens 85 against 89).
 //
 // Few tiles are split over the keys until there are about `want` parts, of
 // min_blocks blocks at least; a split pays a second kernel and the traffic of
 // its partial sums.  (64 requests x 8 KV heads, up to 64 blocks: 199 us in
 // 1536 parts, 208 in 1024, 221 unsplit; 64 x 4 with 16 selected blocks: 44 us
 // unsplit, 52 in two parts; 512 tokens over 8000 keys, 128 rows: 87 us in 512
-// parts, 96 in 256, 149 unsplit; one prompt of 1000 tokens: 27 us unsplit, 39
-// in two parts of 4 blocks.)
+// parts, 96 in 256, 149 unsplit; 256 rows, 1024 tokens over 16000 keys: 264 us in
+// 256 parts, 272 in 512; 800 tokens over selected blocks: 99 us in 256 parts,
+// 114 in 512; one prompt of 1000 tokens: 27 us unsplit, 39 in two parts of 4
+// blocks.)
 Plan plan_for(int64_t T, int64_t B, int64_t Hq, int64_t Hkv, int64_t MB, int64_t nsel) {
   Plan p{};
   const int64_t g = Hq / Hkv;
@@ -62,7 +65,7 @@ Plan plan_for(int64_t T, int64_t B, int64_t Hq, int64_t Hkv, int64_t MB, int64_t
   const int64_t items = std::max<int64_t>(p.ntiles * Hkv * p.hchunks, 1);
   const int64_t blocks = std::max<int64_t>(few && nsel > 0 ? std::min(nsel, MB) : MB, 1);
   p.min_blocks = few ? 2 : 8;
-  const int64_t want = !few ? 512 : nsel > 0 ? 128 : 1536;
+  const int64_t want = nsel > 0 ? (few ? 128 : 256) : few ? 1536 : p.rows == 128 ? 512 : 256;
   int64_t n = items >= want ? 1 : (want + items - 1) / items;
   n = std::min(n, (blocks + p.min_blocks - 1) / p.min_blocks);
   p.nsplit = (int)std::max<int64_t>(1, std::min(n, kMaxSplit));
@@ -84,11 +87,11 @@ hipError_t launch(const AttnParams& p, const Plan& plan, int64_t grid, hipStream
                                       : msa::attn_rows_kernel<KK, false, false>);
     e = msa::launch_kernel(kern, gr, dim3(256), s, p);
   } else if (p.blocks) {
-    e = msa::launch_kernel(msa::attn_tile_kernel<KK, 4, true>, gr, dim3(256), s, p);
+    e = msa::launch_kernel(msa::attn_union_kernel<KK, 8>, gr, dim3(512), s, p);
   } else if (plan.rows == 256) {
-    e = msa::launch_kernel(msa::attn_tile_kernel<KK, 8, false>, gr, dim3(512), s, p);
+    e = msa::launch_kernel(msa::attn_tile_kernel<KK, 8>, gr, dim3(512), s, p);
   } else {
-    e = msa::launch_kernel(msa::attn_tile_kernel<KK, 4, false>, gr, dim3(256), s, p);
+    e = msa::launch_kernel(msa::attn_tile_kernel<KK, 4>, gr, dim3(256), s, p);
   }
   if (e == hipSuccess && p.nsplit > 1)
     e = msa::launch_kernel(msa::attn_join_kernel<KK>, dim3((unsigned)((p.T * p.Hq + 3) / 4)),
@@ -154,7 +157,11 @@ msa_status_t run(const msa_tensor_t* query, const msa_tensor_t* key, const msa_t
   const Plan plan = plan_for(T, batch, Hq, Hkv, max_blocks, selected ? num_blocks : 0);
   const int64_t need = workspace_for(plan, T, Hq);
   if (need > 0 && (!workspace || workspace_bytes < need)) return MSA_ERR_WORKSPACE;
-  const int64_t grid = plan.ntiles * Hkv * plan.hchunks * plan.nsplit;
+  int64_t grid = plan.ntiles * Hkv * plan.hchunks * plan.nsplit;
+  if (selected && plan.rows != msa::kAttnRows) {   // runs of 8 tiles, 8 runs at a time
+    const int64_t runs = (plan.ntiles + 7) / 8 * Hkv * plan.hchunks;
+    grid = (runs + 7) / 8 * 64 * plan.nsplit;
+  }
   if (grid > INT32_MAX || T * Hq > (int64_t)INT32_MAX * 4) return MSA_ERR_SHAPE;
 
   AttnParams p{};

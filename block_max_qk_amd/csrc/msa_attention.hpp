@@ -560,44 +560,30 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnParams p) {
 // Many rows: 32 rows a wave, NW waves a workgroup, every wave reading the same
 // stages of 64 keys from the LDS.
 //
-// The stages' K and V rows are copied straight into a two-deep LDS ring one
+// The stages' K and V rows are copied straight into two-deep LDS rings one
 // stage ahead, through raw buffers that end at the tile's last visible key, so
 // rows past it read zeros (a stored NaN there cannot reach a sum).
-//
-// With selected blocks (SEL) the tile's tokens have lists of their own.  The
-// workgroup walks the union of its tokens' blocks in ascending order: a block
-// is copied once for all of them, a wave none of whose tokens selected it
-// skips its products, and a row of another token gets weight 0.  The bound of
-// one workgroup per token is the copying (64 KB per token, KV head and
-// selected block out of the L2); neighbouring tokens share most of their
-// blocks, and even unrelated lists share them once the tile's tokens name
-// more blocks than there are.
 //
 // A weight of 0 does not hide an infinity or NaN in the value of a key that
 // only other rows of the tile see.  So a tile that ends with an accumulator
 // that is not finite is taken again with the second product formed token by
-// token, from values with the unseen rows cleared (CAREFUL); a tile of finite
+// token, from values with the unseen rows cleared (careful); a tile of finite
 // inputs costs only the look at its accumulators.
 // ---------------------------------------------------------------------------
 
 constexpr int kTileKeys = 64;
 
-template <int KK, int NW, bool SEL>
+template <int KK, int NW>
 __global__ __launch_bounds__(64 * NW, 2) void attn_tile_kernel(AttnParams p) {
   constexpr int SB = kTileKeys * 256;          // bytes of a stage's K (or V) rows
   constexpr int NI = SB / 1024 / NW;           // copies of each per wave and stage
-  constexpr int kSelBits = 16384 * NW;         // (token, block) marks of a workgroup
-  constexpr int kSelSpan = 512 * NW;           // blocks marked at a time, at most
   // One LDS object, cut up by hand: with several, the compiler attaches alias
   // scopes to the copies into the ring and then waits for them before every
   // read of it.
-  constexpr int kMarksAt = 4 * SB, kNamedAt = kMarksAt + (SEL ? kSelBits / 8 : 0);
-  constexpr int kFlagAt = kNamedAt + (SEL ? 2 * kSelSpan : 0);
+  constexpr int kFlagAt = 4 * SB;
   __shared__ __attribute__((aligned(16))) uint8_t lds[kFlagAt + 16];
   uint8_t* const kring = lds;                                       // [2][64 K rows]
   uint8_t* const vring = lds + 2 * SB;                              // [2][64 V rows]
-  uint32_t* const marks = reinterpret_cast<uint32_t*>(lds + kMarksAt);   // [token][block of the span]
-  uint16_t* const named = reinterpret_cast<uint16_t*>(lds + kNamedAt);   // the span's blocks, ascending
   int* const flag = reinterpret_cast<int*>(lds + kFlagAt);
   // heavy tiles (the last tokens of a request see the most keys) first; the
   // KV head changes fastest, so that with 8 XCDs taking workgroups in turn an
@@ -608,7 +594,8 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tile_kernel(AttnParams p) {
   const int hc = rest % p.hchunks;
   rest /= p.hchunks;
   const int hk = rest % p.Hkv;
-  const AttnTile w = attn_tile(p, p.ntiles - 1 - rest / p.Hkv);
+  const int tile = p.ntiles - 1 - rest / p.Hkv;
+  const AttnTile w = attn_tile(p, tile);
   if (!w.valid) return;
 
   const int tid = threadIdx.x;
@@ -636,14 +623,12 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tile_kernel(AttnParams p) {
     for (int s = 0; s < 8; ++s) qv[s] = ld16(qr + 16 * (2 * s + h));
   }
 
-  // The blocks come as a list of `count` entries: the part's own ones in
-  // order, or a span's marked ones.  Their numbers (kNoPage: on no page) and
-  // the places of their rows are held one per lane, 64 entries at a time, so
+  // The part's blocks: their numbers (kNoPage: on no page) and the places of
+  // their rows are held one per lane, 64 at a time, so
   // that a stage takes a few readlanes and no address arithmetic (scalar
   // multiplications per stage held up every wave for hundreds of cycles).
   constexpr int kNoPage = 1 << 30;
-  int base = b0, count = b1 - b0;
-  const int span = SEL ? min(kSelSpan, kSelBits / p.tpt & ~31) : 0;
+  const int count = b1 - b0;
   int bidx = 0, pbase = 0;
   int64_t kat = 0, vat = 0;
   auto load_entries = [&](int from) {
@@ -651,8 +636,7 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tile_kernel(AttnParams p) {
     bidx = kNoPage;
     kat = vat = 0;
     if (from + l < count) {
-      bidx = base + from + l;
-      if constexpr (SEL) bidx = base + named[from + l];
+      bidx = b0 + from + l;
       if (p.paged) {
         const int pg = p.block_table[(int64_t)w.b * p.MB + bidx];
         if (pg >= 0 && pg < p.NP) {
@@ -713,9 +697,9 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tile_kernel(AttnParams p) {
   float m, lsum;
 
   // A stage in two parts: its scores from the K rows at kt, and what follows
-  // from them with the V rows at vt.  `mine`: this lane's row's token selected
-  // the block.  (The copies that may be in flight go to other parts of the
-  // rings, and the parameters say so, as in attn_rows_kernel.)
+  // from them with the V rows at vt.  (The copies that may be in flight go to
+  // other parts of the rings, and the parameters say so, as in
+  // attn_rows_kernel.)
   f32x16 st[2];
   auto scores = [&](const uint8_t* __restrict kt) __attribute__((always_inline)) {
     // S^T, two tiles of 32 keys: register r of tile t is key
@@ -740,7 +724,7 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tile_kernel(AttnParams p) {
       __builtin_amdgcn_sched_barrier(0);
     }
   };
-  auto absorb = [&](const uint8_t* __restrict vt, const Entry& cur, int in, bool mine, auto careful)
+  auto absorb = [&](const uint8_t* __restrict vt, const Entry& cur, int in, auto careful)
       __attribute__((always_inline)) {
     const int j0 = cur.beta * kP + in * kTileKeys;
     const bool there = cur.there;
@@ -760,7 +744,6 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tile_kernel(AttnParams p) {
 #pragma unroll
       for (int r = 0; r < 16; ++r) mx = fmaxf(mx, st[t][r]);
     mx = max_xor32(mx) * p.c;
-    if constexpr (SEL) mx = mine ? mx : -__builtin_inff();
     if (__ballot(mx > m + kMaxLag)) {
       const float mn = mx > m + kMaxLag ? mx : m;
       const float alpha = exp2_hw(m - (mn == -__builtin_inff() ? 0.f : mn));
@@ -777,8 +760,7 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tile_kernel(AttnParams p) {
       const float a = exp2_hw(__builtin_fmaf(st[i >> 3][2 * (i & 7)], p.c, -ms));
       const float b = exp2_hw(__builtin_fmaf(st[i >> 3][2 * (i & 7) + 1], p.c, -ms));
       add += a + b;
-      const int pk = pack2<KK>(a, b);
-      pf[i >> 2][i & 3] = !SEL || mine ? pk : 0;
+      pf[i >> 2][i & 3] = pack2<KK>(a, b);
     };
     // O^T += V^T P^T, 16 keys a step: registers 8 u .. 8 u + 7 of a tile are
     // keys 16 u + 4 h + {0..3} and 16 u + 8 + 4 h + {0..3}
@@ -807,17 +789,16 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tile_kernel(AttnParams p) {
         if (i < 12) weigh(i + 4);
         __builtin_amdgcn_sched_barrier(0);
       }
-      lsum += !SEL || mine ? add : 0.f;
+      lsum += add;
     } else {
       // token by token: the values of keys that it does not see cleared, its
       // rows' sums kept
 #pragma unroll
       for (int i = 0; i < 16; ++i) weigh(i);
-      lsum += !SEL || mine ? add : 0.f;
+      lsum += add;
       const int first = wave * 32 / p.hpt, last = min((wave * 32 + 31) / p.hpt, w.ntok - 1);
       for (int tk = first; tk <= last; ++tk) {
-        const unsigned long long its = __ballot(row_ok && ti == tk && mine);
-        if (!its) continue;
+        if (!__ballot(row_ok && ti == tk)) continue;
         const int end = attn_last(p, w, w.i0 + tk);
 #pragma unroll
         for (int d = 0; d < 4; ++d) {
@@ -839,16 +820,379 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tile_kernel(AttnParams p) {
     }
   };
 
+  // the stages, two per block
+  auto walk = [&](auto careful) __attribute__((always_inline)) {
+    if (count <= 0) return;
+    load_entries(0);
+    if constexpr (decltype(careful)::value) {
+      for (int s = 0; s < 2 * count; ++s) {
+        const Entry x = entry_at(s >> 1);
+        __syncthreads();
+        copy_plain(x, s & 1);
+        __syncthreads();
+        scores(kring);
+        absorb(vring, x, s & 1, careful);
+      }
+      return;
+    }
+    Entry x = entry_at(0);
+    Rows r = rows_of(x, 0);
+    // one half of an entry: the copies of the next into `kd` and `vd`, then its
+    // own work on the rows at kt and vt
+    auto half = [&](const uint8_t* __restrict kt, const uint8_t* __restrict vt,
+                    uint8_t* __restrict kd, uint8_t* __restrict vd, int in)
+        __attribute__((always_inline)) {
+      copy_rows<NI>(kd + wave * NI * 1024, r.k, r.kb, kof);
+      copy_rows<NI>(vd + wave * NI * 1024, r.v, r.vb, vof);
+      scores(kt);
+      absorb(vt, x, in, careful);
+    };
+    copy_rows<NI>(kring + wave * NI * 1024, r.k, r.kb, kof);
+    copy_rows<NI>(vring + wave * NI * 1024, r.v, r.vb, vof);
+    for (int e = 0; e < count; ++e) {
+      // at each half: this wave's copies of the stage have landed; after the
+      // barrier everyone's have, and everyone has read the stage before
+      r = rows_of(x, 1);
+      asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+      half(kring, vring, kring + SB, vring + SB, 0);
+      Entry xn = x;
+      if (e + 1 < count) {
+        xn = entry_at(e + 1);
+        r = rows_of(xn, 0);
+      } else {
+        r.kb = r.vb = 0;       // (nothing is read: the last copies bring zeros)
+      }
+      asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+      half(kring + SB, vring + SB, kring, vring, 1);
+      x = xn;
+    }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  };
+
+  auto pass = [&](auto careful) __attribute__((always_inline)) {
+#pragma unroll
+    for (int d = 0; d < 4; ++d) o[d] = f32x16{};
+    m = -__builtin_inff();
+    lsum = 0.f;
+    walk(careful);
+  };
+
+#pragma unroll
+  for (int s = 0; s < 8; ++s) landed(qv[s]);
+  pass(std::false_type{});
+  if (w.ntok > 1) {
+    // (x - x is 0 for a finite x only; the products add no rounding of their own)
+    float odd = 0.f;
+#pragma unroll
+    for (int d = 0; d < 4; ++d)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) odd += o[d][r] - o[d][r];
+    __syncthreads();
+    if (tid == 0) *flag = 0;
+    __syncthreads();
+    if (row_ok && odd != 0.f) *flag = 1;
+    __syncthreads();
+    if (*flag) pass(std::true_type{});
+  }
+
+  lsum = sum_xor32(lsum);
+  if (!row_ok) return;
+  const int64_t out_row = ((int64_t)(w.t0 + ti) * p.Hq + hk * p.g + hg);
+  // register r of o[d] is head element 32 d + 8 (r / 4) + 4 h + r % 4
+  if (p.nsplit > 1) {
+    const int64_t pr = (int64_t)split * p.T * p.Hq + out_row;
+    if (h == 0) p.part_ml[pr] = float2{m, lsum};
+    if (b0 < b1) {
+#pragma unroll
+      for (int d = 0; d < 4; ++d)
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          *reinterpret_cast<f32x4*>(p.part_o + pr * kD + 32 * d + 8 * q + 4 * h) =
+              f32x4{o[d][4 * q], o[d][4 * q + 1], o[d][4 * q + 2], o[d][4 * q + 3]};
+    }
+    return;
+  }
+  const float inv = lsum == 0.f ? 0.f : 1.f / lsum;
+#pragma unroll
+  for (int d = 0; d < 4; ++d)
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      *reinterpret_cast<i32x2*>(p.out + out_row * (2 * kD) + 2 * (32 * d + 8 * q + 4 * h)) =
+          i32x2{pack2<KK>(o[d][4 * q] * inv, o[d][4 * q + 1] * inv),
+                pack2<KK>(o[d][4 * q + 2] * inv, o[d][4 * q + 3] * inv)};
+  if (p.lse && h == 0)
+    p.lse[out_row] = lsum == 0.f ? -__builtin_inff() : (m + __log2f(lsum)) * kLn2;
+}
+
+// ---------------------------------------------------------------------------
+// Selected blocks, many tokens: 16 rows a wave, NW waves a workgroup.
+//
+// The workgroup walks the union of its tokens' blocks in ascending order: a
+// block is copied into the LDS once for all of them, a wave none of whose
+// tokens selected it skips its products, and a row of another token gets
+// weight 0.  With one workgroup per token the copying bounds it (64 KB per
+// token, KV head and selected block out of the L2); neighbouring tokens share
+// most of their blocks, and even unrelated lists share them once the tile's
+// tokens name more blocks than there are.  Tiles of 16 rows, because a wave
+// takes the union of its own tokens' lists, which for few tokens is little
+// longer than one list, and because four waves fit a SIMD, which hides what
+// the barriers of unequally busy waves cost.
+// ---------------------------------------------------------------------------
+
+template <int KK, int NW>
+__global__ __launch_bounds__(64 * NW, 4) void attn_union_kernel(AttnParams p) {
+  constexpr int SB = kTileKeys * 256;          // bytes of a stage's K (or V) rows
+  constexpr int NI = SB / 1024 / NW;           // copies of each per wave and stage
+  constexpr int kSelBits = 8192 * NW;          // (token, block) marks of a workgroup
+  constexpr int kSelSpan = 256 * NW;           // blocks marked at a time, at most
+  // One LDS object, cut up by hand: with several, the compiler attaches alias
+  // scopes to the copies into the ring and then waits for them before every
+  // read of it.
+  constexpr int kMarksAt = 4 * SB, kNamedAt = kMarksAt + kSelBits / 8;
+  constexpr int kFlagAt = kNamedAt + 2 * kSelSpan;
+  __shared__ __attribute__((aligned(16))) uint8_t lds[kFlagAt + 16];
+  uint8_t* const kring = lds;                                       // [2][64 K rows]
+  uint8_t* const vring = lds + 2 * SB;                              // [2][64 V rows]
+  uint32_t* const marks = reinterpret_cast<uint32_t*>(lds + kMarksAt);   // [token][block of the span]
+  uint16_t* const named = reinterpret_cast<uint16_t*>(lds + kNamedAt);   // the span's blocks, ascending
+  int* const flag = reinterpret_cast<int*>(lds + kFlagAt);
+  // an XCD takes runs of 8 consecutive tiles of one KV head, which have most
+  // of their blocks in common
+  const int per = gridDim.x / p.nsplit;      // (a multiple of 64)
+  const int split = blockIdx.x / per;
+  const int id = blockIdx.x - split * per;
+  const int run = (id >> 6) * 8 + (id & 7);
+  const int tile = (run / (p.Hkv * p.hchunks)) * 8 + ((id >> 3) & 7);
+  const int unit = run % (p.Hkv * p.hchunks);
+  const int hc = unit % p.hchunks;
+  const int hk = unit / p.hchunks;
+  if (tile >= p.ntiles) return;
+  const AttnTile w = attn_tile(p, tile);
+  if (!w.valid) return;
+
+  const int tid = threadIdx.x;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int l = lane_id();
+  const int n = l & 15, G = l >> 4;
+  const int row = wave * 16 + n;
+  const int ti = row / p.hpt;
+  const int hg = hc * p.hpt + (row - ti * p.hpt);
+  const bool row_ok = row < p.hpt * p.tpt && ti < w.ntok && hg < p.g;
+  const int lim = row_ok ? attn_last(p, w, w.i0 + ti) : -1;
+  const int lim_lo = attn_last(p, w, w.i0);
+  const int lim_hi = attn_last(p, w, w.i0 + w.ntok - 1);
+  const int total = lim_hi >= 0 ? lim_hi / kP + 1 : 0;
+  const int parts = max(1, min(p.nsplit, (total + p.min_blocks - 1) / p.min_blocks));
+  const int b0 = (int)((int64_t)total * split / parts);
+  const int b1 = split < parts ? (int)((int64_t)total * (split + 1) / parts) : b0;
+
+  i32x4 qv[4];
+#pragma unroll
+  for (int s = 0; s < 4; ++s) qv[s] = i32x4{0, 0, 0, 0};
+  if (row_ok) {
+    const uint8_t* qr = p.q + (int64_t)(w.t0 + ti) * p.q_row_stride + (hk * p.g + hg) * (2 * kD);
+#pragma unroll
+    for (int s = 0; s < 4; ++s) qv[s] = ld16(qr + 64 * s + 16 * G);
+  }
+
+  // The blocks come as a list of `count` entries, the marked ones of a span;
+  // their numbers and the places of their rows as in attn_tile_kernel.
+  constexpr int kNoPage = 1 << 30;
+  int base = b0, count = b1 - b0;
+  const int span = min(kSelSpan, kSelBits / p.tpt & ~31);
+  int bidx = 0, pbase = 0;
+  int64_t kat = 0, vat = 0;
+  auto load_entries = [&](int from) {
+    pbase = from;
+    bidx = kNoPage;
+    kat = vat = 0;
+    if (from + l < count) {
+      bidx = base + named[from + l];
+      if (p.paged) {
+        const int pg = p.block_table[(int64_t)w.b * p.MB + bidx];
+        if (pg >= 0 && pg < p.NP) {
+          kat = pg * p.k_page_stride;
+          vat = pg * p.v_page_stride;
+        } else {
+          bidx |= kNoPage;
+        }
+      } else {
+        kat = (w.koff + (int64_t)bidx * kP) * p.k_row_stride;
+        vat = (w.koff + (int64_t)bidx * kP) * p.v_row_stride;
+      }
+    }
+    bidx = consumed(bidx);
+    kat += (int64_t)hk * p.k_head_stride;
+    vat += (int64_t)hk * p.v_head_stride;
+  };
+  struct Entry { int beta; bool there; int64_t k, v; };
+  auto entry_at = [&](int e) -> Entry {
+    if (e - pbase >= 64) load_entries(e);
+    const int x = lane_at(bidx, e - pbase);
+    return Entry{x & (kNoPage - 1), x < kNoPage, lane_at(kat, e - pbase), lane_at(vat, e - pbase)};
+  };
+
+  const int cr = l >> 4, cc = l & 15;
+  uint32_t kof[NI], vof[NI];
+#pragma unroll
+  for (int i = 0; i < NI; ++i) {
+    const int r = (wave * NI + i) * 4 + cr;
+    kof[i] = (uint32_t)(r * p.k_row_stride + 16 * (cc ^ (r & 15)));
+    vof[i] = (uint32_t)(r * p.v_row_stride + 16 * (cc ^ ((r & 7) << 1)));
+  }
+  // Where the keys of half `in` of a block lie, and how many bytes of them
+  // there are to the tile's last visible one.
+  struct Rows { const uint8_t *k, *v; int kb, vb; };
+  auto rows_of = [&](const Entry& x, int in) -> Rows {
+    const int left = x.there ? max(0, min(kTileKeys, lim_hi + 1 - x.beta * kP - in * kTileKeys)) : 0;
+    return Rows{p.k + x.k + in * kTileKeys * p.k_row_stride,
+                p.v + x.v + in * kTileKeys * p.v_row_stride,
+                __builtin_amdgcn_readfirstlane(left * p.k_row_stride),
+                __builtin_amdgcn_readfirstlane(left * p.v_row_stride)};
+  };
+  // a stage's rows through registers, for the careful pass (whose copies need
+  // not overlap anything)
+  auto copy_plain = [&](const Entry& x, int in) {
+    const Rows r = rows_of(x, in);
+    for (int i = 0; i < NI; ++i) {
+      const int row = (wave * NI + i) * 4 + cr;
+      const int at = (wave * NI + i) * 1024 + 16 * l;
+      const i32x4 zero = {0, 0, 0, 0};
+      *reinterpret_cast<i32x4*>(kring + at) = row * p.k_row_stride < r.kb ? ld16(r.k + kof[i]) : zero;
+      *reinterpret_cast<i32x4*>(vring + at) =
+          row * p.v_row_stride < r.vb ? ld16(r.v + vof[i]) : zero;
+    }
+  };
+
+  f32x4 o[8];
+  float m, lsum;
+
+  // A stage in two parts: its scores from the K rows at kt, and what follows
+  // from them with the V rows at vt.  `mine`: this lane's row's token selected
+  // the block.  (The copies that may be in flight go to other parts of the
+  // rings, and the parameters say so, as in attn_rows_kernel.)
+  f32x4 st[4];
+  auto scores = [&](const uint8_t* __restrict kt) __attribute__((always_inline)) {
+    // S^T, four tiles of 16 keys: register r of tile t is key
+    // j0 + 16 t + 4 G + r of row n (fragments read ahead and pinned, as there)
+    constexpr int KLEAD = 3;
+    i32x4 kf[16];
+    // (k step k's chunk is 4 k + G with the row's swizzle: 64 k flipped into one
+    // offset, made afresh for each stage -- as loop invariants the operands'
+    // addresses alone would take the registers that make four waves fit)
+    uint32_t kat0 = n * 256 + ((G ^ n) << 4);
+    asm volatile("" : "+v"(kat0));
+    auto key_frag = [&](int i) __attribute__((always_inline)) -> i32x4 {
+      return *reinterpret_cast<const i32x4*>(kt + 4096 * (i >> 2) + (kat0 ^ (64 * (i & 3))));
+    };
+#pragma unroll
+    for (int t = 0; t < 4; ++t) st[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < KLEAD; ++i) kf[i] = key_frag(i);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      if (i + KLEAD < 16) kf[i + KLEAD] = key_frag(i + KLEAD);
+      st[i >> 2] = mfma16x16x32<KK>(kf[i], qv[i & 3], st[i >> 2]);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  auto absorb = [&](const uint8_t* __restrict vt, const Entry& cur, int in, bool mine, auto careful)
+      __attribute__((always_inline)) {
+    const int j0 = cur.beta * kP + in * kTileKeys;
+    if (!cur.there || j0 + kTileKeys - 1 > lim_lo) {
+      const int rel = cur.there ? lim - j0 - 4 * G : -1;
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) st[t][r] = 16 * t + r <= rel ? st[t][r] : -__builtin_inff();
+    }
+    float mx = st[0][0];
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) mx = fmaxf(mx, st[t][r]);
+    mx = max_xor32(max_xor16(mx)) * p.c;
+    mx = mine ? mx : -__builtin_inff();
+    if (__ballot(mx > m + kMaxLag)) {
+      const float mn = mx > m + kMaxLag ? mx : m;
+      const float alpha = exp2_hw(m - (mn == -__builtin_inff() ? 0.f : mn));
+      m = mn;
+      lsum *= alpha;
+#pragma unroll
+      for (int d = 0; d < 8; ++d) o[d] *= alpha;
+    }
+    const float ms = m == -__builtin_inff() ? 0.f : m;
+    float add = 0.f;
+    i32x4 pf[2];
+    // weights 2 i and 2 i + 1 of this lane's 16, rounded and packed
+    auto weigh = [&](int i) __attribute__((always_inline)) {
+      const float a = exp2_hw(__builtin_fmaf(st[i >> 1][2 * (i & 1)], p.c, -ms));
+      const float b = exp2_hw(__builtin_fmaf(st[i >> 1][2 * (i & 1) + 1], p.c, -ms));
+      add += a + b;
+      const int pk = pack2<KK>(a, b);
+      pf[i >> 2][i & 3] = mine ? pk : 0;
+    };
+    // O^T += V^T P^T, 32 keys a step u, in S^T's order: 32 u + 4 G + {0..3} and
+    // 32 u + 16 + 4 G + {0..3}; fragment i is step i / 8, elements 16 (i % 8) on
+    const int vr = 4 * G + (n >> 2);
+    uint32_t vat0 = vr * 256 + (((n >> 1) & 1) ^ ((vr & 7) << 1)) * 16 + (n & 1) * 8;
+    asm volatile("" : "+v"(vat0));
+    auto value = [&](int i) __attribute__((always_inline)) -> i32x4 {
+      const uint8_t* at = vt + 8192 * (i >> 3) + (vat0 ^ (32 * (i & 7)));
+      const i32x2 v0 = lds_read_tr(at), v1 = lds_read_tr(at + 4096);
+      return i32x4{v0[0], v0[1], v1[0], v1[1]};
+    };
+    if constexpr (!decltype(careful)::value) {
+      constexpr int VLEAD = 2;
+      i32x4 vf[16];
+#pragma unroll
+      for (int i = 0; i < VLEAD; ++i) vf[i] = value(i);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) weigh(i);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        if (i + VLEAD < 16) vf[i + VLEAD] = value(i + VLEAD);
+        o[i & 7] = mfma16x16x32<KK>(vf[i], pf[i >> 3], o[i & 7]);
+        if (i < 4) weigh(i + 4);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) weigh(i);
+      const int first = wave * 16 / p.hpt, last = min((wave * 16 + 15) / p.hpt, w.ntok - 1);
+      for (int tk = first; tk <= last; ++tk) {
+        if (!__ballot(row_ok && ti == tk && mine)) continue;
+        const int end = attn_last(p, w, w.i0 + tk);
+#pragma unroll
+        for (int d = 0; d < 8; ++d) {
+          f32x4 x = o[d];
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            i32x4 v = value(8 * u + d);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int j = j0 + 32 * u + 16 * (e >> 1) + 4 * G + 2 * (e & 1);
+              v[e] = j + 1 <= end ? v[e] : j <= end ? v[e] & 0xFFFF : 0;
+            }
+            x = mfma16x16x32<KK>(v, pf[u], x);
+          }
+#pragma unroll
+          for (int r = 0; r < 4; ++r) o[d][r] = ti == tk ? x[r] : o[d][r];
+        }
+      }
+    }
+    lsum += mine ? add : 0.f;
+  };
+
   // the list's stages, two per block
   auto walk = [&](auto careful) __attribute__((always_inline)) {
     if (count <= 0) return;
     load_entries(0);
     auto selected = [&](const Entry& e) -> bool {
-      if constexpr (!SEL) return true;
       const int at = e.beta - base;
       return row_ok && (marks[ti * (span >> 5) + (at >> 5)] >> (at & 31)) & 1;
     };
-    auto some = [&](bool mine) -> bool { return !SEL || __ballot(mine && row_ok) != 0; };
+    auto some = [&](bool mine) -> bool { return __ballot(mine && row_ok) != 0; };
     if constexpr (decltype(careful)::value) {
       for (int s = 0; s < 2 * count; ++s) {
         const Entry x = entry_at(s >> 1);
@@ -903,56 +1247,52 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tile_kernel(AttnParams p) {
 
   auto pass = [&](auto careful) __attribute__((always_inline)) {
 #pragma unroll
-    for (int d = 0; d < 4; ++d) o[d] = f32x16{};
+    for (int d = 0; d < 8; ++d) o[d] = f32x4{0.f, 0.f, 0.f, 0.f};
     m = -__builtin_inff();
     lsum = 0.f;
-    if constexpr (!SEL) {
-      walk(careful);
-    } else {
-      const int words = span >> 5;
-      for (base = b0; base < b1; base += span) {
-        const int end = min(base + span, b1);
-        __syncthreads();
-        for (int i = tid; i < w.ntok * words; i += 64 * NW) marks[i] = 0;
-        __syncthreads();
-        for (int i = tid; i < w.ntok * p.nsel; i += 64 * NW) {
-          const int tk = i / p.nsel;
-          const int e = p.blocks[((int64_t)(w.t0 + tk) * p.Hkv + hk) * p.nsel + (i - tk * p.nsel)];
-          if (e >= base && e < end && (int64_t)e * kP <= attn_last(p, w, w.i0 + tk))
-            atomicOr(&marks[tk * words + ((e - base) >> 5)], 1u << ((e - base) & 31));
-        }
-        __syncthreads();
-        if (wave == 0) {
-          // two words a lane, then the marked blocks' places by a prefix sum
-          int n0 = 0;
-          for (int wd = 0; wd < words; wd += 64) {
-            uint32_t u = 0;
-            if (wd + l < words)
-              for (int tk = 0; tk < w.ntok; ++tk) u |= marks[tk * words + wd + l];
-            const int incl = wave_incl_scan((int)__popc(u));
-            int at = n0 + incl - __popc(u);
-            for (; u; u &= u - 1) named[at++] = (uint16_t)(32 * (wd + l) + __ffs(u) - 1);
-            n0 += lane_at(incl, 63);
-          }
-          if (l == 0) *flag = n0;
-        }
-        __syncthreads();
-        count = __builtin_amdgcn_readfirstlane(*flag);
-        walk(careful);
+    const int words = span >> 5;
+    for (base = b0; base < b1; base += span) {
+      const int end = min(base + span, b1);
+      __syncthreads();
+      for (int i = tid; i < w.ntok * words; i += 64 * NW) marks[i] = 0;
+      __syncthreads();
+      for (int i = tid; i < w.ntok * p.nsel; i += 64 * NW) {
+        const int tk = i / p.nsel;
+        const int e = p.blocks[((int64_t)(w.t0 + tk) * p.Hkv + hk) * p.nsel + (i - tk * p.nsel)];
+        if (e >= base && e < end && (int64_t)e * kP <= attn_last(p, w, w.i0 + tk))
+          atomicOr(&marks[tk * words + ((e - base) >> 5)], 1u << ((e - base) & 31));
       }
+      __syncthreads();
+      if (wave == 0) {
+        // a word a lane at a time, the marked blocks' places by a prefix sum
+        int n0 = 0;
+        for (int wd = 0; wd < words; wd += 64) {
+          uint32_t u = 0;
+          if (wd + l < words)
+            for (int tk = 0; tk < w.ntok; ++tk) u |= marks[tk * words + wd + l];
+          const int incl = wave_incl_scan((int)__popc(u));
+          int at = n0 + incl - __popc(u);
+          for (; u; u &= u - 1) named[at++] = (uint16_t)(32 * (wd + l) + __ffs(u) - 1);
+          n0 += lane_at(incl, 63);
+        }
+        if (l == 0) *flag = n0;
+      }
+      __syncthreads();
+      count = __builtin_amdgcn_readfirstlane(*flag);
+      walk(careful);
     }
   };
 
 #pragma unroll
-  for (int s = 0; s < 8; ++s) landed(qv[s]);
+  for (int s = 0; s < 4; ++s) landed(qv[s]);
   pass(std::false_type{});
   if (w.ntok > 1) {
     // (x - x is 0 for a finite x only; the products add no rounding of their own)
     float odd = 0.f;
 #pragma unroll
-    for (int d = 0; d < 4; ++d)
+    for (int d = 0; d < 8; ++d)
 #pragma unroll
-      for (int r = 0; r < 16; ++r) odd += o[d][r] - o[d][r];
+      for (int r = 0; r < 4; ++r) odd += o[d][r] - o[d][r];
     __syncthreads();
     if (tid == 0) *flag = 0;
     __syncthreads();
@@ -961,32 +1301,26 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tile_kernel(AttnParams p) {
     if (*flag) pass(std::true_type{});
   }
 
-  lsum = sum_xor32(lsum);
+  lsum = sum_xor32(sum_xor16(lsum));
   if (!row_ok) return;
   const int64_t out_row = ((int64_t)(w.t0 + ti) * p.Hq + hk * p.g + hg);
-  // register r of o[d] is head element 32 d + 8 (r / 4) + 4 h + r % 4
+  // register r of o[d] is head element 16 d + 4 G + r
   if (p.nsplit > 1) {
     const int64_t pr = (int64_t)split * p.T * p.Hq + out_row;
-    if (h == 0) p.part_ml[pr] = float2{m, lsum};
+    if (G == 0) p.part_ml[pr] = float2{m, lsum};
     if (b0 < b1) {
 #pragma unroll
-      for (int d = 0; d < 4; ++d)
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-          *reinterpret_cast<f32x4*>(p.part_o + pr * kD + 32 * d + 8 * q + 4 * h) =
-              f32x4{o[d][4 * q], o[d][4 * q + 1], o[d][4 * q + 2], o[d][4 * q + 3]};
+      for (int d = 0; d < 8; ++d)
+        *reinterpret_cast<f32x4*>(p.part_o + pr * kD + 16 * d + 4 * G) = o[d];
     }
     return;
   }
   const float inv = lsum == 0.f ? 0.f : 1.f / lsum;
 #pragma unroll
-  for (int d = 0; d < 4; ++d)
-#pragma unroll
-    for (int q = 0; q < 4; ++q)
-      *reinterpret_cast<i32x2*>(p.out + out_row * (2 * kD) + 2 * (32 * d + 8 * q + 4 * h)) =
-          i32x2{pack2<KK>(o[d][4 * q] * inv, o[d][4 * q + 1] * inv),
-                pack2<KK>(o[d][4 * q + 2] * inv, o[d][4 * q + 3] * inv)};
-  if (p.lse && h == 0)
+  for (int d = 0; d < 8; ++d)
+    *reinterpret_cast<i32x2*>(p.out + out_row * (2 * kD) + 2 * (16 * d + 4 * G)) =
+        i32x2{pack2<KK>(o[d][0] * inv, o[d][1] * inv), pack2<KK>(o[d][2] * inv, o[d][3] * inv)};
+  if (p.lse && G == 0)
     p.lse[out_row] = lsum == 0.f ? -__builtin_inff() : (m + __log2f(lsum)) * kLn2;
 }
 
