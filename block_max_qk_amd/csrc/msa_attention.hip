@@ -30,9 +30,10 @@ struct Plan {
 //
 // Dense: tiles of 16 rows where the requests' new tokens fill no more on
 // average, 128 rows otherwise, and 256 where requests average three quarters
-// of that and there are 128 such tiles (2048 tokens over 32768 keys, 8 heads a
-// group: 911 us with 256 rows, 951 with 128, 3130 with 16; 9 requests of 2 to
-// 258 tokens: 84, 75 and 163 us).
+// of that and such tiles, or their parts of 8 blocks, fill the chip's 256 CUs
+// (2048 tokens over 32768 keys, 8 heads a group: 911 us with 256 rows, 951 with
+// 128, 3130 with 16; 9 requests of 2 to 258 tokens: 81, 74 and 163 us; one
+// prompt of 1000 tokens: 35, 27 and 59 us).
 // Selected blocks: one workgroup per token and KV head (16 rows), or tiles of
 // 128 rows that walk the union of their tokens' blocks once tokens can share
 // them and fill the chip (16 blocks of 16000 keys, 4 KV heads: 60 tokens 21 us
@@ -55,7 +56,8 @@ Plan plan_for(int64_t T, int64_t B, int64_t Hq, int64_t Hkv, int64_t MB, int64_t
   p.rows = few ? msa::kAttnRows : 128;
   if (!few && nsel == 0) {
     const int64_t rows = T * std::min<int64_t>(g, 256);
-    if (rows >= 192 * B && (rows + 255) / 256 * Hkv >= 128) p.rows = 256;
+    const int64_t big = (rows + 255) / 256 * Hkv;
+    if (rows >= 192 * B && big >= 128 && big * std::max<int64_t>(MB / 8, 1) >= 256) p.rows = 256;
   }
   p.hpt = (int)std::min<int64_t>(g, p.rows);
   p.tpt = few && nsel > 0 ? 1 : p.rows / p.hpt;

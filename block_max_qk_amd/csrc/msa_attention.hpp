@@ -514,8 +514,8 @@ __global__ __launch_bounds__(256, 1) void attn_rows_kernel(AttnParams p) {
 }
 
 // ---------------------------------------------------------------------------
-// The join of a split tile's parts: one wave per row, two elements a lane.
-// Rows that no request holds are left as they are.
+// The join of a split tile's parts: one wave per row, half a wave per part, two
+// pairs of parts in flight.  Rows that no request holds are left as they are.
 // ---------------------------------------------------------------------------
 
 template <int KK>
@@ -523,35 +523,40 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnParams p) {
   const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
   const int l = lane_id();
   const int64_t rows = p.T * p.Hq;
-  if (row >= rows || row >= (int64_t)max(p.cu_q[p.B], 0) * p.Hq ||
-      row < (int64_t)p.cu_q[0] * p.Hq)
-    return;
+  if (row >= rows) return;
   float2 ml = {-__builtin_inff(), 0.f};
   if (l < p.nsplit) ml = p.part_ml[l * rows + row];
+  if (row >= (int64_t)max(p.cu_q[p.B], 0) * p.Hq || row < (int64_t)p.cu_q[0] * p.Hq) return;
+  // parts of a row that is in no request, or that the tile did not need, hold
+  // no sums: l = 0 (NaN where anything seen was no number)
   float mt = max_xor32(max_xor16(ml.x));
-  mt = fmaxf(mt, __shfl_xor(mt, 8));
-  mt = fmaxf(mt, __shfl_xor(mt, 4));
-  mt = fmaxf(mt, __shfl_xor(mt, 2));
-  mt = fmaxf(mt, __shfl_xor(mt, 1));
+#pragma unroll
+  for (int d = 8; d > 0; d >>= 1) mt = fmaxf(mt, __shfl_xor(mt, d));
   const float ms = mt == -__builtin_inff() ? 0.f : mt;
-  const float a = exp2_hw(ml.x - ms);
-  float lt = a * ml.y;
-  lt = sum_xor32(sum_xor16(lt));
-  lt += __shfl_xor(lt, 8);
-  lt += __shfl_xor(lt, 4);
-  lt += __shfl_xor(lt, 2);
-  lt += __shfl_xor(lt, 1);
-  float2 o = {0.f, 0.f};
-  for (int s = 0; s < p.nsplit; ++s) {
-    const float as = __builtin_bit_cast(float, lane_at(__builtin_bit_cast(int, a), s));
-    const float lp = __builtin_bit_cast(float, lane_at(__builtin_bit_cast(int, ml.y), s));
-    if (lp == 0.f) continue;      // a part without visible keys wrote no sums
-    const float2 x = *reinterpret_cast<const float2*>(p.part_o + (s * rows + row) * kD + 2 * l);
-    o.x += as * x.x;
-    o.y += as * x.y;
+  const float a = ml.y == 0.f ? 0.f : exp2_hw(ml.x - ms);
+  float lt = sum_xor32(sum_xor16(a * ml.y));
+#pragma unroll
+  for (int d = 8; d > 0; d >>= 1) lt += __shfl_xor(lt, d);
+  const int half = l >> 5;
+  const unsigned long long filled = __ballot(ml.y != 0.f);
+  auto part = [&](int s) -> f32x4 {      // its share of elements 4 (l % 32) .. + 3
+    const f32x4 none = {0.f, 0.f, 0.f, 0.f};
+    if (!(filled >> s & 1)) return none;
+    return *reinterpret_cast<const f32x4*>(p.part_o + (s * rows + row) * kD + 4 * (l & 31));
+  };
+  f32x4 o = {0.f, 0.f, 0.f, 0.f};
+  for (int s = 0; s < p.nsplit; s += 4) {
+    const int s0 = s + half, s1 = s + 2 + half;      // (at most 66: tested before use)
+    const f32x4 x0 = s0 < p.nsplit ? part(s0) : f32x4{0.f, 0.f, 0.f, 0.f};
+    const f32x4 x1 = s1 < p.nsplit ? part(s1) : f32x4{0.f, 0.f, 0.f, 0.f};
+    o += __shfl(a, s0 & 63) * x0 + __shfl(a, s1 & 63) * x1;
   }
+#pragma unroll
+  for (int r = 0; r < 4; ++r) o[r] = sum_xor32(o[r]);
   const float inv = lt == 0.f ? 0.f : 1.f / lt;
-  reinterpret_cast<int*>(p.out + row * (2 * kD))[l] = pack2<KK>(o.x * inv, o.y * inv);
+  if (half == 0)
+    *reinterpret_cast<i32x2*>(p.out + row * (2 * kD) + 8 * l) =
+        i32x2{pack2<KK>(o[0] * inv, o[1] * inv), pack2<KK>(o[2] * inv, o[3] * inv)};
   if (p.lse && l == 0)
     p.lse[row] = lt == 0.f ? -__builtin_inff() : (mt + __log2f(lt)) * kLn2;
 }
