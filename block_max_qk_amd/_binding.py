@@ -533,10 +533,11 @@ def msa_cache_append(items: Sequence[CacheItem], cos: Optional[torch.Tensor],
     lib = _lib or load_library()
     if not 1 <= len(items) <= APPEND_MAX_ITEMS:
         raise ValueError(f"1 to {APPEND_MAX_ITEMS} items, got {len(items)}")
-    index = items[0].src.get_device()
+    lead = items[0][0]
+    index = lead.get_device()
     for t in (cos, sin, block_table, cu_seqlens_q, kv_len):
         if t is not None and t.get_device() != index:
-            raise ValueError(f"tensors are on {t.device} and {items[0].src.device}")
+            raise ValueError(f"tensors are on {t.device} and {lead.device}")
     paged = block_table is not None
     max_blocks = block_table.shape[-1] if paged else 0
     B = _check_lengths(cu_seqlens_q, kv_len, block_table, max_blocks, paged)
@@ -577,6 +578,8 @@ def msa_cache_append(items: Sequence[CacheItem], cos: Optional[torch.Tensor],
             src.data_ptr(), code(src.dtype, -1), m, *src.shape, *src.stride(),
             dst.data_ptr(), code(dst.dtype, -1), n, *dst.shape, *dst.stride(),
             at, lay, 1 if rotate else 0))
+    if index < 0 and lead.numel():
+        raise ValueError(f"the tensors must be on a GPU, src is on {lead.device}")
     handle = _stream_handle(stream, index)
     with _guard(index):
         st = lib.msa_cache_append(b"".join(packed), len(items), _address(cos), _address(sin),
@@ -630,6 +633,8 @@ def _attention(query, key, value, blocks, block_table, cu_seqlens_q, kv_len, lay
         k = blocks.shape[2]
     if workspace is not None and not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous")
+    if index < 0 and query.numel():
+        raise ValueError(f"the tensors must be on a GPU, query is on {query.device}")
     scale = 1.0 / math.sqrt(D) if softmax_scale is None else float(softmax_scale)
     handle = _stream_handle(stream, index)
     with _guard(index):

@@ -50,11 +50,14 @@ msa_status_t item_for(const msa_append_item_t& in, int64_t T, AppendItem& a) {
       return MSA_ERR_SHAPE;
     a.row = (T > 1 ? dst.stride[0] : 0) * eb;
     a.head = (H > 1 ? dst.stride[1] : 0) * eb;
-    // (a zero or overlapping stride would write one place twice)
-    if (dst.stride[2] != 1 || (T > 1 && a.row < last * eb) || (H > 1 && a.head < last * eb) ||
+    // (rows that overlap would be written by two waves: a token's heads lie
+    // within its stride, or a head's tokens within the head's)
+    const int64_t len = last * eb;
+    if (dst.stride[2] != 1 || (T > 1 && a.row < len) || (H > 1 && a.head < len) ||
+        (T > 1 && H > 1 && a.row < a.head * (H - 1) + len && a.head < a.row * (T - 1) + len) ||
         a.row % 16 || a.head % 16 || !msa::aligned16(dst.data))
       return MSA_ERR_STRIDE;
-    a.s_head = i8 ? 4 : 4;             // [T, H] floats, or [T, H, 4] bytes
+    a.s_head = 4;                      // [T, H] floats, or [T, H, 4] bytes
     a.s_row = H * 4;
     a.limit = T;
   } else {
@@ -62,6 +65,9 @@ msa_status_t item_for(const msa_append_item_t& in, int64_t T, AppendItem& a) {
     const msa_status_t st = msa::cache_view(dst, in.layout, last, msa::kP, false, v);
     if (st != MSA_OK) return st;
     if (v.heads != H) return MSA_ERR_SHAPE;
+    // (pages that overlap, likewise)
+    if (in.layout != MSA_LAYOUT_TND && v.pages > 1 && v.page < H * msa::kP * last * eb)
+      return MSA_ERR_STRIDE;
     a.page = v.page;
     a.row = v.row;
     a.head = v.head;
@@ -138,13 +144,13 @@ extern "C" msa_status_t msa_cache_append(const msa_append_item_t* items, int32_t
   p.T = T;
   p.B = batch;
   p.MB = (int32_t)max_blocks;
-  p.items = num_items;
   p.half = rotated ? rotary_dim / 2 : 0;
   p.interleaved = interleaved;
   p.groups = groups_for(T, p.steps);
   p.per_wave = (p.steps + p.groups - 1) / p.groups;
   const int64_t grid = (T * p.groups + msa::kAppendWaves - 1) / msa::kAppendWaves;
-  if (grid > INT32_MAX) return MSA_ERR_SHAPE;
+  // (a launch holds less than 2^32 threads)
+  if (grid * 64 * msa::kAppendWaves > (int64_t)UINT32_MAX) return MSA_ERR_SHAPE;
   hipStream_t s = static_cast<hipStream_t>(stream);
   const dim3 gr((unsigned)grid), bl(64 * msa::kAppendWaves);
   const hipError_t e = dt == MSA_DTYPE_BF16

@@ -40,7 +40,7 @@ struct AppendParams {
   int64_t positions;                  // rows of the angle table
   int64_t T;
   int32_t B, MB;
-  int32_t items, steps;               // steps of all items
+  int32_t steps;                      // of all items
   int32_t per_wave, groups;           // steps per wave, waves per token
   int32_t half;                       // rotary_dim / 2 (0: no rotation)
   int32_t interleaved, packed;        // packed: some item is TND
@@ -83,22 +83,14 @@ __device__ __forceinline__ bool lanes_any(bool x) {
   return (m & ((1ull << LANES) - 1)) != 0;
 }
 
-// Elements 8 i .. 8 i + 7 of a row (lane i of its 16), rotated, in type F.
-// The partners of halves-style pairs lie `half` elements away, in another
-// lane; c and s hold the lane's angles: of its 8 elements (halves) or of its 4
-// pairs (interleaved).
+// Interleaved pairs of a lane's 8 elements, rotated by their 4 angles in type F.
 template <typename F>
-__device__ __forceinline__ void rotate8(F* x, const float* c, const float* s, int i, int half,
-                                        bool interleaved) {
-  if (interleaved) {
-    if (8 * i < 2 * half) {
+__device__ __forceinline__ void rotate_pairs(F* x, const float* c, const float* s) {
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const F a = x[2 * k], b = x[2 * k + 1];
-        x[2 * k] = a * (F)c[k] - b * (F)s[k];
-        x[2 * k + 1] = b * (F)c[k] + a * (F)s[k];
-      }
-    }
+  for (int k = 0; k < 4; ++k) {
+    const F a = x[2 * k], b = x[2 * k + 1];
+    x[2 * k] = a * (F)c[k] - b * (F)s[k];
+    x[2 * k + 1] = b * (F)c[k] + a * (F)s[k];
   }
 }
 
@@ -132,7 +124,8 @@ __global__ __launch_bounds__(64 * kAppendWaves) void append_kernel(AppendParams 
     packed += pos;
   }
 
-  // this lane's angles
+  // this lane's angles: of its 8 elements (halves, whose partners lie p.half
+  // elements away in another lane) or of its 4 pairs (interleaved)
   float c[8], s[8];
   if (p.half > 0) {
     const float* cr = p.cos + pos * p.half;
@@ -206,7 +199,7 @@ __global__ __launch_bounds__(64 * kAppendWaves) void append_kernel(AppendParams 
 #pragma unroll
         for (int k = 0; k < 8; ++k) x[k] = elem16((uint32_t)raw[k >> 1], k & 1, BF);
         if (p.interleaved) {
-          rotate8(x, c, s, i, p.half, true);
+          if (rot_lane) rotate_pairs(x, c, s);
         } else {
           // (every lane takes part in the exchange)
           i32x4 other;
@@ -239,7 +232,7 @@ __global__ __launch_bounds__(64 * kAppendWaves) void append_kernel(AppendParams 
     for (int k = 0; k < 8; ++k) y[k] = elem16((uint32_t)raw[k >> 1], k & 1, BF);
     if (a.rotate) {
       if (p.interleaved) {
-        rotate8(y, c, s, i, p.half, true);
+        if (rot_lane) rotate_pairs(y, c, s);
       } else {
         i32x4 other;
 #pragma unroll

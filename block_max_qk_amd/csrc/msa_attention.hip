@@ -155,6 +155,7 @@ msa_status_t run(const msa_tensor_t* query, const msa_tensor_t* key, const msa_t
       (reinterpret_cast<uintptr_t>(lse) & 3u))
     return MSA_ERR_STRIDE;
   if (T == 0) return MSA_OK;
+  if (!query->data || (kv.pages > 0 && (!key->data || !value->data))) return MSA_ERR_NULL;
 
   const Plan plan = plan_for(T, batch, Hq, Hkv, max_blocks, selected ? num_blocks : 0);
   const int64_t need = workspace_for(plan, T, Hq);
@@ -164,7 +165,11 @@ msa_status_t run(const msa_tensor_t* query, const msa_tensor_t* key, const msa_t
     const int64_t runs = (plan.ntiles + 7) / 8 * Hkv * plan.hchunks;
     grid = (runs + 7) / 8 * 64 * plan.nsplit;
   }
-  if (grid > INT32_MAX || T * Hq > (int64_t)INT32_MAX * 4) return MSA_ERR_SHAPE;
+  // (a launch holds less than 2^32 threads)
+  const int64_t threads = plan.rows == 256 || (selected && plan.rows == 128) ? 512 : 256;
+  if (grid * threads > UINT32_MAX ||
+      (plan.nsplit > 1 && (T * Hq + 3) / 4 * 256 > (int64_t)UINT32_MAX))
+    return MSA_ERR_SHAPE;
 
   AttnParams p{};
   p.q = static_cast<const uint8_t*>(query->data);

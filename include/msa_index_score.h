@@ -291,8 +291,9 @@ msa_status_t msa_block_topk(const float* scores, int64_t Hq, int64_t T, int64_t 
  *  - a table entry outside [0, NP) names no page: nothing is written there,
  *    and its keys are not visible;
  *  - max_blocks <= 2^24, batch <= 2^30, T < 2^31, at most 2^16 heads, at most
- *    2^31 - 1 pages or packed keys, and one 128-token block of one head spans
- *    less than 2 GiB (MSA_ERR_SHAPE otherwise).
+ *    2^31 - 1 pages or packed keys, one 128-token block of one head spans less
+ *    than 2 GiB, and a launch holds less than 2^32 threads (reached from about
+ *    2 million tokens at 8 KV heads on; MSA_ERR_SHAPE otherwise).
  * Blocks at or past max_blocks, and packed keys past the tensor's end, are
  * neither read nor written, whatever kv_len says.  All pointers are
  * caller-owned, nothing is allocated or kept, calls may overlap as long as
@@ -326,7 +327,8 @@ typedef struct {
  *  - in a paged cache (BBND [NP, 128, H, D], BNBD [NP, H, 128, D], strides as
  *    msa_index_score's key) in page block_table[b, pos / 128], slot pos % 128;
  *  - in a packed cache (TND [T2, H, D]) at token sum_{b' < b} kv_len[b'] + pos;
- *  - with MSA_LAYOUT_ROWS in dst[t, h, :] (strides as src; may be src itself).
+ *  - with MSA_LAYOUT_ROWS in dst[t, h, :] (strides as src, rows that do not
+ *    overlap; may be src itself, if no other item reads that src).
  * dst's type says how:
  *  - src's own type: rounded to nearest even;
  *  - F8E4M3, F8E5M2: rounded to nearest even, past the largest finite value to
@@ -351,8 +353,8 @@ typedef struct {
  *
  * A token before position 0, or (if any item is rotated) at or past
  * `positions`, is skipped in every item.  A call must not write one place
- * twice (two requests' tables naming one page for new tokens): which row
- * stays is not defined.
+ * twice (two items with one dst, two requests' tables naming one page for new
+ * tokens): which row stays is not defined.
  * Returns MSA_ERR_ATTR for num_items outside [1, MSA_APPEND_MAX_ITEMS] or a
  * bad rotate, rotary_dim or interleaved, MSA_ERR_SCALE for a scale given with
  * a type that has none or missing, MSA_ERR_DTYPE, _LAYOUT, _SHAPE, _STRIDE,

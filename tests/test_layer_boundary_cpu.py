@@ -65,6 +65,14 @@ def test_attention_nulls():
     assert attend(T=2, n=4, blocks=None) == NULL
 
 
+def test_attention_data_nulls():
+    none = desc((6, 128, 2, 128), addr=None)
+    assert attend(q=desc((2, 8, 128), addr=None), T=2) == NULL
+    assert attend(k=none, T=2) == NULL
+    assert attend(v=none, T=2) == NULL
+    assert attend(v=none, T=2, n=4, blocks=FAKE) == NULL
+
+
 @pytest.mark.parametrize("layout", [-1, 3, 7])
 def test_attention_layouts(layout):
     assert attend(layout=layout) == LAYOUT
@@ -228,6 +236,14 @@ def test_append_shapes_and_strides():
     assert append(item(src=two, dst=dims((2, 2, 128), (256, 0, 1)), layout=ROWS)) == STRIDE
     assert append(item(src=two, dst=dims((9, 2, 128), (512, 128, 1)), layout=TND),
                   table=None, mb=0) == STRIDE
+    # a token's heads between another token's heads; heads outside tokens are taken
+    assert append(item(src=two, dst=dims((2, 2, 128), (128, 128, 1)), layout=ROWS)) == STRIDE
+    three = dims((3, 2, 128))
+    assert append(item(src=three, dst=dims((3, 2, 128), (128, 256, 1)), layout=ROWS)) == STRIDE
+    assert append(item(src=three, dst=dims((3, 2, 128), (128, 384, 1), addr=0),
+                       layout=ROWS)) == NULL
+    # pages that overlap
+    assert append(item(src=two, dst=dims((6, 128, 2, 128), (32752, 256, 128, 1)))) == STRIDE
     assert append(item(src=dims((2, 2, 128), addr=0))) == NULL
     assert append(item(src=two), cos=None) == NULL
 
@@ -317,3 +333,24 @@ def test_append_binding():
         m.msa_cache_append(**app(items=[good._replace(layout="XYZ")]))
     with pytest.raises(m.MsaError):
         m.msa_cache_append(**app(cos=torch.zeros(9, 4), sin=torch.zeros(9, 4)))
+
+
+def test_binding_refuses_host_tensors():
+    # well-formed, but the kernels would be given addresses of host memory
+    for a in (args(), args(query=torch.zeros(2, 8, 128, dtype=torch.float16))):
+        with pytest.raises(ValueError, match="on a GPU"):
+            m.msa_attention(**a)
+    with pytest.raises(ValueError, match="on a GPU"):
+        m.msa_block_attention(blocks=torch.zeros(2, 2, 4, dtype=torch.int32), **args())
+    with pytest.raises(ValueError, match="on a GPU"):
+        m.msa_cache_append(**app(T=2))
+
+
+def test_launches_hold_less_than_2_32_threads():
+    # 2^31 - 1 tokens of 16 heads would need 2^37 workgroups' threads
+    T = 2**31 - 1
+    assert attend(q=desc((T, 16, 128)), T=T) == SHAPE
+    assert attend(q=desc((T, 16, 128)), n=16, blocks=FAKE, T=T) == SHAPE
+    one = dict(layout=ROWS, rotate=0)
+    assert append(item(src=dims((T, 2, 128)), dst=dims((T, 2, 128)), **one), table=None,
+                  mb=0) == SHAPE
