@@ -7,6 +7,12 @@
 // (16-byte loads, whole lines per row).  The step's item is the same for the
 // whole wave, so its type, layout and pointers are scalars and nothing
 // diverges.  Loads run three steps ahead.
+//
+// 14000 tokens of 64 query, 8 key and 8 value rows and an e4m3 index branch: 139
+// us, 4.5 TB/s of reads and writes together (a copy reaches 4.95); 4096 tokens
+// with an MXFP4 index branch 37 us, 2.9 TB/s (the float64 of the encoding is the
+// dearer part there); a decode step of 64 tokens 5.8 us: its three dependent
+// reads and the launch.
 #pragma once
 
 #include "msa_device.hpp"

@@ -514,8 +514,11 @@ __global__ __launch_bounds__(256, 1) void attn_rows_kernel(AttnParams p) {
 }
 
 // ---------------------------------------------------------------------------
-// The join of a split tile's parts: one wave per row, half a wave per part, two
-// pairs of parts in flight.  Rows that no request holds are left as they are.
+// The join of a split tile's parts: one wave per row, half a wave per part (32
+// lanes of 16 bytes are a part's row), two pairs of parts in flight.  Bound by
+// latency and then memory: 4096 rows in 3 parts 4.7 us, 22624 rows in 3 parts
+// (41 MB) 9.7 us, 11.7 with a whole wave per part, one after the other.  Rows
+// that no request holds are left as they are.
 // ---------------------------------------------------------------------------
 
 template <int KK>
@@ -568,6 +571,18 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnParams p) {
 // The stages' K and V rows are copied straight into two-deep LDS rings one
 // stage ahead, through raw buffers that end at the tile's last visible key, so
 // rows past it read zeros (a stored NaN there cannot reach a sum).
+//
+// Bound by the matrix units and, before they are full, by the card's power: 2048
+// tokens over 32768 keys, 32 heads on 4 KV heads, take 909 to 972 us by card
+// (1.10 to 1.17 PFLOP/s; 8192^3 products of the library reach 1.24), with the MFMA
+// busy in 56% of the cycles, vector instructions in 40%, the LDS in 25% without
+// bank conflicts.  32 rows a wave, because a fragment of K or V out of the LDS
+// then feeds the largest MFMA; 8 waves a workgroup share a stage's copies (4
+// where 256 rows would leave CUs without work).  Two waves a SIMD fill the gaps
+// between one wave's MFMAs and its weights.  Without effect within 1%: the next
+// stage's scores beside this one's weights by hand (spills: slower), wave
+// priorities, tiles handed out by weight, leaving out a last half block that no
+// row sees.
 //
 // A weight of 0 does not hide an infinity or NaN in the value of a key that
 // only other rows of the tile see.  So a tile that ends with an accumulator
@@ -942,6 +957,14 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tile_kernel(AttnParams p) {
 // takes the union of its own tokens' lists, which for few tokens is little
 // longer than one list, and because four waves fit a SIMD, which hides what
 // the barriers of unequally busy waves cost.
+//
+// 4096 tokens of 8 heads a group over 16 blocks each of 32768 keys, lists that
+// overlap in part (23 blocks for two tokens together, 51 for sixteen): 328 us,
+// 0.41 PFLOP/s of the selected products; 374 us with 32 rows a wave and half as
+// many waves, 1058 us with a workgroup per token.  With one list for each tile's
+// tokens it takes 183 us: the rest is the wave's own union.  Where K and V come
+// from hardly matters (325 us with every block on one of 16 pages), and no unit
+// is full: MFMA 23%, vector 34%, LDS 24% of the cycles.
 // ---------------------------------------------------------------------------
 
 template <int KK, int NW>
