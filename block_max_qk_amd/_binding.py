@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import math
 import os
 import struct
@@ -455,11 +456,11 @@ _PACK_ITEM = {(i, j): struct.Struct("<" + f + g + "Qii").pack
 
 
 def _packed(t: torch.Tensor) -> bytes:
-    shape = t.shape
-    n = len(shape)
+    stride = t.stride()
+    n = len(stride)
     if not 1 <= n <= 4:
         raise ValueError(f"a tensor of {n} axes: 1 to 4 are taken")
-    return _PACK[n](t.data_ptr(), DTYPE_CODE.get(t.dtype, -1), n, *shape, *t.stride())
+    return _PACK[n](t.data_ptr(), DTYPE_CODE.get(t.dtype, -1), n, *t.shape, *stride)
 
 
 def _address(t: Optional[torch.Tensor]):
@@ -475,8 +476,8 @@ def _check_lengths(cu_seqlens_q, kv_len, block_table, max_blocks, paged) -> int:
         raise ValueError("kv_len must be a contiguous int32 tensor")
     if kv_len.dim() != 1:
         raise ValueError("kv_len must be 1-D [B] (per-request lengths)")
-    B = kv_len.shape[0]
-    if cu_seqlens_q.dim() != 1 or cu_seqlens_q.shape[0] != B + 1:
+    B = kv_len.numel()
+    if cu_seqlens_q.dim() != 1 or cu_seqlens_q.numel() != B + 1:
         raise ValueError(f"cu_seqlens_q must be [B+1] = [{B + 1}], got "
                          f"{tuple(cu_seqlens_q.shape)}")
     if block_table is None:
@@ -497,6 +498,14 @@ def _stream_of(handle, dev):
     if not handle:
         return torch.cuda.default_stream(dev)
     return torch.cuda.ExternalStream(handle, device=dev)
+
+
+def _raw_stream(stream, index: int):
+    """``_stream_handle`` without a stream object for the current stream, which
+    costs a small call a microsecond."""
+    if stream is None and index >= 0:
+        return torch._C._cuda_getCurrentRawStream(index)
+    return _stream_handle(stream, index)
 
 
 def _guard(index: int):
@@ -580,7 +589,7 @@ def msa_cache_append(items: Sequence[CacheItem], cos: Optional[torch.Tensor],
             at, lay, 1 if rotate else 0))
     if index < 0 and lead.numel():
         raise ValueError(f"the tensors must be on a GPU, src is on {lead.device}")
-    handle = _stream_handle(stream, index)
+    handle = _raw_stream(stream, index)
     with _guard(index):
         st = lib.msa_cache_append(b"".join(packed), len(items), _address(cos), _address(sin),
                                   positions, rotary, 1 if interleaved else 0,
@@ -596,6 +605,9 @@ def msa_attention_workspace(T: int, batch: int, Hq: int, Hkv: int, max_blocks: i
     (``num_blocks`` 0: dense)."""
     return int(load_library().msa_attention_workspace(int(T), int(batch), int(Hq), int(Hkv),
                                                       int(max_blocks), int(num_blocks)))
+
+
+_workspace_bytes = functools.lru_cache(maxsize=1024)(msa_attention_workspace)
 
 
 def _attention(query, key, value, blocks, block_table, cu_seqlens_q, kv_len, layout, sparse_mode,
@@ -622,8 +634,11 @@ def _attention(query, key, value, blocks, block_table, cu_seqlens_q, kv_len, lay
     if lse is not None and (lse.dtype != torch.float32 or lse.shape != shape[:2] or
                             not lse.is_contiguous()):
         raise ValueError(f"lse must be a contiguous float32 [{T}, {Hq}] tensor")
-    kr = _key_rows(key, lay)
-    Hkv = kr[1] if kr is not None else 0
+    if key.dim() == 4:
+        Hkv = key.shape[1 if lay == 2 else 2]
+    else:                                # packed, or one head with no axis of its own
+        kr = _key_rows(key, lay)
+        Hkv = kr[1] if kr is not None else 0
     k = 0
     if blocks is not None:
         if (blocks.dtype != torch.int32 or not blocks.is_contiguous() or blocks.dim() != 3 or
@@ -636,10 +651,10 @@ def _attention(query, key, value, blocks, block_table, cu_seqlens_q, kv_len, lay
     if index < 0 and query.numel():
         raise ValueError(f"the tensors must be on a GPU, query is on {query.device}")
     scale = 1.0 / math.sqrt(D) if softmax_scale is None else float(softmax_scale)
-    handle = _stream_handle(stream, index)
+    handle = _raw_stream(stream, index)
     with _guard(index):
-        need = lib.msa_attention_workspace(T, B, Hq, Hkv, max_blocks, k)
-        if need and workspace is None:
+        need = 0 if workspace is not None else _workspace_bytes(T, B, Hq, Hkv, max_blocks, k)
+        if need:
             # memory of the stream that the kernels run on, so that it is
             # handed on only behind them
             if stream is None:
@@ -703,7 +718,7 @@ def _outputs(query, return_lse, stream):
     out = torch.empty_like(query, memory_format=torch.contiguous_format)
     if not return_lse:
         return out, None
-    return out, query.new_empty(query.shape[:2], dtype=torch.float32)
+    return out, torch.empty(query.shape[:2], dtype=torch.float32, device=query.device)
 
 
 def _default_blocks(key, block_table) -> int:

@@ -22,7 +22,8 @@ struct Plan {
                      // 128 with selected blocks: attn_union_kernel)
   int hpt, tpt, hchunks;
   int64_t ntiles;
-  int nsplit, min_blocks;
+  int nsplit, min_blocks, target;
+  int64_t units;     // workgroups (attn_union_kernel: tiles x parts)
   bool once;         // no two workgroups read the same rows of keys
 };
 
@@ -42,13 +43,21 @@ struct Plan {
 //
 // Few tiles are split over the keys until there are about `want` parts, of
 // min_blocks blocks at least; a split pays a second kernel and the traffic of
-// its partial sums.  (64 requests x 8 KV heads, up to 64 blocks: 199 us in
-// 1536 parts, 208 in 1024, 221 unsplit; 64 x 4 with 16 selected blocks: 44 us
-// unsplit, 52 in two parts; 512 tokens over 8000 keys, 128 rows: 87 us in 512
-// parts, 96 in 256, 149 unsplit; 256 rows, 1024 tokens over 16000 keys: 264 us in
-// 256 parts, 272 in 512; 800 tokens over selected blocks: 99 us in 256 parts,
-// 114 in 512; one prompt of 1000 tokens: 27 us unsplit, 39 in two parts of 4
-// blocks.)
+// its partial sums.  (64 x 4 with 16 selected blocks: 44 us unsplit, 52 in two
+// parts; 512 tokens over 8000 keys, 128 rows: 87 us in 512 parts, 96 in 256,
+// 149 unsplit; 256 rows, 1024 tokens over 16000 keys: 264 us in 256 parts, 272
+// in 512; 800 tokens over selected blocks: 99 us in 256 parts, 114 in 512; one
+// prompt of 1000 tokens: 27 us unsplit, 39 in two parts of 4 blocks.)
+//
+// Dense tiles of 16 rows are split by their own lengths (attn_part), aiming at
+// 192 parts, three quarters of the CUs, which leaves the rounding up room in one
+// round of workgroups.  (8 KV heads, one token each; 24 requests of 1024 keys 23
+// us, of up to 4096 32 us, of 512 and one of 8192 32 us; the same number of parts
+// for every tile, 1536 in all: 29, 46 and 58 us; aiming at 128, 256 and 512
+// parts: 23, 48 and 37; 30, 47 and 30; 29, 50 and 36 us.  64 requests of up to
+// 8192 keys: 194 us, 196 with 1536 even parts.)  A cache of fewer than 8 blocks
+// is not worth the second kernel (4 blocks: 8.2 us, 9.1 in two parts), nor are
+// more than 1024 tiles.
 Plan plan_for(int64_t T, int64_t B, int64_t Hq, int64_t Hkv, int64_t MB, int64_t nsel) {
   Plan p{};
   const int64_t g = Hq / Hkv;
@@ -69,8 +78,16 @@ Plan plan_for(int64_t T, int64_t B, int64_t Hq, int64_t Hkv, int64_t MB, int64_t
   p.min_blocks = few ? 2 : 8;
   const int64_t want = nsel > 0 ? (few ? 128 : 256) : few ? 1536 : p.rows == 128 ? 512 : 256;
   int64_t n = items >= want ? 1 : (want + items - 1) / items;
+  p.target = 1;
+  if (few && nsel == 0) {
+    const int64_t heads = Hkv * p.hchunks;
+    p.target = (int)std::max<int64_t>(192 / heads, 1);
+    n = items >= 1024 || MB < 8 ? 1 : std::min<int64_t>(p.target, std::max<int64_t>(8192 / items, 1));
+  }
   n = std::min(n, (blocks + p.min_blocks - 1) / p.min_blocks);
   p.nsplit = (int)std::max<int64_t>(1, std::min(n, kMaxSplit));
+  p.units = p.ntiles * Hkv * p.hchunks * p.nsplit;
+  if (few && nsel == 0 && p.nsplit > 1) p.units = (p.target + 1 + p.ntiles) * Hkv * p.hchunks;
   return p;
 }
 
@@ -160,7 +177,7 @@ msa_status_t run(const msa_tensor_t* query, const msa_tensor_t* key, const msa_t
   const Plan plan = plan_for(T, batch, Hq, Hkv, max_blocks, selected ? num_blocks : 0);
   const int64_t need = workspace_for(plan, T, Hq);
   if (need > 0 && (!workspace || workspace_bytes < need)) return MSA_ERR_WORKSPACE;
-  int64_t grid = plan.ntiles * Hkv * plan.hchunks * plan.nsplit;
+  int64_t grid = plan.units;
   if (selected && plan.rows != msa::kAttnRows) {   // runs of 8 tiles, 8 runs at a time
     const int64_t runs = (plan.ntiles + 7) / 8 * Hkv * plan.hchunks;
     grid = (runs + 7) / 8 * 64 * plan.nsplit;
@@ -209,6 +226,7 @@ msa_status_t run(const msa_tensor_t* query, const msa_tensor_t* key, const msa_t
   p.ntiles = (int32_t)plan.ntiles;
   p.nsplit = plan.nsplit;
   p.min_blocks = plan.min_blocks;
+  p.per_target = 1.f / plan.target;
   hipStream_t s = static_cast<hipStream_t>(stream);
   const hipError_t e = query->dtype == MSA_DTYPE_BF16 ? launch<msa::KBF16>(p, plan, grid, s)
                                                       : launch<msa::KF16>(p, plan, grid, s);

@@ -48,8 +48,9 @@ struct AttnParams {
   int32_t paged, causal;
   float c;                     // softmax_scale * log2(e)
   int32_t hpt, tpt, hchunks, ntiles;      // as in Params
-  int32_t nsplit;              // parts that a tile's blocks are split into
+  int32_t nsplit;              // parts that a tile's blocks are split into, at most
   int32_t min_blocks;          // blocks per part at least
+  float per_target;            // 1 / the parts per KV head that attn_part aims at
 };
 
 constexpr float kLog2e = 1.44269504088896340736f;
@@ -64,10 +65,31 @@ struct AttnTile {
   int64_t koff;                // packed offset of the request's keys
 };
 
+// Keys that exist of a request's kv, packed ones from koff on.
+__device__ __forceinline__ int keys_there(const AttnParams& p, int kv, int64_t koff) {
+  return (int)(p.paged ? min((int64_t)kv, (int64_t)p.MB * kP)
+                       : max(min((int64_t)kv, p.keys - koff), (int64_t)0));
+}
+
+// Tile `tin` of request b, which begins at token t0 with lq new tokens and kv
+// keys.  Lengths that break the rules (negative, past the tensors) are cut to
+// what the tensors hold, so that no address leaves them.
+__device__ __forceinline__ void set_tile(const AttnParams& p, AttnTile& w, int b, int tin, int t0,
+                                         int lq, int kv, int64_t koff) {
+  w.b = b;
+  w.Lq = lq;
+  w.i0 = tin * p.tpt;
+  w.t0 = t0 + w.i0;
+  const int64_t room = p.T - (int64_t)w.t0;
+  w.ntok = (int)min((int64_t)min(p.tpt, w.Lq - w.i0), w.t0 < 0 ? (int64_t)0 : room);
+  w.koff = koff;
+  w.len = kv;
+  w.L = keys_there(p, kv, koff);
+  w.valid = w.ntok > 0;
+}
+
 // The tile-th tile of tpt tokens: a prefix sum of the requests' tile counts,
-// 64 requests at a time (every lane of the wave takes part).  Lengths that
-// break the rules (negative, past the tensors) are cut to what the tensors
-// hold, so that no address leaves them.
+// 64 requests at a time (every lane of the wave takes part).
 __device__ __forceinline__ AttnTile attn_tile(const AttnParams& p, int tile) {
   AttnTile w;
   w.valid = 0;
@@ -82,33 +104,116 @@ __device__ __forceinline__ AttnTile attn_tile(const AttnParams& p, int tile) {
       lq = max(p.cu_q[b + 1] - t0, 0);
       kv = max(p.kv_len[b], 0);
     }
-    const int n = (int)(((int64_t)lq + p.tpt - 1) / p.tpt);
+    int n = lq > 0;
+    if (__ballot(lq > p.tpt)) n = (int)(((uint32_t)lq + p.tpt - 1) / (uint32_t)p.tpt);
     const int incl = wave_incl_scan(n);
-    const int64_t kincl = wave_incl_scan((int64_t)kv);
+    const int64_t kincl = p.paged ? kv : wave_incl_scan((int64_t)kv);
     const int total = lane_at(incl, 63);
     if (tile < acc + total) {
       const unsigned long long m = __ballot(acc + incl > tile);
       const int src = __builtin_amdgcn_readfirstlane(__ffsll((long long)m) - 1);
       const int tin = tile - (acc + lane_at(incl, src) - lane_at(n, src));
-      w.b = base + src;
-      w.Lq = lane_at(lq, src);
-      w.i0 = tin * p.tpt;
-      w.t0 = lane_at(t0, src) + w.i0;
-      const int64_t room = p.T - (int64_t)w.t0;
-      w.ntok = (int)min((int64_t)min(p.tpt, w.Lq - w.i0), w.t0 < 0 ? (int64_t)0 : room);
-      w.koff = kacc + lane_at(kincl, src) - lane_at(kv, src);
-      w.L = w.len = lane_at(kv, src);
-      if (p.paged)
-        w.L = (int)min((int64_t)w.L, (int64_t)p.MB * kP);
-      else
-        w.L = (int)max(min((int64_t)w.L, p.keys - w.koff), (int64_t)0);
-      w.valid = w.ntok > 0;
+      set_tile(p, w, base + src, tin, lane_at(t0, src), lane_at(lq, src), lane_at(kv, src),
+               kacc + lane_at(kincl, src) - lane_at(kv, src));
       return w;
     }
     acc += total;
-    kacc += lane_at(kincl, 63);
+    if (!p.paged) kacc += lane_at(kincl, 63);
   }
   return w;
+}
+
+// Part `unit` of a launch whose tiles are split by their own lengths: parts of
+// at most a `target`-th of all blocks (of one head), min_blocks blocks or more,
+// so that long requests get many and short ones stay whole.  The parts of up to
+// 64 requests (one a lane) are handed out longest first, and the launch ends
+// evenly whatever order the requests come in.  A request's tiles get as many
+// parts each as its last one needs; there are at most target + 1 + ntiles parts.
+struct AttnPart {
+  AttnTile w;
+  int split, parts;
+};
+__device__ __forceinline__ AttnPart attn_part(const AttnParams& p, int unit) {
+  AttnPart r;
+  r.w.valid = 0;
+  const int l = lane_id();
+  int t0 = 0, lq = 0, kv = 0, n = 0, nb = 0;     // of request base + l
+  int64_t koff = 0, kacc = 0;
+  auto load = [&](int base) {
+    const int b = base + l;
+    t0 = lq = kv = 0;
+    if (b < p.B) {
+      t0 = p.cu_q[b];
+      lq = max(p.cu_q[b + 1] - t0, 0);
+      kv = max(p.kv_len[b], 0);
+    }
+    n = lq > 0;
+    if (__ballot(lq > p.tpt)) n = (int)(((uint32_t)lq + p.tpt - 1) / (uint32_t)p.tpt);
+    if (!p.paged) {
+      const int64_t incl = wave_incl_scan((int64_t)kv);
+      koff = kacc + incl - kv;
+      kacc += lane_at(incl, 63);
+    }
+    nb = (int)(((uint32_t)keys_there(p, kv, koff) + kP - 1) / kP);
+  };
+  // Sizes in float32, which spares the prologue integer divisions; they and the
+  // quotients are taken low by more than what rounding adds, so that exact
+  // quotients stay whole, and the bound has a part more for that.
+  float total = 0.f;                             // of each lane, then of the wave
+  if (p.nsplit > 1) {
+    for (int base = 0; base < p.B; base += 64) {
+      load(base);
+      total += (float)n * (float)nb;
+    }
+    total = lane_at(wave_incl_scan(total), 63);
+  }
+  const float size = fmaxf(ceilf(total * p.per_target * 0.9999f), (float)p.min_blocks);
+  const float per_size = 0.9999f * __builtin_amdgcn_rcpf(size);
+  auto parts_of = [&]() -> int { return min((int)((float)nb * per_size) + 1, p.nsplit); };
+  auto take = [&](int b, int src, int off, int parts) {
+    r.parts = parts;
+    const int tin = parts == 1 ? off : (int)((uint32_t)off / (uint32_t)parts);
+    r.split = off - tin * parts;
+    set_tile(p, r.w, b, tin, lane_at(t0, src), lane_at(lq, src), lane_at(kv, src),
+             lane_at(koff, src));
+  };
+  if (p.B <= 64) {
+    if (p.nsplit == 1) load(0);
+    const int parts = parts_of();
+    // (the length of a part above the lane's number; lanes without a request
+    // come last)
+    const int len = n > 0 ? (int)((float)nb * __builtin_amdgcn_rcpf((float)parts)) : 0;
+    const int key = l < p.B ? len << 6 | (63 - l) : -l;
+    int rank = max(l - p.B, 0);
+    for (int j = 0; j < p.B; ++j) rank += lane_at(key, j) > key;
+    // lane i receives the number of the lane of rank i
+    const int from = __builtin_amdgcn_ds_permute(rank << 2, l);
+    const int units = __shfl(n * parts, from);
+    const int incl = wave_incl_scan(units);
+    if (unit >= lane_at(incl, 63)) return r;
+    const int at = __builtin_amdgcn_readfirstlane(__ffsll((long long)__ballot(incl > unit)) - 1);
+    const int src = lane_at(from, at);
+    take(src, src, unit - (lane_at(incl, at) - lane_at(units, at)), lane_at(parts, src));
+    return r;
+  }
+  int acc = 0;
+  kacc = 0;
+  for (int base = 0; base < p.B; base += 64) {
+    load(base);
+    const int parts = parts_of();
+    const int units = n * parts;
+    const int incl = wave_incl_scan(units);
+    const int sum = lane_at(incl, 63);
+    if (unit < acc + sum) {
+      const int src =
+          __builtin_amdgcn_readfirstlane(__ffsll((long long)__ballot(acc + incl > unit)) - 1);
+      take(base + src, src, unit - (acc + lane_at(incl, src) - lane_at(units, src)),
+           lane_at(parts, src));
+      return r;
+    }
+    acc += sum;
+  }
+  return r;
 }
 
 // Last visible key of the request's i-th new token: kv_len - L_q + i under
@@ -166,6 +271,22 @@ __device__ __forceinline__ void landed(i32x4& x) { asm volatile("" : "+v"(x)); }
 // maximum moves, so its bits do not depend on the rows it shares a tile with.)
 constexpr float kMaxLag = 8.f;
 
+// What the join needs to know of a row of a launch with split tiles, written by
+// its first part: that the row is whole (a NaN that no m is: m never is one), or
+// which parts there are not.  `lane` of `lanes` lanes.
+constexpr uint32_t kWholeBits = 0x7FEBCDEFu;
+__device__ __forceinline__ void mark_parts(const AttnParams& p, int64_t row, int parts, int lane,
+                                           int lanes) {
+  if (p.nsplit == 1) return;
+  const int64_t rows = p.T * p.Hq;
+  if (parts == 1) {
+    if (lane == 0) p.part_ml[row].x = __builtin_bit_cast(float, kWholeBits);
+    return;
+  }
+  for (int s = parts + lane; s < p.nsplit; s += lanes)
+    p.part_ml[s * rows + row] = float2{-__builtin_inff(), 0.f};
+}
+
 // NI copies of 1 KB, a wave's lanes' pieces at the byte offsets `of` of a raw
 // buffer of `bytes`; ONCE: rows that nobody else reads (the nontemporal hint).
 template <int NI, bool ONCE = false>
@@ -203,13 +324,23 @@ constexpr int kRowStage = 16384;     // 32 keys' K and V rows
 template <int KK, bool SEL, bool ONCE>
 __global__ __launch_bounds__(256, 1) void attn_rows_kernel(AttnParams p) {
   __shared__ __attribute__((aligned(16))) uint8_t ring[kRowWaves][2][kRowStage];
-  const int item = blockIdx.x;
-  const int split = item % p.nsplit;
-  int rest = item / p.nsplit;
+  int rest = blockIdx.x, split = 0, parts = 1;
+  if constexpr (SEL) {
+    split = rest % p.nsplit;
+    rest /= p.nsplit;
+  }
   const int hc = rest % p.hchunks;
   rest /= p.hchunks;
   const int hk = rest % p.Hkv;
-  const AttnTile w = attn_tile(p, rest / p.Hkv);
+  AttnTile w;
+  if constexpr (SEL) {
+    w = attn_tile(p, rest / p.Hkv);
+  } else {
+    const AttnPart part = attn_part(p, rest / p.Hkv);
+    w = part.w;
+    split = part.split;
+    parts = part.parts;
+  }
   if (!w.valid) return;
 
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -246,9 +377,10 @@ __global__ __launch_bounds__(256, 1) void attn_rows_kernel(AttnParams p) {
     sel = __builtin_amdgcn_ds_permute((ok ? rank : 63) << 2, e);
     if (l >= total) sel = -1;
   }
-  const int parts = max(1, min(p.nsplit, (total + p.min_blocks - 1) / p.min_blocks));
+  if constexpr (SEL) parts = max(1, min(p.nsplit, (total + p.min_blocks - 1) / p.min_blocks));
   const int b0 = (int)((int64_t)total * split / parts);
   const int b1 = split < parts ? (int)((int64_t)total * (split + 1) / parts) : b0;
+  if (SEL && split >= parts) return;
   const int nst = max(b1 - b0, 0);
 
   const int64_t out_row = ((int64_t)(w.t0 + ti) * p.Hq + hk * p.g + hg);
@@ -495,8 +627,10 @@ __global__ __launch_bounds__(256, 1) void attn_rows_kernel(AttnParams p) {
     s1 += a * *reinterpret_cast<const f32x4*>(src + 4);
   }
   if (!row_ok) return;
-  if (p.nsplit > 1) {
-    const int64_t pr = (int64_t)split * p.T * p.Hq + out_row;
+  const int64_t rows = p.T * p.Hq;
+  if (wave == 0 && split == 0) mark_parts(p, out_row, parts, G, 4);
+  if (parts > 1) {
+    const int64_t pr = split * rows + out_row;
     if (wave == 0 && G == 0) p.part_ml[pr] = float2{mt, lt};
     if (nst > 0) {
       float* dst = p.part_o + pr * kD + 32 * wave + 8 * G;
@@ -530,8 +664,9 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnParams p) {
   float2 ml = {-__builtin_inff(), 0.f};
   if (l < p.nsplit) ml = p.part_ml[l * rows + row];
   if (row >= (int64_t)max(p.cu_q[p.B], 0) * p.Hq || row < (int64_t)p.cu_q[0] * p.Hq) return;
-  // parts of a row that is in no request, or that the tile did not need, hold
-  // no sums: l = 0 (NaN where anything seen was no number)
+  if ((uint32_t)lane_at(__builtin_bit_cast(int, ml.x), 0) == kWholeBits) return;
+  // parts that the tile did not need, or that saw nothing, hold no sums: l = 0
+  // (NaN where anything seen was no number)
   float mt = max_xor32(max_xor16(ml.x));
 #pragma unroll
   for (int d = 8; d > 0; d >>= 1) mt = fmaxf(mt, __shfl_xor(mt, d));
@@ -631,8 +766,9 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tile_kernel(AttnParams p) {
   const int lim_hi = attn_last(p, w, w.i0 + w.ntok - 1);
   const int total = lim_hi >= 0 ? lim_hi / kP + 1 : 0;
   const int parts = max(1, min(p.nsplit, (total + p.min_blocks - 1) / p.min_blocks));
+  if (split >= parts) return;
   const int b0 = (int)((int64_t)total * split / parts);
-  const int b1 = split < parts ? (int)((int64_t)total * (split + 1) / parts) : b0;
+  const int b1 = (int)((int64_t)total * (split + 1) / parts);
 
   i32x4 qv[8];
 #pragma unroll
@@ -919,7 +1055,8 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tile_kernel(AttnParams p) {
   if (!row_ok) return;
   const int64_t out_row = ((int64_t)(w.t0 + ti) * p.Hq + hk * p.g + hg);
   // register r of o[d] is head element 32 d + 8 (r / 4) + 4 h + r % 4
-  if (p.nsplit > 1) {
+  if (split == 0) mark_parts(p, out_row, parts, h, 2);
+  if (parts > 1) {
     const int64_t pr = (int64_t)split * p.T * p.Hq + out_row;
     if (h == 0) p.part_ml[pr] = float2{m, lsum};
     if (b0 < b1) {
@@ -1011,8 +1148,9 @@ __global__ __launch_bounds__(64 * NW, 4) void attn_union_kernel(AttnParams p) {
   const int lim_hi = attn_last(p, w, w.i0 + w.ntok - 1);
   const int total = lim_hi >= 0 ? lim_hi / kP + 1 : 0;
   const int parts = max(1, min(p.nsplit, (total + p.min_blocks - 1) / p.min_blocks));
+  if (split >= parts) return;
   const int b0 = (int)((int64_t)total * split / parts);
-  const int b1 = split < parts ? (int)((int64_t)total * (split + 1) / parts) : b0;
+  const int b1 = (int)((int64_t)total * (split + 1) / parts);
 
   i32x4 qv[4];
 #pragma unroll
@@ -1333,7 +1471,8 @@ __global__ __launch_bounds__(64 * NW, 4) void attn_union_kernel(AttnParams p) {
   if (!row_ok) return;
   const int64_t out_row = ((int64_t)(w.t0 + ti) * p.Hq + hk * p.g + hg);
   // register r of o[d] is head element 16 d + 4 G + r
-  if (p.nsplit > 1) {
+  if (split == 0) mark_parts(p, out_row, parts, G, 4);
+  if (parts > 1) {
     const int64_t pr = (int64_t)split * p.T * p.Hq + out_row;
     if (G == 0) p.part_ml[pr] = float2{m, lsum};
     if (b0 < b1) {

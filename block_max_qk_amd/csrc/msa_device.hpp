@@ -87,6 +87,10 @@ __device__ __forceinline__ int64_t dpp_or_zero(int64_t v) {
   const uint32_t hi = (uint32_t)dpp_or_zero<CTRL, ROWS>((int)(uint32_t)((uint64_t)v >> 32));
   return (int64_t)(((uint64_t)hi << 32) | lo);
 }
+template <int CTRL, int ROWS>
+__device__ __forceinline__ float dpp_or_zero(float x) {
+  return __builtin_bit_cast(float, dpp_or_zero<CTRL, ROWS>(__builtin_bit_cast(int, x)));
+}
 template <typename T>
 __device__ __forceinline__ T wave_incl_scan(T x) {
   x += dpp_or_zero<0x111, 0xF>(x);
@@ -106,6 +110,9 @@ __device__ __forceinline__ int64_t lane_at(int64_t x, int src) {
   const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)x, src);
   const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)((uint64_t)x >> 32), src);
   return (int64_t)(((uint64_t)hi << 32) | lo);
+}
+__device__ __forceinline__ float lane_at(float x, int src) {
+  return __builtin_bit_cast(float, lane_at(__builtin_bit_cast(int, x), src));
 }
 
 // Value of another lane in the same row of 16, by a DPP lane pattern.

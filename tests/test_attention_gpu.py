@@ -358,6 +358,37 @@ def test_large_batch(dev):
     run(lc.attention_case(q, kv, 4, 2, k=2, seed=27), dev)
 
 
+@pytest.mark.parametrize("layout", ["BBND", "TND"])
+@pytest.mark.parametrize("q_lens,kv_lens,Hq,Hkv,k", [
+    ([1] * 9, [9000, 1, 0, 130, 128, 127, 300, 40, 6000], 16, 2, 0),
+    ([0, 1, 0, 1], [500, 2049, 0, 1], 8, 1, 0),
+    ([5, 1, 7, 2, 0, 3, 1, 1, 1, 1, 1, 1], [4000, 1500, 7, 1, 10, 2600] + [1025] * 6, 8, 2, 0),
+    ([1, 1, 1], [3000, 1600, 90], 40, 2, 0),
+    ([1] * 64, [5000] + [100 * (i % 13) for i in range(63)], 4, 2, 0),
+    ([1, 0] * 65, [64 * (i % 40) for i in range(129)] + [7000], 4, 1, 0),
+    ([300, 20, 1, 40], [9000, 20, 3000, 700], 16, 2, 0),
+    ([120, 9, 0, 2], [9000, 40, 300, 2], 16, 8, 6),
+    ([1, 1, 1, 1], [9000, 40, 0, 2500], 16, 4, 20),
+])
+def test_uneven_batches(layout, q_lens, kv_lens, Hq, Hkv, k, dev):
+    """Long requests in many parts beside whole ones, and requests of none;
+    nothing is read of the workspace that the call did not write."""
+    import block_max_qk_amd as m
+    c = lc.attention_case(q_lens, kv_lens, Hq, Hkv, layout, k=k, seed=80)
+    d = to(c, dev)
+    mb = d["table"].shape[1] if d["table"] is not None else (d["k"].shape[0] + 127) // 128
+    need = m.msa_attention_workspace(d["q"].shape[0], len(q_lens), Hq, Hkv, mb,
+                                     0 if d["blocks"] is None else d["blocks"].shape[2])
+    got = []
+    for fill in (255, 0x41):
+        ws = torch.full((need + 64,), fill, dtype=torch.uint8, device=dev)
+        got.append(call(d, workspace=ws[:need]) if need else call(d))
+        torch.cuda.synchronize()
+        assert (ws[need:] == fill).all()
+    check(c, *got[0])
+    assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+
+
 def test_same_bits_every_time(dev):
     for c in (lc.attention_case([1, 1], [5000, 129], 16, 2, seed=28),
               lc.attention_case([200], [1000], 16, 2, seed=29),
