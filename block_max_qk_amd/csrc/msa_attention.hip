@@ -23,6 +23,7 @@ struct Plan {
   int hpt, tpt, hchunks;
   int64_t ntiles;
   int nsplit, min_blocks, target;
+  bool balanced;
   int64_t units;     // workgroups (attn_union_kernel: tiles x parts)
   bool once;         // no two workgroups read the same rows of keys
 };
@@ -49,15 +50,23 @@ struct Plan {
 // in 512; 800 tokens over selected blocks: 99 us in 256 parts, 114 in 512; one
 // prompt of 1000 tokens: 27 us unsplit, 39 in two parts of 4 blocks.)
 //
-// Dense tiles of 16 rows are split by their own lengths (attn_part), aiming at
-// 192 parts, three quarters of the CUs, which leaves the rounding up room in one
-// round of workgroups.  (8 KV heads, one token each; 24 requests of 1024 keys 23
-// us, of up to 4096 32 us, of 512 and one of 8192 32 us; the same number of parts
-// for every tile, 1536 in all: 29, 46 and 58 us; aiming at 128, 256 and 512
-// parts: 23, 48 and 37; 30, 47 and 30; 29, 50 and 36 us.  64 requests of up to
-// 8192 keys: 194 us, 196 with 1536 even parts.)  A cache of fewer than 8 blocks
-// is not worth the second kernel (4 blocks: 8.2 us, 9.1 in two parts), nor are
-// more than 1024 tiles.
+// Dense tiles of 16 rows, and larger ones of more than one request, are split
+// by their own lengths (attn_part), aiming at 192 parts, three quarters of the
+// CUs, which leaves the rounding up room in one round of workgroups, and at
+// twice as many of 128 rows, of which a CU holds two.
+//  - 16 rows: 24 requests of one token, 8 KV heads; all of 1024 keys, of up to
+//    4096, or of 1024 and one of 8192: 23, 42 and 32 us; aiming at 128 parts
+//    23, 48 and 37, at 256 30, 47 and 30, at 512 29, 50 and 36; every tile in
+//    the same number of parts, 1536 in all, 29, 53 and 58.  64 requests of up
+//    to 8192 keys: 194 us, 196 in 1536 even parts.
+//  - 128 rows: 100, 300, 40 and 20 tokens over 32768, 400, 900 and 20 keys: 87
+//    us, 94 aiming at 192, 155 in even parts; 9 requests of 2 to 258 tokens: 66
+//    us, 74 in even parts.
+//  - 256 rows: 8 requests of 200 tokens over 2048 keys: 69 us, 94 aiming at
+//    384, 90 in even parts.
+// Not split are caches of fewer than 8 blocks (16 for the larger tiles; 4 blocks
+// 8.2 us, 9.1 in two parts), 1024 tiles and more, and what would write partial
+// sums of more than 2^18 rows (136 MB).
 Plan plan_for(int64_t T, int64_t B, int64_t Hq, int64_t Hkv, int64_t MB, int64_t nsel) {
   Plan p{};
   const int64_t g = Hq / Hkv;
@@ -79,15 +88,17 @@ Plan plan_for(int64_t T, int64_t B, int64_t Hq, int64_t Hkv, int64_t MB, int64_t
   const int64_t want = nsel > 0 ? (few ? 128 : 256) : few ? 1536 : p.rows == 128 ? 512 : 256;
   int64_t n = items >= want ? 1 : (want + items - 1) / items;
   p.target = 1;
-  if (few && nsel == 0) {
+  if (nsel == 0 && (few || B > 1)) {
     const int64_t heads = Hkv * p.hchunks;
-    p.target = (int)std::max<int64_t>(192 / heads, 1);
-    n = items >= 1024 || MB < 8 ? 1 : std::min<int64_t>(p.target, std::max<int64_t>(8192 / items, 1));
+    p.target = (int)std::max<int64_t>((p.rows == 128 ? 384 : 192) / heads, 1);
+    n = items >= 1024 || MB < (few ? 8 : 16) ? 1
+        : std::min<int64_t>(p.target, std::max<int64_t>((1 << 18) / (T * Hq), 1));
+    p.balanced = true;
   }
   n = std::min(n, (blocks + p.min_blocks - 1) / p.min_blocks);
   p.nsplit = (int)std::max<int64_t>(1, std::min(n, kMaxSplit));
   p.units = p.ntiles * Hkv * p.hchunks * p.nsplit;
-  if (few && nsel == 0 && p.nsplit > 1) p.units = (p.target + 1 + p.ntiles) * Hkv * p.hchunks;
+  if (p.balanced && p.nsplit > 1) p.units = (p.target + 1 + p.ntiles) * Hkv * p.hchunks;
   return p;
 }
 
@@ -113,7 +124,8 @@ hipError_t launch(const AttnParams& p, const Plan& plan, int64_t grid, hipStream
     e = msa::launch_kernel(msa::attn_tile_kernel<KK, 4>, gr, dim3(256), s, p);
   }
   if (e == hipSuccess && p.nsplit > 1)
-    e = msa::launch_kernel(msa::attn_join_kernel<KK>, dim3((unsigned)((p.T * p.Hq + 3) / 4)),
+    e = msa::launch_kernel(msa::attn_join_kernel<KK>,
+                           dim3((unsigned)((p.T * p.Hq + 4 * p.join_rows - 1) / (4 * p.join_rows))),
                            dim3(256), s, p);
   return e;
 }
@@ -185,7 +197,7 @@ msa_status_t run(const msa_tensor_t* query, const msa_tensor_t* key, const msa_t
   // (a launch holds less than 2^32 threads)
   const int64_t threads = plan.rows == 256 || (selected && plan.rows == 128) ? 512 : 256;
   if (grid * threads > UINT32_MAX ||
-      (plan.nsplit > 1 && (T * Hq + 3) / 4 * 256 > (int64_t)UINT32_MAX))
+      (plan.nsplit > 1 && T * Hq * 64 > (int64_t)UINT32_MAX))
     return MSA_ERR_SHAPE;
 
   AttnParams p{};
@@ -226,6 +238,8 @@ msa_status_t run(const msa_tensor_t* query, const msa_tensor_t* key, const msa_t
   p.ntiles = (int32_t)plan.ntiles;
   p.nsplit = plan.nsplit;
   p.min_blocks = plan.min_blocks;
+  p.balanced = plan.balanced ? 1 : 0;
+  p.join_rows = (int32_t)std::clamp<int64_t>(T * Hq / 8192, 1, 64);   // the chip holds 8192 waves
   p.per_target = 1.f / plan.target;
   hipStream_t s = static_cast<hipStream_t>(stream);
   const hipError_t e = query->dtype == MSA_DTYPE_BF16 ? launch<msa::KBF16>(p, plan, grid, s)

@@ -50,6 +50,8 @@ struct AttnParams {
   int32_t hpt, tpt, hchunks, ntiles;      // as in Params
   int32_t nsplit;              // parts that a tile's blocks are split into, at most
   int32_t min_blocks;          // blocks per part at least
+  int32_t join_rows;           // rows of a wave of attn_join_kernel
+  int32_t balanced;            // dense tiles are split by attn_part
   float per_target;            // 1 / the parts per KV head that attn_part aims at
 };
 
@@ -172,9 +174,10 @@ __device__ __forceinline__ AttnPart attn_part(const AttnParams& p, int unit) {
   auto parts_of = [&]() -> int { return min((int)((float)nb * per_size) + 1, p.nsplit); };
   auto take = [&](int b, int src, int off, int parts) {
     r.parts = parts;
+    // (a request's last tiles first)
     const int tin = parts == 1 ? off : (int)((uint32_t)off / (uint32_t)parts);
     r.split = off - tin * parts;
-    set_tile(p, r.w, b, tin, lane_at(t0, src), lane_at(lq, src), lane_at(kv, src),
+    set_tile(p, r.w, b, lane_at(n, src) - 1 - tin, lane_at(t0, src), lane_at(lq, src), lane_at(kv, src),
              lane_at(koff, src));
   };
   if (p.B <= 64) {
@@ -648,8 +651,9 @@ __global__ __launch_bounds__(256, 1) void attn_rows_kernel(AttnParams p) {
 }
 
 // ---------------------------------------------------------------------------
-// The join of a split tile's parts: one wave per row, half a wave per part (32
-// lanes of 16 bytes are a part's row), two pairs of parts in flight.  Bound by
+// The join of a split tile's parts: a wave takes join_rows rows, of which it
+// passes over those that were not split, one by one with half a wave per part
+// (32 lanes of 16 bytes are a part's row), two pairs of parts in flight.  Bound by
 // latency and then memory: 4096 rows in 3 parts 4.7 us, 22624 rows in 3 parts
 // (41 MB) 9.7 us, 11.7 with a whole wave per part, one after the other.  Rows
 // that no request holds are left as they are.
@@ -657,46 +661,52 @@ __global__ __launch_bounds__(256, 1) void attn_rows_kernel(AttnParams p) {
 
 template <int KK>
 __global__ __launch_bounds__(256) void attn_join_kernel(AttnParams p) {
-  const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
   const int l = lane_id();
   const int64_t rows = p.T * p.Hq;
-  if (row >= rows) return;
-  float2 ml = {-__builtin_inff(), 0.f};
-  if (l < p.nsplit) ml = p.part_ml[l * rows + row];
-  if (row >= (int64_t)max(p.cu_q[p.B], 0) * p.Hq || row < (int64_t)p.cu_q[0] * p.Hq) return;
-  if ((uint32_t)lane_at(__builtin_bit_cast(int, ml.x), 0) == kWholeBits) return;
-  // parts that the tile did not need, or that saw nothing, hold no sums: l = 0
-  // (NaN where anything seen was no number)
-  float mt = max_xor32(max_xor16(ml.x));
+  const int64_t end = min(rows, (int64_t)max(p.cu_q[p.B], 0) * p.Hq);
+  const int64_t from = ((int64_t)blockIdx.x * 4 + (threadIdx.x >> 6)) * p.join_rows;
+  // which of the wave's rows are in parts
+  bool open = false;
+  if (l < p.join_rows && from + l < end && from + l >= (int64_t)p.cu_q[0] * p.Hq)
+    open = __builtin_bit_cast(uint32_t, p.part_ml[from + l].x) != kWholeBits;
+  for (unsigned long long todo = __ballot(open); todo; todo &= todo - 1) {
+    const int64_t row = from + (__ffsll((long long)todo) - 1);
+    // parts that the tile did not need, or that saw nothing, hold no sums: l = 0
+    // (NaN where anything seen was no number)
+    float2 ml = {-__builtin_inff(), 0.f};
+    if (l < p.nsplit) ml = p.part_ml[l * rows + row];
+    float mt = max_xor32(max_xor16(ml.x));
 #pragma unroll
-  for (int d = 8; d > 0; d >>= 1) mt = fmaxf(mt, __shfl_xor(mt, d));
-  const float ms = mt == -__builtin_inff() ? 0.f : mt;
-  const float a = ml.y == 0.f ? 0.f : exp2_hw(ml.x - ms);
-  float lt = sum_xor32(sum_xor16(a * ml.y));
+    for (int d = 8; d > 0; d >>= 1) mt = fmaxf(mt, __shfl_xor(mt, d));
+    const float ms = mt == -__builtin_inff() ? 0.f : mt;
+    const float a = ml.y == 0.f ? 0.f : exp2_hw(ml.x - ms);
+    float lt = sum_xor32(sum_xor16(a * ml.y));
 #pragma unroll
-  for (int d = 8; d > 0; d >>= 1) lt += __shfl_xor(lt, d);
-  const int half = l >> 5;
-  const unsigned long long filled = __ballot(ml.y != 0.f);
-  auto part = [&](int s) -> f32x4 {      // its share of elements 4 (l % 32) .. + 3
-    const f32x4 none = {0.f, 0.f, 0.f, 0.f};
-    if (!(filled >> s & 1)) return none;
-    return *reinterpret_cast<const f32x4*>(p.part_o + (s * rows + row) * kD + 4 * (l & 31));
-  };
-  f32x4 o = {0.f, 0.f, 0.f, 0.f};
-  for (int s = 0; s < p.nsplit; s += 4) {
-    const int s0 = s + half, s1 = s + 2 + half;      // (at most 66: tested before use)
-    const f32x4 x0 = s0 < p.nsplit ? part(s0) : f32x4{0.f, 0.f, 0.f, 0.f};
-    const f32x4 x1 = s1 < p.nsplit ? part(s1) : f32x4{0.f, 0.f, 0.f, 0.f};
-    o += __shfl(a, s0 & 63) * x0 + __shfl(a, s1 & 63) * x1;
+    for (int d = 8; d > 0; d >>= 1) lt += __shfl_xor(lt, d);
+    const int half = l >> 5;
+    const unsigned long long filled = __ballot(ml.y != 0.f);
+    auto part = [&](int s) -> f32x4 {      // its share of elements 4 (l % 32) .. + 3
+      const f32x4 none = {0.f, 0.f, 0.f, 0.f};
+      if (!(filled >> s & 1)) return none;
+      return *reinterpret_cast<const f32x4*>(p.part_o + (s * rows + row) * kD + 4 * (l & 31));
+    };
+    f32x4 o = {0.f, 0.f, 0.f, 0.f};
+    for (int s = 0; s < p.nsplit; s += 4) {
+      if (!(filled >> s)) break;
+      const int s0 = s + half, s1 = s + 2 + half;      // (at most 66: tested before use)
+      const f32x4 x0 = s0 < p.nsplit ? part(s0) : f32x4{0.f, 0.f, 0.f, 0.f};
+      const f32x4 x1 = s1 < p.nsplit ? part(s1) : f32x4{0.f, 0.f, 0.f, 0.f};
+      o += __shfl(a, s0 & 63) * x0 + __shfl(a, s1 & 63) * x1;
+    }
+#pragma unroll
+    for (int r = 0; r < 4; ++r) o[r] = sum_xor32(o[r]);
+    const float inv = lt == 0.f ? 0.f : 1.f / lt;
+    if (half == 0)
+      *reinterpret_cast<i32x2*>(p.out + row * (2 * kD) + 8 * l) =
+          i32x2{pack2<KK>(o[0] * inv, o[1] * inv), pack2<KK>(o[2] * inv, o[3] * inv)};
+    if (p.lse && l == 0)
+      p.lse[row] = lt == 0.f ? -__builtin_inff() : (mt + __log2f(lt)) * kLn2;
   }
-#pragma unroll
-  for (int r = 0; r < 4; ++r) o[r] = sum_xor32(o[r]);
-  const float inv = lt == 0.f ? 0.f : 1.f / lt;
-  if (half == 0)
-    *reinterpret_cast<i32x2*>(p.out + row * (2 * kD) + 8 * l) =
-        i32x2{pack2<KK>(o[0] * inv, o[1] * inv), pack2<KK>(o[2] * inv, o[3] * inv)};
-  if (p.lse && l == 0)
-    p.lse[row] = lt == 0.f ? -__builtin_inff() : (mt + __log2f(lt)) * kLn2;
 }
 
 // ---------------------------------------------------------------------------
@@ -743,14 +753,25 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tile_kernel(AttnParams p) {
   // heavy tiles (the last tokens of a request see the most keys) first; the
   // KV head changes fastest, so that with 8 XCDs taking workgroups in turn an
   // XCD's L2 holds the keys of few heads
-  int rest = blockIdx.x;
-  const int split = rest % p.nsplit;
-  rest /= p.nsplit;
+  int rest = blockIdx.x, split = 0;
+  if (!p.balanced) {
+    split = rest % p.nsplit;
+    rest /= p.nsplit;
+  }
   const int hc = rest % p.hchunks;
   rest /= p.hchunks;
   const int hk = rest % p.Hkv;
-  const int tile = p.ntiles - 1 - rest / p.Hkv;
-  const AttnTile w = attn_tile(p, tile);
+  rest /= p.Hkv;
+  AttnTile w;
+  int parts = p.nsplit;
+  if (p.balanced) {
+    const AttnPart part = attn_part(p, rest);
+    w = part.w;
+    split = part.split;
+    parts = part.parts;
+  } else {
+    w = attn_tile(p, p.ntiles - 1 - rest);
+  }
   if (!w.valid) return;
 
   const int tid = threadIdx.x;
@@ -765,7 +786,7 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tile_kernel(AttnParams p) {
   const int lim_lo = attn_last(p, w, w.i0);
   const int lim_hi = attn_last(p, w, w.i0 + w.ntok - 1);
   const int total = lim_hi >= 0 ? lim_hi / kP + 1 : 0;
-  const int parts = max(1, min(p.nsplit, (total + p.min_blocks - 1) / p.min_blocks));
+  parts = max(1, min(parts, (total + p.min_blocks - 1) / p.min_blocks));
   if (split >= parts) return;
   const int b0 = (int)((int64_t)total * split / parts);
   const int b1 = (int)((int64_t)total * (split + 1) / parts);
