@@ -314,10 +314,12 @@ __device__ __forceinline__ void copy_rows(uint8_t* dst, const uint8_t* src, int 
 // four waves' results are joined through LDS at the end.  The bound is the
 // reading of keys and values: each wave copies its 16 KB of a block straight
 // into its own part of the LDS, one block ahead, with no barrier in the loop.
-// ONCE: no other workgroup reads the same rows, and the copies say so (64
-// requests of up to 8192 keys, 8 KV heads: 219 us without the hint, 199 with
-// it, 1.17 GB; where tokens share their selected blocks the hint costs as much
-// as it gains here).  Stages of 16 keys with two workgroups a CU instead: 207 us.
+// 64 requests of up to 8192 keys, 8 KV heads, 1.17 GB: 190 us, 6.2 TB/s, which is
+// what a large read reaches.
+// ONCE: no other workgroup reads the same rows, and the copies say so (the same
+// requests in 1536 even parts: 219 us without the hint, 199 with it; where tokens
+// share their selected blocks the hint costs as much as it gains here).  Stages
+// of 16 keys with two workgroups a CU instead: 207 us.
 // ---------------------------------------------------------------------------
 
 constexpr int kAttnRows = 16;
@@ -654,9 +656,10 @@ __global__ __launch_bounds__(256, 1) void attn_rows_kernel(AttnParams p) {
 // The join of a split tile's parts: a wave takes join_rows rows, of which it
 // passes over those that were not split, one by one with half a wave per part
 // (32 lanes of 16 bytes are a part's row), two pairs of parts in flight.  Bound by
-// latency and then memory: 4096 rows in 3 parts 4.7 us, 22624 rows in 3 parts
-// (41 MB) 9.7 us, 11.7 with a whole wave per part, one after the other.  Rows
-// that no request holds are left as they are.
+// latency and then memory: 4096 whole rows 2.8 us, 4096 in 3 parts 4.7, 22624
+// rows in up to 6 parts 9.4; in 3 parts (41 MB) 9.7 us against 11.7 with a whole
+// wave per part, one after the other.  Rows that no request holds are left as
+// they are.
 // ---------------------------------------------------------------------------
 
 template <int KK>
