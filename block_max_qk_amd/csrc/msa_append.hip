@@ -31,15 +31,14 @@ msa_status_t item_for(const msa_append_item_t& in, int64_t T, AppendItem& a) {
   const msa_tensor_t& dst = in.dst;
   if (in.layout < MSA_LAYOUT_TND || in.layout > MSA_LAYOUT_ROWS) return MSA_ERR_LAYOUT;
   if (in.rotate != 0 && in.rotate != 1) return MSA_ERR_ATTR;
-  if (msa::elem_bytes(dst.dtype) == 0 || (msa::elem_bytes(dst.dtype) == 2 && dst.dtype != src.dtype))
-    return MSA_ERR_DTYPE;
+  const int eb = msa::elem_bytes(dst.dtype);
+  if (eb == 0 || (eb == 2 && dst.dtype != src.dtype)) return MSA_ERR_DTYPE;
   const bool i8 = dst.dtype == MSA_DTYPE_I8, mx = dst.dtype == MSA_DTYPE_MXFP4;
   if (T > 0 && (i8 || mx) != (in.scale != nullptr)) return MSA_ERR_SCALE;
   if (src.ndim != 3 || src.shape[0] != T || src.shape[1] < 1 || src.shape[1] > 65536 ||
       src.shape[2] != msa::kD)
     return MSA_ERR_SHAPE;
   const int64_t H = src.shape[1], last = mx ? msa::kD / 2 : msa::kD;
-  const int eb = msa::elem_bytes(dst.dtype);
   a.src_row = (T > 1 ? src.stride[0] : 0) * 2;
   a.src_head = (H > 1 ? src.stride[1] : 0) * 2;
   if (src.stride[2] != 1 || a.src_row < 0 || a.src_head < 0 || a.src_row % 16 || a.src_head % 16 ||

@@ -177,8 +177,8 @@ __device__ __forceinline__ AttnPart attn_part(const AttnParams& p, int unit) {
     // (a request's last tiles first)
     const int tin = parts == 1 ? off : (int)((uint32_t)off / (uint32_t)parts);
     r.split = off - tin * parts;
-    set_tile(p, r.w, b, lane_at(n, src) - 1 - tin, lane_at(t0, src), lane_at(lq, src), lane_at(kv, src),
-             lane_at(koff, src));
+    set_tile(p, r.w, b, lane_at(n, src) - 1 - tin, lane_at(t0, src), lane_at(lq, src),
+             lane_at(kv, src), lane_at(koff, src));
   };
   if (p.B <= 64) {
     if (p.nsplit == 1) load(0);
@@ -853,7 +853,8 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tile_kernel(AttnParams p) {
   // there are to the tile's last visible one.
   struct Rows { const uint8_t *k, *v; int kb, vb; };
   auto rows_of = [&](const Entry& x, int in) -> Rows {
-    const int left = x.there ? max(0, min(kTileKeys, lim_hi + 1 - x.beta * kP - in * kTileKeys)) : 0;
+    const int left =
+        x.there ? max(0, min(kTileKeys, lim_hi + 1 - x.beta * kP - in * kTileKeys)) : 0;
     return Rows{p.k + x.k + in * kTileKeys * p.k_row_stride,
                 p.v + x.v + in * kTileKeys * p.v_row_stride,
                 __builtin_amdgcn_readfirstlane(left * p.k_row_stride),
@@ -867,7 +868,8 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tile_kernel(AttnParams p) {
       const int row = (wave * NI + i) * 4 + cr;
       const int at = (wave * NI + i) * 1024 + 16 * l;
       const i32x4 zero = {0, 0, 0, 0};
-      *reinterpret_cast<i32x4*>(kring + at) = row * p.k_row_stride < r.kb ? ld16(r.k + kof[i]) : zero;
+      *reinterpret_cast<i32x4*>(kring + at) =
+          row * p.k_row_stride < r.kb ? ld16(r.k + kof[i]) : zero;
       *reinterpret_cast<i32x4*>(vring + at) =
           row * p.v_row_stride < r.vb ? ld16(r.v + vof[i]) : zero;
     }
@@ -1142,8 +1144,9 @@ __global__ __launch_bounds__(64 * NW, 4) void attn_union_kernel(AttnParams p) {
   __shared__ __attribute__((aligned(16))) uint8_t lds[kFlagAt + 16];
   uint8_t* const kring = lds;                                       // [2][64 K rows]
   uint8_t* const vring = lds + 2 * SB;                              // [2][64 V rows]
-  uint32_t* const marks = reinterpret_cast<uint32_t*>(lds + kMarksAt);   // [token][block of the span]
-  uint16_t* const named = reinterpret_cast<uint16_t*>(lds + kNamedAt);   // the span's blocks, ascending
+  // [token][block of the span], and the span's blocks in ascending order
+  uint32_t* const marks = reinterpret_cast<uint32_t*>(lds + kMarksAt);
+  uint16_t* const named = reinterpret_cast<uint16_t*>(lds + kNamedAt);
   int* const flag = reinterpret_cast<int*>(lds + kFlagAt);
   // an XCD takes runs of 8 consecutive tiles of one KV head, which have most
   // of their blocks in common
@@ -1234,7 +1237,8 @@ __global__ __launch_bounds__(64 * NW, 4) void attn_union_kernel(AttnParams p) {
   // there are to the tile's last visible one.
   struct Rows { const uint8_t *k, *v; int kb, vb; };
   auto rows_of = [&](const Entry& x, int in) -> Rows {
-    const int left = x.there ? max(0, min(kTileKeys, lim_hi + 1 - x.beta * kP - in * kTileKeys)) : 0;
+    const int left =
+        x.there ? max(0, min(kTileKeys, lim_hi + 1 - x.beta * kP - in * kTileKeys)) : 0;
     return Rows{p.k + x.k + in * kTileKeys * p.k_row_stride,
                 p.v + x.v + in * kTileKeys * p.v_row_stride,
                 __builtin_amdgcn_readfirstlane(left * p.k_row_stride),
@@ -1248,7 +1252,8 @@ __global__ __launch_bounds__(64 * NW, 4) void attn_union_kernel(AttnParams p) {
       const int row = (wave * NI + i) * 4 + cr;
       const int at = (wave * NI + i) * 1024 + 16 * l;
       const i32x4 zero = {0, 0, 0, 0};
-      *reinterpret_cast<i32x4*>(kring + at) = row * p.k_row_stride < r.kb ? ld16(r.k + kof[i]) : zero;
+      *reinterpret_cast<i32x4*>(kring + at) =
+          row * p.k_row_stride < r.kb ? ld16(r.k + kof[i]) : zero;
       *reinterpret_cast<i32x4*>(vring + at) =
           row * p.v_row_stride < r.vb ? ld16(r.v + vof[i]) : zero;
     }
