@@ -266,3 +266,39 @@ def test_workspace_of_the_caller(dev):
     assert (ws[need:] == 255).all()
     with pytest.raises(m.MsaError):
         call(d, workspace=ws[:need - 16])
+
+
+@pytest.mark.parametrize("T,Hq,Hkv,k,steps", [
+    # a decode loop's graph: slots fill and empty, one request runs far ahead
+    (8, 16, 2, 0, [([1] * 8, [100] * 8), ([1] * 5 + [0] * 3, [4000, 1, 0, 129, 128, 0, 7, 300]),
+                   ([2, 0, 3, 0, 0, 1, 0, 0], [5000, 9, 3, 1, 0, 1025, 0, 0])]),
+    # chunks of changing shares of the same rows
+    (200, 16, 2, 0, [([100, 100], [100, 100]), ([190, 1], [2900, 2900]), ([0, 150], [5, 150])]),
+    (8, 16, 2, 4, [([1] * 8, [900] * 8), ([3, 1] + [0] * 6, [4000, 1] + [0] * 6)]),
+    (300, 16, 4, 4, [([150, 150], [600, 150]), ([299, 0], [3000, 40]), ([1, 100], [2000, 2000])]),
+])
+def test_graph_with_new_lengths(T, Hq, Hkv, k, steps, dev):
+    """One captured call, replayed as the lengths in its tensors change: the
+    split follows them, within the launch that was captured."""
+    B, width = len(steps[0][0]), 40
+    gen = torch.Generator().manual_seed(90 + T)
+    c = lc.attention_case([0] * B, [128 * width] * B, Hq, Hkv, T_extra=T, k=k, seed=91)
+    d = to(c, dev)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        out, lse = call(d)
+    torch.cuda.current_stream().wait_stream(s)
+    for q_lens, kv_lens in steps + steps[:1]:
+        cu, _ = lc.lengths(q_lens, T - sum(q_lens), 0)
+        kv = torch.tensor(kv_lens, dtype=torch.int32)
+        c["q"] = torch.randn(T, Hq, 128, generator=gen).to(BF)
+        c["cu"], c["kv"] = cu, kv
+        for n in ("q", "cu", "kv"):
+            d[n].copy_(c[n])
+        g.replay()
+        torch.cuda.synchronize()
+        n = int(cu[-1])
+        check(c, out, lse)
+        assert torch.isnan(out[n:]).all() and torch.isnan(lse[n:]).all()
