@@ -715,10 +715,13 @@ def _outputs(query, return_lse, stream):
     if stream is not None and query.is_cuda:
         with torch.cuda.stream(_stream_of(_stream_handle(stream, query.device), query.device)):
             return _outputs(query, return_lse, None)
+    shape = query.shape
+    if len(shape) != 3:
+        raise ValueError(f"query must be [T, Hq, 128], got {tuple(shape)}")
     out = torch.empty_like(query, memory_format=torch.contiguous_format)
     if not return_lse:
         return out, None
-    return out, torch.empty(query.shape[:2], dtype=torch.float32, device=query.device)
+    return out, query.new_empty((shape[0], shape[1]), dtype=torch.float32)
 
 
 def _default_blocks(key, block_table) -> int:

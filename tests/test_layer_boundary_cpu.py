@@ -354,3 +354,15 @@ def test_launches_hold_less_than_2_32_threads():
     one = dict(layout=ROWS, rotate=0)
     assert append(item(src=dims((T, 2, 128)), dst=dims((T, 2, 128)), **one), table=None,
                   mb=0) == SHAPE
+
+
+def test_allocating_forms_reject():
+    a = args(T=0)
+    rest = (a["key"], a["value"], a["block_table"], a["cu_seqlens_q"], a["kv_len"], "BBND")
+    for q in (torch.zeros(16, 128, dtype=torch.float16), torch.zeros(128, dtype=torch.float16)):
+        with pytest.raises(ValueError):
+            m.attention(q, *rest)
+        with pytest.raises(ValueError):
+            m.block_attention(q, *rest[:2], torch.zeros(0, 2, 4, dtype=torch.int32), *rest[2:])
+    with pytest.raises(ValueError):
+        m.block_attention(a["query"], *rest[:2], None, *rest[2:])
