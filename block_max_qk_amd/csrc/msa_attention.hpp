@@ -3,12 +3,12 @@
 // blocks that the top-k selection names (msa_block_attention).
 //
 //   S = c <q, k_j>, c = softmax_scale * log2(e), over the visible j
-//   m = max S,  l = sum 2^(S - m),  out = sum 2^(S - m) v_j / l,
-//   lse = ln 2 (m + log2 l)
+//   l = sum 2^(S - m),  out = sum 2^(S - m) v_j / l,  lse = ln 2 (m + log2 l)
 //
-// in one pass over the keys with the running m and l.  Both products are taken
-// transposed, with the keys (then the head elements) as the MFMA's M side and
-// the rows -- (query token, head) pairs of one KV head -- as its N side:
+// for any m near max S (kLift, kReach), in one pass over the keys with the
+// running m and l.  Both products are taken transposed, with the keys (then the
+// head elements) as the MFMA's M side and the rows -- (query token, head) pairs
+// of one KV head -- as its N side:
 // S^T = K Q^T leaves a lane with many keys of ONE row, so m and l are mostly
 // in-register reductions, and O^T = V^T P^T takes the lane's own weights as
 // its B operand without moving them: the order of the keys inside an MFMA's
@@ -267,12 +267,37 @@ __device__ __forceinline__ float sum_xor16(float x) {
 // loop, where the wait would count the loop's own copies.
 __device__ __forceinline__ void landed(i32x4& x) { asm volatile("" : "+v"(x)); }
 
-// The running maximum may lag the true one by this much (in powers of two)
-// before the accumulators are rescaled: weights then reach 2^8, exact in
-// range for both 16-bit types and float32 sums, and almost every stage after
-// the first skips the rescaling.  (A row's own scores alone decide when its
-// maximum moves, so its bits do not depend on the rows it shares a tile with.)
-constexpr float kMaxLag = 8.f;
+// m, the power of two that a row's weights 2^(S - m) are taken against, follows
+// the row's running maximum with a lag: it moves, and the accumulators are
+// rescaled, only when a score passes m + kReach, and then to kLift below that
+// score.  Almost every stage after the first skips the rescaling; m cancels in
+// out and is put back in lse.  (A row's own scores alone decide when its m
+// moves, so its bits do not depend on the rows it shares a tile with.)
+//  - bf16 weights have float32's range: no lift, a lag of 2^8.
+//  - f16 weights end at 2^-24, in steps of that below 2^-14.  Against a largest
+//    weight of 1 the keys 17 nats below a row's largest score (a sink's, say)
+//    would drop out of the sum of values and stay in l: 32768 keys 18 nats below
+//    a sink came out as 0 for 5e-4.  So the row's largest weight lies in
+//    [2^11, 2^15] (65504 is the type's largest), what rounds to 0 is 2^-36 of it,
+//    and steps grow coarser than 2^-11 only 17 nats below it.  The lag is 2^4 so
+//    that the lift may be that large.
+template <int KK>
+constexpr float kLift = KK == KF16 ? 11.f : 0.f;
+template <int KK>
+constexpr float kReach = KK == KF16 ? 15.f : 8.f;
+
+// The row's m with the largest score so far, mx, in sight.
+template <int KK>
+__device__ __forceinline__ float moved(float m, float mx) {
+  return mx > m + kReach<KK> ? mx - kLift<KK> : m;
+}
+
+// ln of the sum l 2^m, without the lift's cancelling digits.
+template <int KK>
+__device__ __forceinline__ float lse_of(float m, float l) {
+  if (l == 0.f) return -__builtin_inff();
+  return ((m + kLift<KK>) + __log2f(l * __builtin_exp2f(-kLift<KK>))) * kLn2;
+}
 
 // What the join needs to know of a row of a launch with split tiles, written by
 // its first part: that the row is whole (a NaN that no m is: m never is one), or
@@ -499,8 +524,8 @@ __global__ __launch_bounds__(256, 1) void attn_rows_kernel(AttnParams p) {
     float mx = fmaxf(fmaxf(fmaxf(sa[0], sa[1]), fmaxf(sa[2], sa[3])),
                      fmaxf(fmaxf(sb[0], sb[1]), fmaxf(sb[2], sb[3])));
     mx = max_xor32(max_xor16(mx)) * p.c;
-    if (__ballot(mx > m + kMaxLag)) {
-      const float mn = mx > m + kMaxLag ? mx : m;
+    if (__ballot(mx > m + kReach<KK>)) {
+      const float mn = moved<KK>(m, mx);
       const float alpha = exp2_hw(m - (mn == -__builtin_inff() ? 0.f : mn));
       m = mn;
       lsum *= alpha;
@@ -649,7 +674,7 @@ __global__ __launch_bounds__(256, 1) void attn_rows_kernel(AttnParams p) {
                      pack2<KK>(s1[0] * inv, s1[1] * inv), pack2<KK>(s1[2] * inv, s1[3] * inv)};
   *reinterpret_cast<i32x4*>(p.out + out_row * (2 * kD) + 64 * wave + 16 * G) = res;
   if (p.lse && wave == 0 && G == 0)
-    p.lse[out_row] = lt == 0.f ? -__builtin_inff() : (mt + __log2f(lt)) * kLn2;
+    p.lse[out_row] = lse_of<KK>(mt, lt);
 }
 
 // ---------------------------------------------------------------------------
@@ -708,7 +733,7 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnParams p) {
       *reinterpret_cast<i32x2*>(p.out + row * (2 * kD) + 8 * l) =
           i32x2{pack2<KK>(o[0] * inv, o[1] * inv), pack2<KK>(o[2] * inv, o[3] * inv)};
     if (p.lse && l == 0)
-      p.lse[row] = lt == 0.f ? -__builtin_inff() : (mt + __log2f(lt)) * kLn2;
+      p.lse[row] = lse_of<KK>(mt, lt);
   }
 }
 
@@ -926,8 +951,8 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tile_kernel(AttnParams p) {
 #pragma unroll
       for (int r = 0; r < 16; ++r) mx = fmaxf(mx, st[t][r]);
     mx = max_xor32(mx) * p.c;
-    if (__ballot(mx > m + kMaxLag)) {
-      const float mn = mx > m + kMaxLag ? mx : m;
+    if (__ballot(mx > m + kReach<KK>)) {
+      const float mn = moved<KK>(m, mx);
       const float alpha = exp2_hw(m - (mn == -__builtin_inff() ? 0.f : mn));
       m = mn;
       lsum *= alpha;
@@ -1104,7 +1129,7 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tile_kernel(AttnParams p) {
           i32x2{pack2<KK>(o[d][4 * q] * inv, o[d][4 * q + 1] * inv),
                 pack2<KK>(o[d][4 * q + 2] * inv, o[d][4 * q + 3] * inv)};
   if (p.lse && h == 0)
-    p.lse[out_row] = lsum == 0.f ? -__builtin_inff() : (m + __log2f(lsum)) * kLn2;
+    p.lse[out_row] = lse_of<KK>(m, lsum);
 }
 
 // ---------------------------------------------------------------------------
@@ -1308,8 +1333,8 @@ __global__ __launch_bounds__(64 * NW, 4) void attn_union_kernel(AttnParams p) {
       for (int r = 0; r < 4; ++r) mx = fmaxf(mx, st[t][r]);
     mx = max_xor32(max_xor16(mx)) * p.c;
     mx = mine ? mx : -__builtin_inff();
-    if (__ballot(mx > m + kMaxLag)) {
-      const float mn = mx > m + kMaxLag ? mx : m;
+    if (__ballot(mx > m + kReach<KK>)) {
+      const float mn = moved<KK>(m, mx);
       const float alpha = exp2_hw(m - (mn == -__builtin_inff() ? 0.f : mn));
       m = mn;
       lsum *= alpha;
@@ -1517,7 +1542,7 @@ __global__ __launch_bounds__(64 * NW, 4) void attn_union_kernel(AttnParams p) {
     *reinterpret_cast<i32x2*>(p.out + out_row * (2 * kD) + 2 * (16 * d + 4 * G)) =
         i32x2{pack2<KK>(o[d][0] * inv, o[d][1] * inv), pack2<KK>(o[d][2] * inv, o[d][3] * inv)};
   if (p.lse && G == 0)
-    p.lse[out_row] = lsum == 0.f ? -__builtin_inff() : (m + __log2f(lsum)) * kLn2;
+    p.lse[out_row] = lse_of<KK>(m, lsum);
 }
 
 }  // namespace msa

@@ -378,7 +378,9 @@ msa_status_t msa_cache_append(const msa_append_item_t* items, int32_t num_items,
  * over the visible j: j < kv_len[b] and, with sparse_mode 3, j <= pos(t).  A
  * row that sees no key gets out 0 and lse -inf.  S, the softmax's maximum and
  * sum and both products' sums are float32; the weights exp(S - m) are rounded
- * to the query's type for the second product, and out once at the end.
+ * to the query's type for the second product, and out once at the end.  (f16
+ * weights are scaled first, so that the row's largest is at least 2^11: a key's
+ * share is lost only below 2^-36 of it, 25 nats.)
  * Infinities and NaN in keys or values that a row does not see never reach it.
  *
  * query        f16 or bf16 [T, Hq, 128], any token stride >= Hq * 128 of whole

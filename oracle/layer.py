@@ -112,9 +112,10 @@ def attention_bounds(ref: Attention, dtype: torch.dtype):
     With e = 2^-24 and u = eps / 2 of the type, a score of 128 products is off
     by at most ds = 130 e size (128 additions, the scale, its constant) and
     its weight by the factor 1 +- (ds + 4 e (1 + size)) (the exponent's own
-    rounding and exp2's); rounding it costs u more, for float16 at least
-    2^-25 against a largest weight of 1.  The sums of n weights and products
-    add n e each, a rescaling of the sums 2 e per 64 keys (within n e).  The
+    rounding and exp2's); rounding it costs u more.  The smallest step of
+    float16 is 2^-24; weights that are scaled so that the row's largest is at
+    least 2^11 are off by half of that, 2^-36 of their sum (n of them: n 2^-36
+    of the largest value).  The sums of n weights and products add n e each, a rescaling of the sums 2 e per 64 keys (within n e).  The
     quotient is off by both sums' shares, and u at its own rounding."""
     e = 2.0 ** -24
     u = torch.finfo(dtype).eps / 2
@@ -123,7 +124,7 @@ def attention_bounds(ref: Attention, dtype: torch.dtype):
     share = 2 * dw + 2 * n * e + 4 * e
     out = ref.spread * (share + u * (1 + share))[..., None] + u * ref.out.abs() * 1.01
     if dtype == torch.float16:
-        out = out + (n * 2.0 ** -25 * ref.top)[..., None] + 2.0 ** -25
+        out = out + (n * 2.0 ** -36 * ref.top)[..., None] + 2.0 ** -25
     lse = dw + n * e + 4 * e * (1 + ref.lse.abs().nan_to_num(0, 0, 0))
     return out, lse
 
