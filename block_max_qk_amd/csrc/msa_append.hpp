@@ -75,6 +75,19 @@ __device__ __forceinline__ float elem16(uint32_t w, int hi, bool bf) {
   return (float)__builtin_bit_cast(_Float16, (uint16_t)x);
 }
 
+// The float32 that a rounding to fewer bits takes where it would take y: the bits
+// that a float32 has no room for leave the last one set, which keeps a value next
+// to a border of the narrower type on its own side.  (To the nearest float32
+// instead, 1 rotated row element in 2 million lands on the border and goes to the
+// even code.  Below float32's normal range the cast rounds, far from any border.)
+__device__ __forceinline__ float to_odd(double y) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, y);
+  const uint32_t lo = (uint32_t)u;
+  // (the sum carries into bit 29 if any of the 29 bits below is set)
+  const uint32_t kept = (lo | ((lo & 0x1FFFFFFFu) + 0x1FFFFFFFu)) & 0xE0000000u;
+  return (float)__builtin_bit_cast(double, (u >> 32 << 32) | kept);
+}
+
 // max over the 16 lanes of a row (or 4 of a group), in float64
 template <int LANES>
 __device__ __forceinline__ double lanes_max(double x) {
@@ -257,7 +270,7 @@ __global__ __launch_bounds__(64 * kAppendWaves) void append_kernel(AppendParams 
       float f[8];
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        const float v = (float)y[k];
+        const float v = to_odd(y[k]);
         f[k] = v != v ? v : fminf(fmaxf(v, -top), top);
       }
       int w[2];

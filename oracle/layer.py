@@ -115,8 +115,9 @@ def attention_bounds(ref: Attention, dtype: torch.dtype):
     rounding and exp2's); rounding it costs u more.  The smallest step of
     float16 is 2^-24; weights that are scaled so that the row's largest is at
     least 2^11 are off by half of that, 2^-36 of their sum (n of them: n 2^-36
-    of the largest value).  The sums of n weights and products add n e each, a rescaling of the sums 2 e per 64 keys (within n e).  The
-    quotient is off by both sums' shares, and u at its own rounding."""
+    of the largest value).  The sums of n weights and products add n e each, a
+    rescaling of the sums 2 e per 64 keys (within n e).  The quotient is off by
+    both sums' shares, and u at its own rounding."""
     e = 2.0 ** -24
     u = torch.finfo(dtype).eps / 2
     n = ref.keys.double()
@@ -167,7 +168,7 @@ def encode_fp8(y, dtype):
     grid, names = vals[keep].sort()
     names = codes[keep][names]
     out = torch.zeros(D, dtype=torch.uint8)
-    for i, v in enumerate(y.float().double()):
+    for i, v in enumerate(y.double()):
         if math.isnan(float(v)):
             out[i] = 0x7F
             continue
