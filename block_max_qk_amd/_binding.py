@@ -38,7 +38,8 @@ EXPORTED = ("msa_index_score", "msa_index_score_family", "msa_index_score_ex",
             "msa_index_score_mxfp4", "msa_index_score_mxfp4_family",
             "msa_index_score_out_width", "msa_status_str",
             "msa_index_score_kernel_family", "msa_block_topk", "msa_cache_append",
-            "msa_attention", "msa_block_attention", "msa_attention_workspace")
+            "msa_attention", "msa_block_attention", "msa_attention_workspace",
+            "msa_attention_tile_rows")
 LOCAL_MODE_CODE = {"request": 0, "query": 1}
 
 
@@ -122,6 +123,8 @@ def load_library(path: Optional[str] = None):
         lib.msa_block_attention.restype = ctypes.c_int
         lib.msa_attention_workspace.argtypes = [i64, i32, i32, i32, i64, i32]
         lib.msa_attention_workspace.restype = i64
+        lib.msa_attention_tile_rows.argtypes = [i64, i32, i32, i32, i64, i32]
+        lib.msa_attention_tile_rows.restype = i32
         if path is None:
             _lib = lib
         return lib
@@ -604,6 +607,14 @@ def msa_attention_workspace(T: int, batch: int, Hq: int, Hkv: int, max_blocks: i
     """Bytes of workspace that an attention call of these sizes needs
     (``num_blocks`` 0: dense)."""
     return int(load_library().msa_attention_workspace(int(T), int(batch), int(Hq), int(Hkv),
+                                                      int(max_blocks), int(num_blocks)))
+
+
+def msa_attention_tile_rows(T: int, batch: int, Hq: int, Hkv: int, max_blocks: int,
+                            num_blocks: int = 0) -> int:
+    """Rows of the tiles (16, 128 or 256) that an attention call of these sizes
+    uses (``num_blocks`` 0: dense)."""
+    return int(load_library().msa_attention_tile_rows(int(T), int(batch), int(Hq), int(Hkv),
                                                       int(max_blocks), int(num_blocks)))
 
 

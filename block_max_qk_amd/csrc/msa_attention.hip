@@ -106,6 +106,13 @@ int64_t workspace_for(const Plan& p, int64_t T, int64_t Hq) {
   return p.nsplit > 1 ? p.nsplit * T * Hq * (int64_t)(msa::kD * sizeof(float) + sizeof(float2)) : 0;
 }
 
+// Sizes that a plan is asked for without a call.
+bool sizes_ok(int64_t T, int32_t batch, int32_t Hq, int32_t Hkv, int64_t max_blocks,
+              int32_t num_blocks) {
+  return T >= 1 && T <= INT32_MAX && batch >= 1 && Hq >= 1 && Hkv >= 1 && Hq % Hkv == 0 &&
+         max_blocks >= 0 && max_blocks <= (1 << 24) && num_blocks >= 0 && num_blocks <= 64;
+}
+
 template <int KK>
 hipError_t launch(const AttnParams& p, const Plan& plan, int64_t grid, hipStream_t s) {
   hipError_t e;
@@ -277,10 +284,14 @@ msa_status_t msa_block_attention(const msa_tensor_t* query, const msa_tensor_t* 
 
 int64_t msa_attention_workspace(int64_t T, int32_t batch, int32_t Hq, int32_t Hkv,
                                 int64_t max_blocks, int32_t num_blocks) {
-  if (T < 1 || batch < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv || T > INT32_MAX || max_blocks < 0 ||
-      max_blocks > (1 << 24) || num_blocks < 0 || num_blocks > 64)
-    return 0;
+  if (!sizes_ok(T, batch, Hq, Hkv, max_blocks, num_blocks)) return 0;
   return workspace_for(plan_for(T, batch, Hq, Hkv, max_blocks, num_blocks), T, Hq);
+}
+
+int32_t msa_attention_tile_rows(int64_t T, int32_t batch, int32_t Hq, int32_t Hkv,
+                                int64_t max_blocks, int32_t num_blocks) {
+  if (!sizes_ok(T, batch, Hq, Hkv, max_blocks, num_blocks)) return 0;
+  return plan_for(T, batch, Hq, Hkv, max_blocks, num_blocks).rows;
 }
 
 }  // extern "C"

@@ -426,6 +426,13 @@ msa_status_t msa_block_attention(const msa_tensor_t* query, const msa_tensor_t* 
 int64_t msa_attention_workspace(int64_t T, int32_t batch, int32_t Hq, int32_t Hkv,
                                 int64_t max_blocks, int32_t num_blocks);
 
+/* Rows -- (query token, head) pairs of one KV head -- of the tiles that
+ * msa_attention (num_blocks = 0) or msa_block_attention would use for a call of
+ * these sizes: 16, 128 or 256; 0 for sizes that no call takes.  All tiles compute
+ * the same definition.  Host-only; for benchmarks and tests. */
+int32_t msa_attention_tile_rows(int64_t T, int32_t batch, int32_t Hq, int32_t Hkv,
+                                int64_t max_blocks, int32_t num_blocks);
+
 /* Output width RoundUp(max(max_blocks, 1), 16) (guide, section 五: the last
  * axis is aligned to 16, and an all-empty packed batch clamps MB to 1). */
 int64_t msa_index_score_out_width(int64_t max_blocks);
