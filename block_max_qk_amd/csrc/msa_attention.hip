@@ -25,7 +25,6 @@ struct Plan {
   int nsplit, min_blocks, target;
   bool balanced;
   int64_t units;     // workgroups (attn_union_kernel: tiles x parts)
-  bool once;         // no two workgroups read the same rows of keys
 };
 
 // The tile and the split, from the sizes alone.
@@ -81,7 +80,6 @@ Plan plan_for(int64_t T, int64_t B, int64_t Hq, int64_t Hkv, int64_t MB, int64_t
   p.tpt = few && nsel > 0 ? 1 : p.rows / p.hpt;
   p.hchunks = (int)((g + p.hpt - 1) / p.hpt);
   p.ntiles = std::min<int64_t>(T, (T + B * (p.tpt - 1)) / p.tpt);
-  p.once = p.hchunks == 1 && (nsel == 0 || T <= 2 * B);
   const int64_t items = std::max<int64_t>(p.ntiles * Hkv * p.hchunks, 1);
   const int64_t blocks = std::max<int64_t>(few && nsel > 0 ? std::min(nsel, MB) : MB, 1);
   p.min_blocks = few ? 2 : 8;
@@ -118,11 +116,9 @@ hipError_t launch(const AttnParams& p, const Plan& plan, int64_t grid, hipStream
   hipError_t e;
   const dim3 gr((unsigned)grid);
   if (plan.rows == msa::kAttnRows) {
-    auto kern = p.blocks ? (plan.once ? msa::attn_rows_kernel<KK, true, true>
-                                      : msa::attn_rows_kernel<KK, true, false>)
-                         : (plan.once ? msa::attn_rows_kernel<KK, false, true>
-                                      : msa::attn_rows_kernel<KK, false, false>);
-    e = msa::launch_kernel(kern, gr, dim3(256), s, p);
+    e = msa::launch_kernel(p.blocks ? msa::attn_rows_kernel<KK, true>
+                                    : msa::attn_rows_kernel<KK, false>,
+                           gr, dim3(256), s, p);
   } else if (p.blocks) {
     e = msa::launch_kernel(msa::attn_union_kernel<KK, 8>, gr, dim3(512), s, p);
   } else if (plan.rows == 256) {

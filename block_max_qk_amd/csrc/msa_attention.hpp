@@ -341,17 +341,19 @@ __device__ __forceinline__ void copy_rows(uint8_t* dst, const uint8_t* src, int 
 // into its own part of the LDS, one block ahead, with no barrier in the loop.
 // 64 requests of up to 8192 keys, 8 KV heads, 1.17 GB: 190 us, 6.2 TB/s, which is
 // what a large read reaches.
-// ONCE: no other workgroup reads the same rows, and the copies say so (the same
-// requests in 1536 even parts: 219 us without the hint, 199 with it; where tokens
-// share their selected blocks the hint costs as much as it gains here).  Stages
-// of 16 keys with two workgroups a CU instead: 207 us.
+// A request of one tile (and head chunk) is the only reader of its rows, and its
+// copies say so with the nontemporal hint; other tiles' copies do not.  With the
+// hint and without: 64 requests of one token, up to 8000 keys, 157 and 174 us, of
+// two tokens 180 and 200; 63 of one token beside one of 900 over 32768 keys, 32
+// heads of their own, 3822 and 2192 (tile by tile, as here).
+// Stages of 16 keys with two workgroups a CU instead: 207 us against 199.
 // ---------------------------------------------------------------------------
 
 constexpr int kAttnRows = 16;
 constexpr int kRowWaves = 4;
 constexpr int kRowStage = 16384;     // 32 keys' K and V rows
 
-template <int KK, bool SEL, bool ONCE>
+template <int KK, bool SEL>
 __global__ __launch_bounds__(256, 1) void attn_rows_kernel(AttnParams p) {
   __shared__ __attribute__((aligned(16))) uint8_t ring[kRowWaves][2][kRowStage];
   int rest = blockIdx.x, split = 0, parts = 1;
@@ -483,6 +485,17 @@ __global__ __launch_bounds__(256, 1) void attn_rows_kernel(AttnParams p) {
     vof[i] = (uint32_t)(r * p.v_row_stride + 16 * (cc ^ ((r & 7) << 1)));
   }
 
+  const bool once = __builtin_amdgcn_readfirstlane(w.Lq <= p.tpt && p.hchunks == 1);
+  auto copy = [&](uint8_t* dst, const Rows& r) __attribute__((always_inline)) {
+    if (once) {
+      copy_rows<8, true>(dst, r.k, r.n * p.k_row_stride, kof);
+      copy_rows<8, true>(dst + 8192, r.v, r.n * p.v_row_stride, vof);
+    } else {
+      copy_rows<8>(dst, r.k, r.n * p.k_row_stride, kof);
+      copy_rows<8>(dst + 8192, r.v, r.n * p.v_row_stride, vof);
+    }
+  };
+
   f32x4 o[8];
   float m, lsum;
 
@@ -494,8 +507,7 @@ __global__ __launch_bounds__(256, 1) void attn_rows_kernel(AttnParams p) {
                   const Rows& next, bool more, auto careful) __attribute__((always_inline)) {
     if constexpr (!decltype(careful)::value) {
       if (more) {
-        copy_rows<8, ONCE>(dst, next.k, next.n * p.k_row_stride, kof);
-        copy_rows<8, ONCE>(dst + 8192, next.v, next.n * p.v_row_stride, vof);
+        copy(dst, next);
         asm volatile("s_waitcnt vmcnt(16)" ::: "memory");
       } else {
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
@@ -583,8 +595,7 @@ __global__ __launch_bounds__(256, 1) void attn_rows_kernel(AttnParams p) {
     Block cur = block_at(0);
     Rows r = rows_of(cur);
     if constexpr (!decltype(careful)::value) {
-      copy_rows<8, ONCE>(mine, r.k, r.n * p.k_row_stride, kof);
-      copy_rows<8, ONCE>(mine + 8192, r.v, r.n * p.v_row_stride, vof);
+      copy(mine, r);
     }
     for (int s = 0; s < nst; ++s) {
       Block next = cur;
