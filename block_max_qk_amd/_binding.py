@@ -503,11 +503,16 @@ def _stream_of(handle, dev):
     return torch.cuda.ExternalStream(handle, device=dev)
 
 
+# torch's getter of the current stream's handle, where this build of torch has it
+_current_raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _raw_stream(stream, index: int):
     """``_stream_handle`` without a stream object for the current stream, which
-    costs a small call a microsecond."""
-    if stream is None and index >= 0:
-        return torch._C._cuda_getCurrentRawStream(index)
+    costs a small call a microsecond (torch's own compiled code takes the handle
+    the same way; a torch without that getter costs the stream object)."""
+    if stream is None and index >= 0 and _current_raw is not None:
+        return _current_raw(index)
     return _stream_handle(stream, index)
 
 
