@@ -749,6 +749,95 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnParams p) {
 }
 
 // ---------------------------------------------------------------------------
+// What the two kernels of many rows share: stages of 64 keys, two per block,
+// and where their rows come from.
+// ---------------------------------------------------------------------------
+
+constexpr int kTileKeys = 64;
+constexpr int kNoPage = 1 << 30;
+
+// A block of the walk: its number, whether it is on a page, the places of its rows.
+struct Entry {
+  int beta;
+  bool there;
+  int64_t k, v;
+};
+
+// Entries of the walk, their numbers (kNoPage: on no page) and places held one
+// per lane, 64 at a time, so that a stage takes a few readlanes and no address
+// arithmetic (scalar multiplications per stage held up every wave for hundreds
+// of cycles).
+struct BlockList {
+  int bidx = 0, base = 0;
+  int64_t kat = 0, vat = 0;
+
+  // Entries from .. from + 63 of `count`; number(i) is the number of entry i.
+  template <typename F>
+  __device__ __forceinline__ void load(const AttnParams& p, const AttnTile& w, int hk, int from,
+                                       int count, F number) {
+    const int l = lane_id();
+    base = from;
+    bidx = kNoPage;
+    kat = vat = 0;
+    if (from + l < count) {
+      bidx = number(from + l);
+      if (p.paged) {
+        const int pg = p.block_table[(int64_t)w.b * p.MB + bidx];
+        if (pg >= 0 && pg < p.NP) {
+          kat = pg * p.k_page_stride;
+          vat = pg * p.v_page_stride;
+        } else {
+          bidx |= kNoPage;
+        }
+      } else {
+        kat = (w.koff + (int64_t)bidx * kP) * p.k_row_stride;
+        vat = (w.koff + (int64_t)bidx * kP) * p.v_row_stride;
+      }
+    }
+    bidx = consumed(bidx);
+    kat += (int64_t)hk * p.k_head_stride;
+    vat += (int64_t)hk * p.v_head_stride;
+  }
+  __device__ __forceinline__ Entry at(int e) const {
+    const int x = lane_at(bidx, e - base);
+    return Entry{x & (kNoPage - 1), x < kNoPage, lane_at(kat, e - base), lane_at(vat, e - base)};
+  }
+};
+
+// Where the keys of half `in` of a block lie, and how many bytes of them there
+// are to the tile's last visible one, lim_hi.
+struct StageRows {
+  const uint8_t *k, *v;
+  int kb, vb;
+};
+__device__ __forceinline__ StageRows stage_rows(const AttnParams& p, int lim_hi, const Entry& x,
+                                                int in) {
+  const int left = x.there ? max(0, min(kTileKeys, lim_hi + 1 - x.beta * kP - in * kTileKeys)) : 0;
+  return StageRows{p.k + x.k + in * kTileKeys * p.k_row_stride,
+                   p.v + x.v + in * kTileKeys * p.v_row_stride,
+                   __builtin_amdgcn_readfirstlane(left * p.k_row_stride),
+                   __builtin_amdgcn_readfirstlane(left * p.v_row_stride)};
+}
+
+// A wave's NI copies of a stage's rows through registers, for the careful pass
+// (whose copies need not overlap anything); kof, vof as for copy_rows.
+template <int NI>
+__device__ __forceinline__ void copy_plain(const AttnParams& p, uint8_t* kring, uint8_t* vring,
+                                           int wave, const StageRows& r, const uint32_t* kof,
+                                           const uint32_t* vof) {
+  const int l = lane_id();
+  for (int i = 0; i < NI; ++i) {
+    const int row = (wave * NI + i) * 4 + (l >> 4);
+    const int at = (wave * NI + i) * 1024 + 16 * l;
+    const i32x4 zero = {0, 0, 0, 0};
+    *reinterpret_cast<i32x4*>(kring + at) =
+        row * p.k_row_stride < r.kb ? ld16(r.k + kof[i]) : zero;
+    *reinterpret_cast<i32x4*>(vring + at) =
+        row * p.v_row_stride < r.vb ? ld16(r.v + vof[i]) : zero;
+  }
+}
+
+// ---------------------------------------------------------------------------
 // Many rows: 32 rows a wave, NW waves a workgroup, every wave reading the same
 // stages of 64 keys from the LDS.
 //
@@ -774,8 +863,6 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnParams p) {
 // token, from values with the unseen rows cleared (careful); a tile of finite
 // inputs costs only the look at its accumulators.
 // ---------------------------------------------------------------------------
-
-constexpr int kTileKeys = 64;
 
 template <int KK, int NW>
 __global__ __launch_bounds__(64 * NW, 2) void attn_tile_kernel(AttnParams p) {
@@ -839,42 +926,14 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tile_kernel(AttnParams p) {
     for (int s = 0; s < 8; ++s) qv[s] = ld16(qr + 16 * (2 * s + h));
   }
 
-  // The part's blocks: their numbers (kNoPage: on no page) and the places of
-  // their rows are held one per lane, 64 at a time, so
-  // that a stage takes a few readlanes and no address arithmetic (scalar
-  // multiplications per stage held up every wave for hundreds of cycles).
-  constexpr int kNoPage = 1 << 30;
   const int count = b1 - b0;
-  int bidx = 0, pbase = 0;
-  int64_t kat = 0, vat = 0;
-  auto load_entries = [&](int from) {
-    pbase = from;
-    bidx = kNoPage;
-    kat = vat = 0;
-    if (from + l < count) {
-      bidx = b0 + from + l;
-      if (p.paged) {
-        const int pg = p.block_table[(int64_t)w.b * p.MB + bidx];
-        if (pg >= 0 && pg < p.NP) {
-          kat = pg * p.k_page_stride;
-          vat = pg * p.v_page_stride;
-        } else {
-          bidx |= kNoPage;
-        }
-      } else {
-        kat = (w.koff + (int64_t)bidx * kP) * p.k_row_stride;
-        vat = (w.koff + (int64_t)bidx * kP) * p.v_row_stride;
-      }
-    }
-    bidx = consumed(bidx);
-    kat += (int64_t)hk * p.k_head_stride;
-    vat += (int64_t)hk * p.v_head_stride;
+  BlockList list;
+  auto load_entries = [&](int from) __attribute__((always_inline)) {
+    list.load(p, w, hk, from, count, [&](int i) { return b0 + i; });
   };
-  struct Entry { int beta; bool there; int64_t k, v; };
-  auto entry_at = [&](int e) -> Entry {
-    if (e - pbase >= 64) load_entries(e);
-    const int x = lane_at(bidx, e - pbase);
-    return Entry{x & (kNoPage - 1), x < kNoPage, lane_at(kat, e - pbase), lane_at(vat, e - pbase)};
+  auto entry_at = [&](int e) __attribute__((always_inline)) -> Entry {
+    if (e - list.base >= 64) load_entries(e);
+    return list.at(e);
   };
 
   const int cr = l >> 4, cc = l & 15;
@@ -885,30 +944,8 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tile_kernel(AttnParams p) {
     kof[i] = (uint32_t)(r * p.k_row_stride + 16 * (cc ^ (r & 15)));
     vof[i] = (uint32_t)(r * p.v_row_stride + 16 * (cc ^ ((r & 3) << 2)));
   }
-  // Where the keys of half `in` of a block lie, and how many bytes of them
-  // there are to the tile's last visible one.
-  struct Rows { const uint8_t *k, *v; int kb, vb; };
-  auto rows_of = [&](const Entry& x, int in) -> Rows {
-    const int left =
-        x.there ? max(0, min(kTileKeys, lim_hi + 1 - x.beta * kP - in * kTileKeys)) : 0;
-    return Rows{p.k + x.k + in * kTileKeys * p.k_row_stride,
-                p.v + x.v + in * kTileKeys * p.v_row_stride,
-                __builtin_amdgcn_readfirstlane(left * p.k_row_stride),
-                __builtin_amdgcn_readfirstlane(left * p.v_row_stride)};
-  };
-  // a stage's rows through registers, for the careful pass (whose copies need
-  // not overlap anything)
-  auto copy_plain = [&](const Entry& x, int in) {
-    const Rows r = rows_of(x, in);
-    for (int i = 0; i < NI; ++i) {
-      const int row = (wave * NI + i) * 4 + cr;
-      const int at = (wave * NI + i) * 1024 + 16 * l;
-      const i32x4 zero = {0, 0, 0, 0};
-      *reinterpret_cast<i32x4*>(kring + at) =
-          row * p.k_row_stride < r.kb ? ld16(r.k + kof[i]) : zero;
-      *reinterpret_cast<i32x4*>(vring + at) =
-          row * p.v_row_stride < r.vb ? ld16(r.v + vof[i]) : zero;
-    }
+  auto rows_of = [&](const Entry& x, int in) __attribute__((always_inline)) -> StageRows {
+    return stage_rows(p, lim_hi, x, in);
   };
 
   f32x16 o[4];
@@ -1046,7 +1083,7 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tile_kernel(AttnParams p) {
       for (int s = 0; s < 2 * count; ++s) {
         const Entry x = entry_at(s >> 1);
         __syncthreads();
-        copy_plain(x, s & 1);
+        copy_plain<NI>(p, kring, vring, wave, rows_of(x, s & 1), kof, vof);
         __syncthreads();
         scores(kring);
         absorb(vring, x, s & 1, careful);
@@ -1054,7 +1091,7 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tile_kernel(AttnParams p) {
       return;
     }
     Entry x = entry_at(0);
-    Rows r = rows_of(x, 0);
+    StageRows r = rows_of(x, 0);
     // one half of an entry: the copies of the next into `kd` and `vd`, then its
     // own work on the rows at kt and vt
     auto half = [&](const uint8_t* __restrict kt, const uint8_t* __restrict vt,
@@ -1224,41 +1261,16 @@ __global__ __launch_bounds__(64 * NW, 4) void attn_union_kernel(AttnParams p) {
     for (int s = 0; s < 4; ++s) qv[s] = ld16(qr + 64 * s + 16 * G);
   }
 
-  // The blocks come as a list of `count` entries, the marked ones of a span;
-  // their numbers and the places of their rows as in attn_tile_kernel.
-  constexpr int kNoPage = 1 << 30;
+  // the blocks come as a list of `count` entries, the marked ones of a span
   int base = b0, count = b1 - b0;
   const int span = min(kSelSpan, kSelBits / p.tpt & ~31);
-  int bidx = 0, pbase = 0;
-  int64_t kat = 0, vat = 0;
-  auto load_entries = [&](int from) {
-    pbase = from;
-    bidx = kNoPage;
-    kat = vat = 0;
-    if (from + l < count) {
-      bidx = base + named[from + l];
-      if (p.paged) {
-        const int pg = p.block_table[(int64_t)w.b * p.MB + bidx];
-        if (pg >= 0 && pg < p.NP) {
-          kat = pg * p.k_page_stride;
-          vat = pg * p.v_page_stride;
-        } else {
-          bidx |= kNoPage;
-        }
-      } else {
-        kat = (w.koff + (int64_t)bidx * kP) * p.k_row_stride;
-        vat = (w.koff + (int64_t)bidx * kP) * p.v_row_stride;
-      }
-    }
-    bidx = consumed(bidx);
-    kat += (int64_t)hk * p.k_head_stride;
-    vat += (int64_t)hk * p.v_head_stride;
+  BlockList list;
+  auto load_entries = [&](int from) __attribute__((always_inline)) {
+    list.load(p, w, hk, from, count, [&](int i) { return base + named[i]; });
   };
-  struct Entry { int beta; bool there; int64_t k, v; };
-  auto entry_at = [&](int e) -> Entry {
-    if (e - pbase >= 64) load_entries(e);
-    const int x = lane_at(bidx, e - pbase);
-    return Entry{x & (kNoPage - 1), x < kNoPage, lane_at(kat, e - pbase), lane_at(vat, e - pbase)};
+  auto entry_at = [&](int e) __attribute__((always_inline)) -> Entry {
+    if (e - list.base >= 64) load_entries(e);
+    return list.at(e);
   };
 
   const int cr = l >> 4, cc = l & 15;
@@ -1269,30 +1281,8 @@ __global__ __launch_bounds__(64 * NW, 4) void attn_union_kernel(AttnParams p) {
     kof[i] = (uint32_t)(r * p.k_row_stride + 16 * (cc ^ (r & 15)));
     vof[i] = (uint32_t)(r * p.v_row_stride + 16 * (cc ^ ((r & 7) << 1)));
   }
-  // Where the keys of half `in` of a block lie, and how many bytes of them
-  // there are to the tile's last visible one.
-  struct Rows { const uint8_t *k, *v; int kb, vb; };
-  auto rows_of = [&](const Entry& x, int in) -> Rows {
-    const int left =
-        x.there ? max(0, min(kTileKeys, lim_hi + 1 - x.beta * kP - in * kTileKeys)) : 0;
-    return Rows{p.k + x.k + in * kTileKeys * p.k_row_stride,
-                p.v + x.v + in * kTileKeys * p.v_row_stride,
-                __builtin_amdgcn_readfirstlane(left * p.k_row_stride),
-                __builtin_amdgcn_readfirstlane(left * p.v_row_stride)};
-  };
-  // a stage's rows through registers, for the careful pass (whose copies need
-  // not overlap anything)
-  auto copy_plain = [&](const Entry& x, int in) {
-    const Rows r = rows_of(x, in);
-    for (int i = 0; i < NI; ++i) {
-      const int row = (wave * NI + i) * 4 + cr;
-      const int at = (wave * NI + i) * 1024 + 16 * l;
-      const i32x4 zero = {0, 0, 0, 0};
-      *reinterpret_cast<i32x4*>(kring + at) =
-          row * p.k_row_stride < r.kb ? ld16(r.k + kof[i]) : zero;
-      *reinterpret_cast<i32x4*>(vring + at) =
-          row * p.v_row_stride < r.vb ? ld16(r.v + vof[i]) : zero;
-    }
+  auto rows_of = [&](const Entry& x, int in) __attribute__((always_inline)) -> StageRows {
+    return stage_rows(p, lim_hi, x, in);
   };
 
   f32x4 o[8];
@@ -1428,7 +1418,7 @@ __global__ __launch_bounds__(64 * NW, 4) void attn_union_kernel(AttnParams p) {
       for (int s = 0; s < 2 * count; ++s) {
         const Entry x = entry_at(s >> 1);
         __syncthreads();
-        copy_plain(x, s & 1);
+        copy_plain<NI>(p, kring, vring, wave, rows_of(x, s & 1), kof, vof);
         __syncthreads();
         const bool mine = selected(x);
         if (some(mine)) {
@@ -1439,7 +1429,7 @@ __global__ __launch_bounds__(64 * NW, 4) void attn_union_kernel(AttnParams p) {
       return;
     }
     Entry x = entry_at(0);
-    Rows r = rows_of(x, 0);
+    StageRows r = rows_of(x, 0);
     // one half of an entry: the copies of the next into `kd` and `vd`, then its
     // own work on the rows at kt and vt
     auto half = [&](const uint8_t* __restrict kt, const uint8_t* __restrict vt,
