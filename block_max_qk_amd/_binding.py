@@ -752,7 +752,10 @@ def attention(query: torch.Tensor, key: torch.Tensor, value: torch.Tensor,
               softmax_scale: Optional[float] = None, max_blocks: Optional[int] = None,
               return_lse: bool = False, stream=None):
     """Allocate ``out`` (and ``lse``) and fill them with ``msa_attention``;
-    returns ``out`` or ``(out, lse)``."""
+    returns ``out`` or ``(out, lse)``.  Rows that no request holds (a padded
+    batch) are not written.  On a ``stream`` that is given, they are that
+    stream's memory: use on another stream needs an ordering, and ``record_stream``
+    before they are freed."""
     out, lse = _outputs(query, return_lse, stream)
     if max_blocks is None:
         max_blocks = _default_blocks(key, block_table)
@@ -767,7 +770,8 @@ def block_attention(query: torch.Tensor, key: torch.Tensor, value: torch.Tensor,
                     sparse_mode: int = 3, softmax_scale: Optional[float] = None,
                     max_blocks: Optional[int] = None, return_lse: bool = False, stream=None):
     """Allocate ``out`` (and ``lse``) and fill them with
-    ``msa_block_attention``; returns ``out`` or ``(out, lse)``."""
+    ``msa_block_attention``, as ``attention`` does; returns ``out`` or
+    ``(out, lse)``."""
     if blocks is None:
         raise ValueError("blocks is required")
     out, lse = _outputs(query, return_lse, stream)

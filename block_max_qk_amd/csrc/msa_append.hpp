@@ -8,11 +8,15 @@
 // whole wave, so its type, layout and pointers are scalars and nothing
 // diverges.  Loads run three steps ahead.
 //
-// 14000 tokens of 64 query, 8 key and 8 value rows and an e4m3 index branch: 139
+// 14000 tokens of 64 query, 8 key and 8 value rows and an e4m3 index branch: 140
 // us, 4.5 TB/s of reads and writes together (a copy reaches 4.95); 4096 tokens
-// with an MXFP4 index branch 37 us, 2.9 TB/s (the float64 of the encoding is the
-// dearer part there); a decode step of 64 tokens 5.8 us: its three dependent
-// reads and the launch.
+// with an MXFP4 index branch 37 us, 2.9 TB/s; a decode step of 64 tokens 5.8 us:
+// its three dependent reads and the launch.  20 rows of 8192 tokens alone, by the
+// destination's type: 16-bit 20.3 us (4.3 TB/s), e4m3 25.9 (2.6), MXFP4 30.4 (1.9),
+// int8 37.2 (1.8).  What the encoded types take longer is arithmetic and fewer
+// waves: with the rotation in float32 they take 21.9, 25.5 and 32.6 us, int8 with
+// a reciprocal for its quotients too 26.5, but codes next to a border are then
+// not the nearest.
 #pragma once
 
 #include "msa_device.hpp"

@@ -34,7 +34,11 @@ struct Plan {
 // of that and such tiles, or their parts of 8 blocks, fill the chip's 256 CUs
 // (2048 tokens over 32768 keys, 8 heads a group: 911 us with 256 rows, 951 with
 // 128, 3130 with 16; 9 requests of 2 to 258 tokens: 81, 74 and 163 us; one
-// prompt of 1000 tokens: 35, 27 and 59 us).
+// prompt of 1000 tokens: 35, 27 and 59 us; 64 requests of one token: 193 with
+// 16, 240 with 128).  The average is all that the sizes tell: where few chunks
+// stand among many decode tokens, it chooses 16 rows for both (63 tokens beside
+// a chunk of 65 over 32768 keys: 510 us with 16 rows, 174 with 128; beside one of
+// 900, 32 heads of their own: 2190 and 800).
 // Selected blocks: one workgroup per token and KV head (16 rows), or tiles of
 // 128 rows that walk the union of their tokens' blocks once tokens can share
 // them and fill the chip (16 blocks of 16000 keys, 4 KV heads: 60 tokens 21 us
@@ -64,8 +68,14 @@ struct Plan {
 //  - 256 rows: 8 requests of 200 tokens over 2048 keys: 69 us, 94 aiming at
 //    384, 90 in even parts.
 // Not split are caches of fewer than 8 blocks (16 for the larger tiles; 4 blocks
-// 8.2 us, 9.1 in two parts), 1024 tiles and more, and what would write partial
-// sums of more than 2^18 rows (136 MB).
+// 8.2 us, 9.1 in two parts), what would write partial sums of more than 2^18 rows
+// (136 MB), and 1024 items (tile, KV head, chunk) and more: there every workgroup
+// would go over the whole batch before it knows a part's length, and an even
+// batch pays for that (requests of 512 keys, 64 heads on 8: 256 of them 103 us,
+// 111 in parts; 1024 of them 454 and 544; 4096 of 16 heads on 2 664 and 1109),
+// while one request far longer than the rest then holds the launch up (one of
+// 131072 keys beside 127, 255 or 1023 of 512: 1380, 1430 and 1790 us, in parts
+// 167, 246 and 890).
 Plan plan_for(int64_t T, int64_t B, int64_t Hq, int64_t Hkv, int64_t MB, int64_t nsel) {
   Plan p{};
   const int64_t g = Hq / Hkv;

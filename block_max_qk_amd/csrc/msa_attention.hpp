@@ -846,8 +846,8 @@ __device__ __forceinline__ void copy_plain(const AttnParams& p, uint8_t* kring, 
 // rows past it read zeros (a stored NaN there cannot reach a sum).
 //
 // Bound by the matrix units and, before they are full, by the card's power: 2048
-// tokens over 32768 keys, 32 heads on 4 KV heads, take 909 to 972 us by card
-// (1.10 to 1.17 PFLOP/s; 8192^3 products of the library reach 1.24), with the MFMA
+// tokens over 32768 keys, 32 heads on 4 KV heads, take 907 to 988 us by card
+// (1.08 to 1.17 PFLOP/s; 8192^3 products of the library reach 1.24), with the MFMA
 // busy in 56% of the cycles, vector instructions in 40%, the LDS in 25% without
 // bank conflicts.  32 rows a wave, because a fragment of K or V out of the LDS
 // then feeds the largest MFMA; 8 waves a workgroup share a stage's copies (4
@@ -1195,11 +1195,13 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tile_kernel(AttnParams p) {
 // the barriers of unequally busy waves cost.
 //
 // 4096 tokens of 8 heads a group over 16 blocks each of 32768 keys, lists that
-// overlap in part (23 blocks for two tokens together, 51 for sixteen): 328 us,
-// 0.41 PFLOP/s of the selected products; 374 us with 32 rows a wave and half as
-// many waves, 1058 us with a workgroup per token.  With one list for each tile's
-// tokens it takes 183 us: the rest is the wave's own union.  Where K and V come
-// from hardly matters (325 us with every block on one of 16 pages), and no unit
+// overlap in part (23 blocks for two tokens together, 51 for sixteen): 328 to 347
+// us by card, 0.39 to 0.41 PFLOP/s of the selected products; where that took 328,
+// 374 us with 32 rows a wave and half as many waves, 1058 us with a workgroup per
+// token.  With one list for each tile's tokens it takes 183 us: the rest is the
+// wave's own union, and waiting at the stages' barriers for waves that have more
+// of the blocks.  Where K and V come from hardly matters (325 us with every block
+// on one of 16 pages), and no unit
 // is full: MFMA 23%, vector 34%, LDS 24% of the cycles.
 // ---------------------------------------------------------------------------
 

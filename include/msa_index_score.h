@@ -343,7 +343,9 @@ typedef struct {
  * The rotation for the last three is evaluated in float64, so that a value
  * next to a rounding border falls on its own side; a zero row or group has
  * scale 0 and zero elements; a row (I8) or group (MXFP4) that holds an
- * infinity or NaN gets a NaN scale (E8M0 255) and zero elements.
+ * infinity or NaN gets a NaN scale (E8M0 255) and zero elements.  The encoded
+ * types are the index branch's (msa_index_score and its variants read them);
+ * msa_attention takes keys and values of the query's type.
  *
  * cos, sin     device float32 [positions, rotary_dim / 2], compact, 16-byte
  *              aligned; may be NULL if no item is rotated.
@@ -382,6 +384,8 @@ msa_status_t msa_cache_append(const msa_append_item_t* items, int32_t num_items,
  * weights are scaled first, so that the row's largest is at least 2^11: a key's
  * share is lost only below 2^-36 of it, 25 nats.)
  * Infinities and NaN in keys or values that a row does not see never reach it.
+ * (The sums are taken before the division, with bf16 weights of up to 2^8 each:
+ * n visible bf16 values past 2^120 / n in magnitude may give infinities.)
  *
  * query        f16 or bf16 [T, Hq, 128], any token stride >= Hq * 128 of whole
  *              16 bytes, other axes compact.
