@@ -1195,8 +1195,8 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tile_kernel(AttnParams p) {
 // the barriers of unequally busy waves cost.
 //
 // 4096 tokens of 8 heads a group over 16 blocks each of 32768 keys, lists that
-// overlap in part (23 blocks for two tokens together, 51 for sixteen): 328 to 347
-// us by card, 0.39 to 0.41 PFLOP/s of the selected products; where that took 328,
+// overlap in part (23 blocks for two tokens together, 51 for sixteen): 328 to 354
+// us by card, 0.38 to 0.41 PFLOP/s of the selected products; where that took 328,
 // 374 us with 32 rows a wave and half as many waves, 1058 us with a workgroup per
 // token.  With one list for each tile's tokens it takes 183 us: the rest is the
 // wave's own union, and waiting at the stages' barriers for waves that have more
