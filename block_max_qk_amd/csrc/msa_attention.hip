@@ -117,8 +117,9 @@ int64_t workspace_for(const Plan& p, int64_t T, int64_t Hq) {
 // Sizes that a plan is asked for without a call.
 bool sizes_ok(int64_t T, int32_t batch, int32_t Hq, int32_t Hkv, int64_t max_blocks,
               int32_t num_blocks) {
-  return T >= 1 && T <= INT32_MAX && batch >= 1 && Hq >= 1 && Hkv >= 1 && Hq % Hkv == 0 &&
-         max_blocks >= 0 && max_blocks <= (1 << 24) && num_blocks >= 0 && num_blocks <= 64;
+  return T >= 1 && T <= INT32_MAX && batch >= 1 && batch <= (1 << 30) && Hq >= 1 &&
+         Hq <= (1 << 16) && Hkv >= 1 && Hq % Hkv == 0 && max_blocks >= 0 &&
+         max_blocks <= (1 << 24) && num_blocks >= 0 && num_blocks <= 64;
 }
 
 template <int KK>

@@ -25,5 +25,6 @@ def test_the_other_tiles():
 
 def test_sizes_that_no_call_takes():
     for at in ((0, 1, 8, 2, 4), (2, 0, 8, 2, 4), (2, 1, 8, 3, 4), (2, 1, 0, 2, 4), (2, 1, 8, 2, -1),
-               (2 ** 31, 1, 8, 2, 4), (2, 1, 8, 2, 1 << 25), (2, 1, 8, 2, 4, 65)):
+               (2 ** 31, 1, 8, 2, 4), (2, 1, 8, 2, 1 << 25), (2, 1, 8, 2, 4, 65),
+               (2, 1, 1 << 17, 1, 4), (2, (1 << 30) + 1, 8, 2, 4), (2, 1, 8, 2, 4, -1)):
         assert m.msa_attention_tile_rows(*at) == 0 and m.msa_attention_workspace(*at) == 0
