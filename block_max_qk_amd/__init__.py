@@ -14,6 +14,7 @@ from ._binding import (  # noqa: F401
     MsaError,
     MsaLayoutError,
     MsaTensor,
+    StepTables,
     attention,
     block_attention,
     block_topk,
@@ -31,4 +32,7 @@ from ._binding import (  # noqa: F401
     msa_index_score_mxfp4,
     msa_index_score_out_width,
     msa_status_str,
+    msa_step_tables,
+    new_step_tables,
+    step_tables,
 )

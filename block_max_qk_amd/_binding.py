@@ -39,7 +39,7 @@ EXPORTED = ("msa_index_score", "msa_index_score_family", "msa_index_score_ex",
             "msa_index_score_out_width", "msa_status_str",
             "msa_index_score_kernel_family", "msa_block_topk", "msa_cache_append",
             "msa_attention", "msa_block_attention", "msa_attention_workspace",
-            "msa_attention_tile_rows")
+            "msa_attention_tile_rows", "msa_step_tables")
 LOCAL_MODE_CODE = {"request": 0, "query": 1}
 
 
@@ -125,6 +125,13 @@ def load_library(path: Optional[str] = None):
         lib.msa_attention_workspace.restype = i64
         lib.msa_attention_tile_rows.argtypes = [i64, i32, i32, i32, i64, i32]
         lib.msa_attention_tile_rows.restype = i32
+        # new_tokens, ctx_len, rows, batch, pool, pool_rows, pool_blocks,
+        # free_pages, free_size, free_count, free_out, max_blocks, T, block_size,
+        # cu_seqlens_q, kv_len, start_loc, block_table, positions, slots,
+        # cu_pages, stream
+        lib.msa_step_tables.argtypes = [ptr, ptr, ptr, i32, ptr, i64, i64, ptr, i64, ptr, ptr, i64,
+                                        i64, i32, ptr, ptr, ptr, ptr, ptr, ptr, ptr, ptr]
+        lib.msa_step_tables.restype = ctypes.c_int
         if path is None:
             _lib = lib
         return lib
@@ -780,3 +787,106 @@ def block_attention(query: torch.Tensor, key: torch.Tensor, value: torch.Tensor,
     _attention(query, key, value, blocks, block_table, cu_seqlens_q, kv_len, layout, sparse_mode,
                softmax_scale, out, lse, max_blocks, None, stream, BLOCK_SIZE)
     return (out, lse) if return_lse else out
+
+
+# ---------------------------------------------------------------------------
+# the step's tables
+# ---------------------------------------------------------------------------
+
+
+class StepTables(NamedTuple):
+    """What ``msa_step_tables`` writes: int32 tensors, but int64 slots."""
+    cu_seqlens_q: torch.Tensor   # [B + 1]
+    kv_len: torch.Tensor         # [B], new tokens included
+    start_loc: torch.Tensor      # [B], block of the first new token
+    block_table: torch.Tensor    # [B, max_blocks]
+    positions: torch.Tensor      # [T]
+    slots: torch.Tensor          # [T], page * 128 + position % 128, -1: none
+    cu_pages: torch.Tensor       # [B + 1], pages taken from the free list
+
+
+def new_step_tables(batch: int, T: int, max_blocks: int, device=None) -> StepTables:
+    """Tensors for ``msa_step_tables`` to write, which a server keeps from step
+    to step."""
+    def ints(*shape):
+        return torch.empty(shape, dtype=torch.int32, device=device)
+
+    return StepTables(ints(batch + 1), ints(batch), ints(batch), ints(batch, max_blocks), ints(T),
+                      torch.empty(T, dtype=torch.int64, device=device), ints(batch + 1))
+
+
+def msa_step_tables(new_tokens: torch.Tensor, ctx_len: torch.Tensor, pool: torch.Tensor,
+                    free_pages: torch.Tensor, free_count: torch.Tensor, out: StepTables,
+                    rows: Optional[torch.Tensor] = None, free_out: Optional[torch.Tensor] = None,
+                    stream=None, block_size: int = BLOCK_SIZE) -> StepTables:
+    """Call the C ABI: from ``new_tokens`` and ``ctx_len`` ([B] int32) the tables
+    of one step, into ``out``; blocks that the new tokens begin take pages from
+    the end of ``free_pages``' first ``free_count[0]``, and are entered in
+    ``pool`` ([rows, blocks] int32), whose row ``rows[b]`` (None: b) is request
+    b's.  ``free_out`` ([2] int32: pages left, pages missing) is ``free_count``
+    itself if it is None.  T and max_blocks are ``out``'s; asynchronous on
+    ``stream`` (default: torch's current stream)."""
+    lib = _lib or load_library()
+    index = new_tokens.get_device()
+    if free_out is None:
+        free_out = free_count
+    i32 = torch.int32
+    B = new_tokens.numel()
+    T = out.positions.numel()
+    if pool.dim() != 2 or out.block_table.dim() != 2:
+        raise ValueError(f"pool must be [rows, blocks] and block_table [{B}, max_blocks], got "
+                         f"{tuple(pool.shape)} and {tuple(out.block_table.shape)}")
+    max_blocks = out.block_table.shape[1]
+    if free_pages.dim() != 1:
+        raise ValueError(f"free_pages must be 1-D, got {tuple(free_pages.shape)}")
+    for name, t, shape in (("new_tokens", new_tokens, (B,)), ("ctx_len", ctx_len, (B,)),
+                           ("rows", rows, (B,)), ("pool", pool, None),
+                           ("free_pages", free_pages, None), ("free_count", free_count, (2,)),
+                           ("free_out", free_out, (2,)),
+                           ("cu_seqlens_q", out.cu_seqlens_q, (B + 1,)),
+                           ("kv_len", out.kv_len, (B,)), ("start_loc", out.start_loc, (B,)),
+                           ("block_table", out.block_table, (B, max_blocks)),
+                           ("positions", out.positions, (T,)), ("slots", out.slots, (T,)),
+                           ("cu_pages", out.cu_pages, (B + 1,))):
+        if t is None:
+            continue
+        want = torch.int64 if name == "slots" else i32
+        if t.dtype != want or not t.is_contiguous() or (shape is not None and t.shape != shape):
+            raise ValueError(f"{name} must be a contiguous {want} tensor"
+                             f"{'' if shape is None else f' {list(shape)}'}, got {t.dtype} "
+                             f"{tuple(t.shape)}")
+        if t.get_device() != index:
+            raise ValueError(f"{name} is on {t.device}, new_tokens on {new_tokens.device}")
+    if index < 0:
+        raise ValueError(f"the tensors must be on a GPU, new_tokens is on {new_tokens.device}")
+    handle = _raw_stream(stream, index)
+    with _guard(index):
+        st = lib.msa_step_tables(
+            new_tokens.data_ptr(), ctx_len.data_ptr(), _address(rows), B, pool.data_ptr(),
+            pool.shape[0], pool.shape[1], free_pages.data_ptr(), free_pages.numel(),
+            free_count.data_ptr(), free_out.data_ptr(), max_blocks, T, int(block_size),
+            out.cu_seqlens_q.data_ptr(), out.kv_len.data_ptr(), out.start_loc.data_ptr(),
+            out.block_table.data_ptr(), out.positions.data_ptr(), out.slots.data_ptr(),
+            out.cu_pages.data_ptr(), handle)
+    if st:
+        _raise_status(st)
+    return out
+
+
+def step_tables(new_tokens: torch.Tensor, ctx_len: torch.Tensor, pool: torch.Tensor,
+                free_pages: torch.Tensor, free_count: torch.Tensor, T: int,
+                rows: Optional[torch.Tensor] = None, max_blocks: Optional[int] = None,
+                free_out: Optional[torch.Tensor] = None, stream=None) -> StepTables:
+    """Allocate the tables of a step of up to ``T`` new tokens and fill them with
+    ``msa_step_tables`` (``max_blocks`` defaults to the pool's width).  On a
+    ``stream`` that is given, they are that stream's memory, as ``attention``'s
+    outputs are."""
+    width = pool.shape[-1] if max_blocks is None else max_blocks
+    if stream is not None and new_tokens.is_cuda:
+        with torch.cuda.stream(_stream_of(_stream_handle(stream, new_tokens.device),
+                                          new_tokens.device)):
+            out = new_step_tables(new_tokens.numel(), T, width, new_tokens.device)
+    else:
+        out = new_step_tables(new_tokens.numel(), T, width, new_tokens.device)
+    return msa_step_tables(new_tokens, ctx_len, pool, free_pages, free_count, out, rows=rows,
+                           free_out=free_out, stream=stream)

@@ -11,7 +11,7 @@ import sys
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 SOURCES = [os.path.join(HERE, "csrc", f) for f in ("msa_index_score.hip", "msa_attention.hip",
-                                                   "msa_append.hip")]
+                                                   "msa_append.hip", "msa_tables.hip")]
 LIB = os.path.join(HERE, "libmsa_index_score.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 

@@ -437,6 +437,62 @@ int64_t msa_attention_workspace(int64_t T, int32_t batch, int32_t Hq, int32_t Hk
 int32_t msa_attention_tile_rows(int64_t T, int32_t batch, int32_t Hq, int32_t Hkv,
                                 int64_t max_blocks, int32_t num_blocks);
 
+/*
+ * The tables of one serving step, from the requests' lengths: what the entry
+ * points here take as cu_seqlens_q, kv_len, start_loc and block_table, with
+ * pages from a free list for the blocks that the new tokens begin, and every new
+ * token's position and slot.  For request b with q = new_tokens[b], c =
+ * ctx_len[b] (negative counts as 0), row r = rows[b] of the pool:
+ *
+ *   cu_seqlens_q[b + 1] = sum of the new tokens of requests 0..b
+ *   kv_len[b] = c + q,  start_loc[b] = floor(c / 128)
+ *   blocks ceil(c / 128) .. ceil(kv_len[b] / 128) - 1 take the next pages, in the
+ *     order of b and then of the block, from the end of the free list:
+ *     free_pages[n - 1], free_pages[n - 2], ... with n = free_count[0]; behind
+ *     the last one, -1.  They are written to pool[r, :].
+ *   block_table[b, k] = pool[r, k] for k < ceil(kv_len[b] / 128), -1 behind
+ *   cu_pages[b + 1] = pages that requests 0..b took
+ *   positions[t] = c + i,  slots[t] = page * 128 + positions[t] % 128 for the
+ *     request's i-th new token t, -1 where no page is; rows behind the last
+ *     token get 0 and -1
+ *   free_out[0] = free pages that are left, free_out[1] = pages that were missing
+ *
+ * new_tokens, ctx_len  device int32 [batch].
+ * rows         device int32 [batch], distinct, or NULL: request b has row b.  A
+ *              row outside [0, pool_rows) holds no pages and takes none.
+ * pool         device int32 [pool_rows, pool_blocks]: the pages of every request
+ *              that the server holds; row r's first ceil(ctx_len / 128) entries are
+ *              read.
+ * free_pages   device int32 [free_size], of which the first free_count[0] are free
+ *              (cut to [0, free_size]).  Pages that requests give back are written
+ *              behind them by the caller, who raises the count.
+ * free_count   device int32 [2] (the second is not read).
+ * free_out     device int32 [2]; may be free_count itself (one small launch more).
+ * max_blocks   blocks of a request that exist, 1..min(pool_blocks, 2^24): later ones get no
+ *              page, and their tokens no slot.
+ * T            rows of positions and slots: at least the sum of new_tokens.  (Where
+ *              the sum is larger, nothing is written past T and cu_seqlens_q ends
+ *              at T.)
+ * block_size   128, as for msa_index_score.
+ * cu_seqlens_q, cu_pages   device int32 [batch + 1], written in full, as are
+ * kv_len, start_loc        device int32 [batch],
+ * block_table              device int32 [batch, max_blocks],
+ * positions, slots         device int32 and int64 [T].
+ *
+ * All arrays are compact; nothing that is written may overlap anything else
+ * (MSA_ERR_STRIDE; but free_out and free_count).  Nothing is allocated or kept; a
+ * call may be captured into a graph.  MSA_ERR_SHAPE for sizes out of range (batch
+ * > 2^30, T, pool_rows, pool_blocks or free_size > 2^31 - 1), MSA_ERR_NULL for a
+ * pointer that the call must use, MSA_ERR_HIP if a launch fails.
+ */
+msa_status_t msa_step_tables(const int32_t* new_tokens, const int32_t* ctx_len,
+                             const int32_t* rows, int32_t batch, int32_t* pool, int64_t pool_rows,
+                             int64_t pool_blocks, const int32_t* free_pages, int64_t free_size,
+                             const int32_t* free_count, int32_t* free_out, int64_t max_blocks,
+                             int64_t T, int32_t block_size, int32_t* cu_seqlens_q, int32_t* kv_len,
+                             int32_t* start_loc, int32_t* block_table, int32_t* positions,
+                             int64_t* slots, int32_t* cu_pages, void* stream);
+
 /* Output width RoundUp(max(max_blocks, 1), 16) (guide, section 五: the last
  * axis is aligned to 16, and an all-empty packed batch clamps MB to 1). */
 int64_t msa_index_score_out_width(int64_t max_blocks);

@@ -246,3 +246,46 @@ def append(item, cos, sin, block_table, cu_seqlens_q, kv_len, interleaved, any_r
             else:
                 dst[at] = y.float().to(dst.dtype)
     return dst, scale, rows, mags, written
+
+
+# ---------------------------------------------------------------------------
+# the step's tables
+# ---------------------------------------------------------------------------
+
+
+def step_tables(new_tokens, ctx_len, rows, pool, free_pages, free_count: int, max_blocks: int,
+                T: int):
+    """What ``msa_step_tables`` leaves, request by request: a dict of lists and
+    tensors (``pool`` a changed copy, ``free`` the two counts)."""
+    pool = pool.clone()
+    B = len(new_tokens)
+    count = min(max(int(free_count), 0), len(free_pages))
+    stack = [int(x) for x in free_pages[:count]]
+    missing = 0
+    out = {"cu_seqlens_q": [0], "kv_len": [], "start_loc": [], "cu_pages": [0],
+           "block_table": torch.full((B, max_blocks), -1, dtype=torch.int32),
+           "positions": [], "slots": []}
+    for b in range(B):
+        q, c = max(int(new_tokens[b]), 0), max(int(ctx_len[b]), 0)
+        row = b if rows is None else int(rows[b])
+        held = 0 <= row < pool.shape[0]
+        blocks = [-1] * max_blocks
+        for k in range(min(max_blocks, -(-(c + q) // P))):
+            if held and k >= -(-c // P):
+                missing += not stack
+                pool[row, k] = stack.pop() if stack else -1
+            if held:
+                blocks[k] = int(pool[row, k])
+        out["block_table"][b] = torch.tensor(blocks, dtype=torch.int32)
+        for pos in range(c, c + q):
+            page = blocks[pos // P] if pos // P < max_blocks else -1
+            out["positions"].append(pos)
+            out["slots"].append(page * P + pos % P if page >= 0 else -1)
+        out["cu_seqlens_q"].append(out["cu_seqlens_q"][-1] + q)
+        out["kv_len"].append(c + q)
+        out["start_loc"].append(c // P)
+        out["cu_pages"].append(count - len(stack))
+    pad = T - len(out["positions"])
+    out["positions"] += [0] * pad
+    out["slots"] += [-1] * pad
+    return out | {"pool": pool, "free": [len(stack), missing]}
