@@ -39,7 +39,7 @@ EXPORTED = ("msa_index_score", "msa_index_score_family", "msa_index_score_ex",
             "msa_index_score_out_width", "msa_status_str",
             "msa_index_score_kernel_family", "msa_block_topk", "msa_cache_append",
             "msa_attention", "msa_block_attention", "msa_attention_workspace",
-            "msa_attention_tile_rows", "msa_step_tables")
+            "msa_attention_tile_rows", "msa_step_tables", "msa_cache_append_axes")
 LOCAL_MODE_CODE = {"request": 0, "query": 1}
 
 
@@ -112,6 +112,10 @@ def load_library(path: Optional[str] = None):
         lib.msa_cache_append.argtypes = [ptr, i32, ptr, ptr, i64, i32, i32, ptr, i64, ptr, ptr,
                                          i32, i32, ptr]
         lib.msa_cache_append.restype = ctypes.c_int
+        # axis_positions, axes, pair_axes (host bytes) after interleaved
+        args = lib.msa_cache_append.argtypes
+        lib.msa_cache_append_axes.argtypes = [*args[:7], ptr, i32, ctypes.c_char_p, *args[7:]]
+        lib.msa_cache_append_axes.restype = ctypes.c_int
         # block_table, max_blocks, cu_seqlens_q, kv_len, batch, block_size,
         # layout, sparse_mode, softmax_scale, out, lse, workspace,
         # workspace_bytes, stream
@@ -542,18 +546,39 @@ def _item_layout(layout) -> int:
     return int(layout)
 
 
+def _check_axes(axis_positions, pair_axes, lead, index, rotary) -> bytes:
+    """The axis of each pair as bytes, of tensors that fit the items."""
+    if (axis_positions.dtype != torch.int32 or not axis_positions.is_contiguous() or
+            axis_positions.dim() != 2 or axis_positions.shape[1] != lead.shape[0]):
+        raise ValueError(f"axis_positions must be a contiguous int32 [axes, {lead.shape[0]}] "
+                         f"tensor, got {axis_positions.dtype} {tuple(axis_positions.shape)}")
+    if axis_positions.get_device() != index:
+        raise ValueError(f"tensors are on {axis_positions.device} and {lead.device}")
+    if pair_axes is None or len(pair_axes) != rotary // 2:
+        raise ValueError(f"pair_axes must hold the axis of each of the {rotary // 2} pairs")
+    try:
+        return bytes(pair_axes)
+    except (TypeError, ValueError) as e:
+        raise ValueError("pair_axes must hold integers from 0 on") from e
+
+
 def msa_cache_append(items: Sequence[CacheItem], cos: Optional[torch.Tensor],
                      sin: Optional[torch.Tensor], block_table: Optional[torch.Tensor],
                      cu_seqlens_q: torch.Tensor, kv_len: torch.Tensor,
-                     interleaved: bool = False, stream=None,
-                     block_size: int = BLOCK_SIZE) -> None:
+                     interleaved: bool = False, stream=None, block_size: int = BLOCK_SIZE,
+                     axis_positions: Optional[torch.Tensor] = None,
+                     pair_axes: Optional[Sequence[int]] = None) -> None:
     """Append the new tokens' rows to their caches, rotated by their positions
     and encoded as the caches hold them, and rotate or encode the queries, in
     one launch (see ``CacheItem``; the C ABI's header defines the encodings).
 
     ``cos`` and ``sin`` [positions, rotary_dim / 2] float32 may be None if no
     item is rotated, ``block_table`` [>= B, MB] int32 if no item is paged;
-    ``kv_len`` counts the new tokens."""
+    ``kv_len`` counts the new tokens.
+
+    With ``axis_positions`` ([axes, T] int32, 1 to 4 axes) pair r of a token is
+    rotated by the position of axis ``pair_axes[r]`` (rotary_dim / 2 integers, or
+    the same as bytes) instead of the token's position in its sequence."""
     lib = _lib or load_library()
     if not 1 <= len(items) <= APPEND_MAX_ITEMS:
         raise ValueError(f"1 to {APPEND_MAX_ITEMS} items, got {len(items)}")
@@ -575,6 +600,11 @@ def msa_cache_append(items: Sequence[CacheItem], cos: Optional[torch.Tensor],
         positions, rotary = cos.shape[0], 2 * cos.shape[1]
     elif cos is not None or sin is not None or any(it[4] for it in items):
         raise ValueError("rotated items need both cos and sin")
+    axes = None
+    if axis_positions is not None:
+        axes = _check_axes(axis_positions, pair_axes, lead, index, rotary)
+    elif pair_axes is not None:
+        raise ValueError("pair_axes needs axis_positions")
     packed, code = [], DTYPE_CODE.get
     for i, (src, dst, layout, scale, rotate) in enumerate(items):
         lay = _ITEM_LAYOUT.get(layout)
@@ -605,11 +635,16 @@ def msa_cache_append(items: Sequence[CacheItem], cos: Optional[torch.Tensor],
     if index < 0 and lead.numel():
         raise ValueError(f"the tensors must be on a GPU, src is on {lead.device}")
     handle = _raw_stream(stream, index)
+    head = (b"".join(packed), len(items), _address(cos), _address(sin), positions, rotary,
+            1 if interleaved else 0)
+    tail = (_address(block_table), max_blocks, cu_seqlens_q.data_ptr(), kv_len.data_ptr(), B,
+            int(block_size), handle)
     with _guard(index):
-        st = lib.msa_cache_append(b"".join(packed), len(items), _address(cos), _address(sin),
-                                  positions, rotary, 1 if interleaved else 0,
-                                  _address(block_table), max_blocks, cu_seqlens_q.data_ptr(),
-                                  kv_len.data_ptr(), B, int(block_size), handle)
+        if axes is None:
+            st = lib.msa_cache_append(*head, *tail)
+        else:
+            st = lib.msa_cache_append_axes(*head, axis_positions.data_ptr(),
+                                           axis_positions.shape[0], axes, *tail)
     if st:
         _raise_status(st)
 

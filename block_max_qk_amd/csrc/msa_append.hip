@@ -91,14 +91,18 @@ msa_status_t item_for(const msa_append_item_t& in, int64_t T, AppendItem& a) {
   return MSA_OK;
 }
 
-}  // namespace
+// Position axes of a call (axes 0: none).
+struct Axes {
+  const int32_t* positions;
+  int32_t axes;
+  const uint8_t* of_pair;
+};
 
-extern "C" msa_status_t msa_cache_append(const msa_append_item_t* items, int32_t num_items,
-                                         const float* cos, const float* sin, int64_t positions,
-                                         int32_t rotary_dim, int32_t interleaved,
-                                         const int32_t* block_table, int64_t max_blocks,
-                                         const int32_t* cu_seqlens_q, const int32_t* kv_len,
-                                         int32_t batch, int32_t block_size, void* stream) {
+msa_status_t append(const msa_append_item_t* items, int32_t num_items, const float* cos,
+                    const float* sin, int64_t positions, int32_t rotary_dim, int32_t interleaved,
+                    const Axes& ax, const int32_t* block_table, int64_t max_blocks,
+                    const int32_t* cu_seqlens_q, const int32_t* kv_len, int32_t batch,
+                    int32_t block_size, void* stream) {
   if (!items || !cu_seqlens_q) return MSA_ERR_NULL;
   if (batch > 0 && !kv_len) return MSA_ERR_NULL;
   if (num_items < 1 || num_items > MSA_APPEND_MAX_ITEMS) return MSA_ERR_ATTR;
@@ -127,6 +131,16 @@ extern "C" msa_status_t msa_cache_append(const msa_append_item_t* items, int32_t
     if (rotary_dim < 16 || rotary_dim > msa::kD || rotary_dim % 16) return MSA_ERR_ATTR;
     if (T > 0 && positions > 0 && (!cos || !sin)) return MSA_ERR_NULL;
     if (!msa::aligned16(cos) || !msa::aligned16(sin)) return MSA_ERR_STRIDE;
+    if (ax.axes > 0) {
+      if (!ax.of_pair || (T > 0 && !ax.positions)) return MSA_ERR_NULL;
+      if (reinterpret_cast<uintptr_t>(ax.positions) & 3u) return MSA_ERR_STRIDE;
+      for (int r = 0; r < rotary_dim / 2; ++r) {
+        if (ax.of_pair[r] >= ax.axes) return MSA_ERR_ATTR;
+        p.pair_axis[r >> 5] |= (uint64_t)ax.of_pair[r] << (2 * (r & 31));
+      }
+      p.axis_pos = ax.positions;
+      p.axes = ax.axes;
+    }
   }
   if (paged) {
     if (max_blocks < 1) return MSA_ERR_SHAPE;
@@ -157,3 +171,32 @@ extern "C" msa_status_t msa_cache_append(const msa_append_item_t* items, int32_t
                            : msa::launch_kernel(msa::append_kernel<false>, gr, bl, s, p);
   return e == hipSuccess ? MSA_OK : MSA_ERR_HIP;
 }
+
+}  // namespace
+
+extern "C" {
+
+msa_status_t msa_cache_append(const msa_append_item_t* items, int32_t num_items, const float* cos,
+                              const float* sin, int64_t positions, int32_t rotary_dim,
+                              int32_t interleaved, const int32_t* block_table, int64_t max_blocks,
+                              const int32_t* cu_seqlens_q, const int32_t* kv_len, int32_t batch,
+                              int32_t block_size, void* stream) {
+  return append(items, num_items, cos, sin, positions, rotary_dim, interleaved, Axes{}, block_table,
+                max_blocks, cu_seqlens_q, kv_len, batch, block_size, stream);
+}
+
+msa_status_t msa_cache_append_axes(const msa_append_item_t* items, int32_t num_items,
+                                   const float* cos, const float* sin, int64_t positions,
+                                   int32_t rotary_dim, int32_t interleaved,
+                                   const int32_t* axis_positions, int32_t axes,
+                                   const uint8_t* pair_axes, const int32_t* block_table,
+                                   int64_t max_blocks, const int32_t* cu_seqlens_q,
+                                   const int32_t* kv_len, int32_t batch, int32_t block_size,
+                                   void* stream) {
+  if (axes < 1 || axes > MSA_APPEND_MAX_AXES) return MSA_ERR_ATTR;
+  return append(items, num_items, cos, sin, positions, rotary_dim, interleaved,
+                Axes{axis_positions, axes, pair_axes}, block_table, max_blocks, cu_seqlens_q,
+                kv_len, batch, block_size, stream);
+}
+
+}  // extern "C"

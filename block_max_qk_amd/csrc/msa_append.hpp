@@ -47,6 +47,8 @@ struct AppendParams {
   const int32_t* block_table;
   const int32_t* cu_q;
   const int32_t* kv_len;
+  const int32_t* axis_pos;            // [axes, T] positions that the angles go by
+  uint64_t pair_axis[2];              // the axis of each rotated pair, two bits a pair
   int64_t positions;                  // rows of the angle table
   int64_t T;
   int32_t B, MB;
@@ -54,6 +56,7 @@ struct AppendParams {
   int32_t per_wave, groups;           // steps per wave, waves per token
   int32_t half;                       // rotary_dim / 2 (0: no rotation)
   int32_t interleaved, packed;        // packed: some item is TND
+  int32_t axes;                       // 0: the angles go by the token's position
 };
 
 // The request of token t: the largest b with cu[b] <= t, found 64 bounds at a
@@ -131,7 +134,13 @@ __global__ __launch_bounds__(64 * kAppendWaves) void append_kernel(AppendParams 
   const int q0 = p.cu_q[b];
   const int lq = p.cu_q[b + 1] - q0;
   const int64_t pos = (int64_t)p.kv_len[b] - lq + (t - q0);
-  if (pos < 0 || (p.half > 0 && pos >= p.positions)) return;
+  if (pos < 0 || (p.half > 0 && p.axes == 0 && pos >= p.positions)) return;
+  int64_t turn[4];                                 // a token's angle rows, by axis
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    turn[k] = k < p.axes ? p.axis_pos[k * p.T + t] : 0;
+    if (k < p.axes && (turn[k] < 0 || turn[k] >= p.positions)) return;
+  }
   const int l = lane_id();
   const int i = l & 15, rr = l >> 4;
 
@@ -150,7 +159,31 @@ __global__ __launch_bounds__(64 * kAppendWaves) void append_kernel(AppendParams 
   // this lane's angles: of its 8 elements (halves, whose partners lie p.half
   // elements away in another lane) or of its 4 pairs (interleaved)
   float c[8], s[8];
-  if (p.half > 0) {
+  if (p.axes > 0) {
+    // (a row of angles per axis; a lane reads those that its pairs belong to)
+    const int at = 8 * i < 2 * p.half ? (p.interleaved ? 4 * i : (8 * i) % p.half) : 0;
+    // two bits a pair from bit 2 at on: at is a multiple of 4, so 8 pairs lie in
+    // one word unless at % 32 is 28, where only the 4 pairs of an interleaved lane begin
+    const uint32_t mine = (uint32_t)(p.pair_axis[at >> 5] >> (2 * (at & 31)));
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      if (x >= p.axes) break;
+      const float* cr = p.cos + turn[x] * p.half + at;
+      const float* sr = p.sin + turn[x] * p.half + at;
+#pragma unroll
+      for (int k = 0; k < 8; k += 4) {
+        if (p.interleaved && k > 0) break;
+        const f32x4 cv = *reinterpret_cast<const f32x4*>(cr + k);
+        const f32x4 sv = *reinterpret_cast<const f32x4*>(sr + k);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const bool is = x == 0 || (mine >> (2 * (k + e)) & 3) == (uint32_t)x;
+          c[k + e] = is ? cv[e] : c[k + e];
+          s[k + e] = is ? sv[e] : s[k + e];
+        }
+      }
+    }
+  } else if (p.half > 0) {
     const float* cr = p.cos + pos * p.half;
     const float* sr = p.sin + pos * p.half;
     const int at = 8 * i < 2 * p.half ? (p.interleaved ? 4 * i : (8 * i) % p.half) : 0;

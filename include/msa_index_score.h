@@ -368,6 +368,35 @@ msa_status_t msa_cache_append(const msa_append_item_t* items, int32_t num_items,
                               const int32_t* cu_seqlens_q, const int32_t* kv_len, int32_t batch,
                               int32_t block_size, void* stream);
 
+#define MSA_APPEND_MAX_AXES 4
+
+/*
+ * The same with several position axes (time, height and width of an image's or
+ * a video's tokens): pair r of token t is rotated by the angles of row
+ * axis_positions[pair_axes[r], t] instead of the token's position in its
+ * sequence, which still says where the row is stored.
+ *
+ * axis_positions  device int32 [axes, T], compact.
+ * axes            1..MSA_APPEND_MAX_AXES (MSA_ERR_ATTR otherwise).
+ * pair_axes       host uint8 [rotary_dim / 2]: the axis of each pair, below axes
+ *                 (MSA_ERR_ATTR); read before the call returns.  Axes in runs of
+ *                 pairs (0 0 .. 1 1 .. 2 2) or in turn (0 1 2 0 1 2 ..) are both
+ *                 said this way.
+ *
+ * A token with any axis position outside [0, positions), or before position 0 of
+ * its sequence, is skipped in every item; its position may be at or past
+ * `positions`.  If no item is rotated, the axes are not looked at.  Everything else
+ * as msa_cache_append.
+ */
+msa_status_t msa_cache_append_axes(const msa_append_item_t* items, int32_t num_items,
+                                   const float* cos, const float* sin, int64_t positions,
+                                   int32_t rotary_dim, int32_t interleaved,
+                                   const int32_t* axis_positions, int32_t axes,
+                                   const uint8_t* pair_axes, const int32_t* block_table,
+                                   int64_t max_blocks, const int32_t* cu_seqlens_q,
+                                   const int32_t* kv_len, int32_t batch, int32_t block_size,
+                                   void* stream);
+
 /*
  * Attention of the new tokens: over a paged cache (a chunk of a prompt, one
  * decode token, speculative tokens, or requests of each kind in one batch), or

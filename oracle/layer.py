@@ -202,10 +202,13 @@ def encode_mxfp4(y):
             torch.tensor(scales, dtype=torch.uint8))
 
 
-def append(item, cos, sin, block_table, cu_seqlens_q, kv_len, interleaved, any_rotated):
+def append(item, cos, sin, block_table, cu_seqlens_q, kv_len, interleaved, any_rotated,
+           axis_positions=None, pair_axes=None):
     """What ``msa_cache_append`` leaves of one item (src, dst, layout, scale,
     rotate; CPU tensors): (dst, scale, exact float64 rows, term magnitudes, written
-    mask [T, H]), the rows and magnitudes per token and head."""
+    mask [T, H]), the rows and magnitudes per token and head.  With
+    ``axis_positions`` [axes, T] pair r turns by the position of axis
+    ``pair_axes[r]``."""
     src, dst, layout, scale, rotate = item
     T, H, _ = src.shape
     dst = dst.clone()
@@ -215,12 +218,18 @@ def append(item, cos, sin, block_table, cu_seqlens_q, kv_len, interleaved, any_r
     written = torch.zeros(T, H, dtype=torch.bool)
     kv = [max(int(x), 0) for x in kv_len]
     for t, b, pos in positions(cu_seqlens_q, kv_len, T):
-        if pos < 0 or (any_rotated and pos >= cos.shape[0]):
+        turns = [pos] * (cos.shape[1] if any_rotated else 0)
+        if any_rotated and axis_positions is not None:
+            if not all(0 <= int(x) < cos.shape[0] for x in axis_positions[:, t]):
+                continue
+            turns = [int(axis_positions[a, t]) for a in pair_axes]
+        if pos < 0 or (turns and max(turns) >= cos.shape[0]):
             continue
+        pair = torch.arange(len(turns))
         for h in range(H):
             y, mag = src[t, h].double(), src[t, h].double().abs()
             if rotate:
-                y, mag = rotated(src[t, h], cos[pos], sin[pos], interleaved)
+                y, mag = rotated(src[t, h], cos[turns, pair], sin[turns, pair], interleaved)
             if layout == "ROWS":
                 at, sat = (t, h), (t, h)
             elif layout == "TND":
