@@ -39,7 +39,8 @@ EXPORTED = ("msa_index_score", "msa_index_score_family", "msa_index_score_ex",
             "msa_index_score_out_width", "msa_status_str",
             "msa_index_score_kernel_family", "msa_block_topk", "msa_cache_append",
             "msa_attention", "msa_block_attention", "msa_attention_workspace",
-            "msa_attention_tile_rows", "msa_step_tables", "msa_cache_append_axes")
+            "msa_attention_tile_rows", "msa_step_tables", "msa_cache_append_axes",
+            "msa_attention_ex")
 LOCAL_MODE_CODE = {"request": 0, "query": 1}
 
 
@@ -123,6 +124,9 @@ def load_library(path: Optional[str] = None):
         three = [ptr] * 3                # descriptors, as packed bytes or byref()
         lib.msa_attention.argtypes = three + tail
         lib.msa_attention.restype = ctypes.c_int
+        # softcap, slopes, visible after softmax_scale
+        lib.msa_attention_ex.argtypes = three + tail[:9] + [ctypes.c_float, ptr, ptr] + tail[9:]
+        lib.msa_attention_ex.restype = ctypes.c_int
         lib.msa_block_attention.argtypes = three + [ptr, i32] + tail
         lib.msa_block_attention.restype = ctypes.c_int
         lib.msa_attention_workspace.argtypes = [i64, i32, i32, i32, i64, i32]
@@ -669,7 +673,8 @@ _workspace_bytes = functools.lru_cache(maxsize=1024)(msa_attention_workspace)
 
 
 def _attention(query, key, value, blocks, block_table, cu_seqlens_q, kv_len, layout, sparse_mode,
-               softmax_scale, out, lse, max_blocks, workspace, stream, block_size):
+               softmax_scale, out, lse, max_blocks, workspace, stream, block_size, softcap=0.0,
+               slopes=None, visible=None):
     lib = _lib or load_library()
     index = query.get_device()
     if (key.get_device() != index or value.get_device() != index or
@@ -706,6 +711,14 @@ def _attention(query, key, value, blocks, block_table, cu_seqlens_q, kv_len, lay
         k = blocks.shape[2]
     if workspace is not None and not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous")
+    if slopes is not None and (slopes.dtype != torch.float32 or slopes.shape != (Hq,) or
+                               not slopes.is_contiguous() or slopes.get_device() != index):
+        raise ValueError(f"slopes must be a contiguous float32 [{Hq}] tensor on {query.device}, "
+                         f"got {slopes.dtype} {tuple(slopes.shape)} on {slopes.device}")
+    if visible is not None and (visible.dtype != torch.int32 or visible.shape != (T, 2) or
+                                not visible.is_contiguous() or visible.get_device() != index):
+        raise ValueError(f"visible must be a contiguous int32 [{T}, 2] tensor on {query.device}, "
+                         f"got {visible.dtype} {tuple(visible.shape)} on {visible.device}")
     if index < 0 and query.numel():
         raise ValueError(f"the tensors must be on a GPU, query is on {query.device}")
     scale = 1.0 / math.sqrt(D) if softmax_scale is None else float(softmax_scale)
@@ -721,14 +734,18 @@ def _attention(query, key, value, blocks, block_table, cu_seqlens_q, kv_len, lay
                 with torch.cuda.stream(_stream_of(handle, query.device)):
                     workspace = query.new_empty(need, dtype=torch.uint8)
         wb = 0 if workspace is None else workspace.numel() * workspace.element_size()
-        tail = (_address(block_table), max_blocks, cu_seqlens_q.data_ptr(), kv_len.data_ptr(), B,
-                int(block_size), lay, int(sparse_mode), scale, out.data_ptr(), _address(lse),
-                _address(workspace), wb, handle)
-        if blocks is None:
-            st = lib.msa_attention(_packed(query), _packed(key), _packed(value), *tail)
-        else:
+        lens = (_address(block_table), max_blocks, cu_seqlens_q.data_ptr(), kv_len.data_ptr(), B,
+                int(block_size), lay, int(sparse_mode), scale)
+        rest = (out.data_ptr(), _address(lse), _address(workspace), wb, handle)
+        if blocks is not None:
             st = lib.msa_block_attention(_packed(query), _packed(key), _packed(value),
-                                         blocks.data_ptr(), k, *tail)
+                                         blocks.data_ptr(), k, *lens, *rest)
+        elif softcap or slopes is not None or visible is not None:
+            st = lib.msa_attention_ex(_packed(query), _packed(key), _packed(value), *lens,
+                                      float(softcap or 0.0), _address(slopes), _address(visible),
+                                      *rest)
+        else:
+            st = lib.msa_attention(_packed(query), _packed(key), _packed(value), *lens, *rest)
     if st:
         _raise_status(st)
     return out
@@ -739,16 +756,24 @@ def msa_attention(query: torch.Tensor, key: torch.Tensor, value: torch.Tensor,
                   kv_len: torch.Tensor, layout, sparse_mode: int, softmax_scale: Optional[float],
                   out: torch.Tensor, max_blocks: int, lse: Optional[torch.Tensor] = None,
                   workspace: Optional[torch.Tensor] = None, stream=None,
-                  block_size: int = BLOCK_SIZE) -> torch.Tensor:
+                  block_size: int = BLOCK_SIZE, softcap: Optional[float] = None,
+                  slopes: Optional[torch.Tensor] = None,
+                  visible: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Call the C ABI: ``out`` ([T, Hq, 128], the query's type) receives the
     attention of every new token over its request's visible keys, ``lse``
     ([T, Hq] float32, if given) the log of its softmax's sum; asynchronous on
     ``stream`` (default: torch's current stream).  ``softmax_scale`` None is
     1 / sqrt(128).  Without ``workspace`` the memory that a split over the keys
-    needs (``msa_attention_workspace``) is allocated here."""
+    needs (``msa_attention_workspace``) is allocated here.
+
+    ``softcap`` (None or 0: none) caps the scores by softcap * tanh(S / softcap);
+    ``slopes`` ([Hq] float32) takes slopes[h] * |position - key| off them;
+    ``visible`` ([T, 2] int32: first key and end of keys) narrows what each token
+    sees beyond ``sparse_mode`` (documents with mode 3, images and prefixes with
+    mode 0)."""
     return _attention(query, key, value, None, block_table, cu_seqlens_q, kv_len, layout,
                       sparse_mode, softmax_scale, out, lse, max_blocks, workspace, stream,
-                      block_size)
+                      block_size, softcap, slopes, visible)
 
 
 def msa_block_attention(query: torch.Tensor, key: torch.Tensor, value: torch.Tensor,
@@ -792,8 +817,10 @@ def attention(query: torch.Tensor, key: torch.Tensor, value: torch.Tensor,
               block_table: Optional[torch.Tensor], cu_seqlens_q: torch.Tensor,
               kv_len: torch.Tensor, layout, sparse_mode: int = 3,
               softmax_scale: Optional[float] = None, max_blocks: Optional[int] = None,
-              return_lse: bool = False, stream=None):
-    """Allocate ``out`` (and ``lse``) and fill them with ``msa_attention``;
+              return_lse: bool = False, stream=None, softcap: Optional[float] = None,
+              slopes: Optional[torch.Tensor] = None, visible: Optional[torch.Tensor] = None):
+    """Allocate ``out`` (and ``lse``) and fill them with ``msa_attention`` (which
+    says what ``softcap``, ``slopes`` and ``visible`` do);
     returns ``out`` or ``(out, lse)``.  Rows that no request holds (a padded
     batch) are not written.  On a ``stream`` that is given, they are that
     stream's memory: use on another stream needs an ordering, and ``record_stream``
@@ -802,7 +829,8 @@ def attention(query: torch.Tensor, key: torch.Tensor, value: torch.Tensor,
     if max_blocks is None:
         max_blocks = _default_blocks(key, block_table)
     _attention(query, key, value, None, block_table, cu_seqlens_q, kv_len, layout, sparse_mode,
-               softmax_scale, out, lse, max_blocks, None, stream, BLOCK_SIZE)
+               softmax_scale, out, lse, max_blocks, None, stream, BLOCK_SIZE, softcap, slopes,
+               visible)
     return (out, lse) if return_lse else out
 
 

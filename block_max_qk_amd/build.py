@@ -11,7 +11,9 @@ import sys
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 SOURCES = [os.path.join(HERE, "csrc", f) for f in ("msa_index_score.hip", "msa_attention.hip",
-                                                   "msa_append.hip", "msa_tables.hip")]
+                                                   "msa_append.hip", "msa_tables.hip",
+                                                   "msa_attention_forms_bf16.hip",
+                                                   "msa_attention_forms_f16.hip")]
 LIB = os.path.join(HERE, "libmsa_index_score.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 

@@ -9,6 +9,7 @@
 #include <cstdint>
 
 #include "msa_attention.hpp"
+#include "msa_attention_forms.hpp"
 #include "msa_host.hpp"
 
 namespace {
@@ -123,10 +124,12 @@ bool sizes_ok(int64_t T, int32_t batch, int32_t Hq, int32_t Hkv, int64_t max_blo
 }
 
 template <int KK>
-hipError_t launch(const AttnParams& p, const Plan& plan, int64_t grid, hipStream_t s) {
+hipError_t launch(const AttnParams& p, const Plan& plan, int form, int64_t grid, hipStream_t s) {
   hipError_t e;
   const dim3 gr((unsigned)grid);
-  if (plan.rows == msa::kAttnRows) {
+  if (form != 0) {
+    e = msa::launch_form<KK>(p, plan.rows, form, gr, s);
+  } else if (plan.rows == msa::kAttnRows) {
     e = msa::launch_kernel(p.blocks ? msa::attn_rows_kernel<KK, true>
                                     : msa::attn_rows_kernel<KK, false>,
                            gr, dim3(256), s, p);
@@ -144,12 +147,45 @@ hipError_t launch(const AttnParams& p, const Plan& plan, int64_t grid, hipStream
   return e;
 }
 
+// Forms of the scores, as the entry points take them.
+struct Forms {
+  float softcap;            // 0: none
+  const float* slopes;      // or NULL
+  const int32_t* visible;   // or NULL
+};
+
+// The forms in the kernels' terms; a sum of ScoreForms.
+int set_forms(const Forms& f, float scale, AttnParams& p) {
+  int form = 0;
+  p.slopes = f.slopes;
+  p.visible = reinterpret_cast<const int2*>(f.visible);
+  p.per_scale = 1.f / scale;
+  if (f.slopes) form |= msa::kBias;
+  if (f.softcap > 0.f) {
+    form |= msa::kCap;
+    // tanh(x) = x (1 + c1 x^2 + .. + c4 x^8) for |x| <= 0.6, off by 2.8e-8 at most
+    constexpr double kTanh[5] = {1.0, -0.33332248, 0.133080983, -0.0519943375, 0.0153192069};
+    const double a = (double)scale / f.softcap;
+    double unit = (double)scale * msa::kLog2e;
+    p.cap_top = f.softcap * msa::kLog2e;
+    p.cap_twice = (float)(2.0 * msa::kLog2e * a);
+    p.cap_near = (float)(0.6 / a);
+    for (int i = 0; i < 5; ++i, unit *= a * a) {
+      p.cap_poly[i] = (float)(kTanh[i] * unit);
+      // (a cap so small that a coefficient has no float32: never near)
+      if (!std::isfinite(p.cap_poly[i])) p.cap_near = -1.f;
+    }
+  }
+  if (f.visible || form) form |= msa::kRange;
+  return form;
+}
+
 msa_status_t run(const msa_tensor_t* query, const msa_tensor_t* key, const msa_tensor_t* value,
                  const int32_t* blocks, int64_t num_blocks, bool selected,
                  const int32_t* block_table, int64_t max_blocks, const int32_t* cu_seqlens_q,
                  const int32_t* kv_len, int32_t batch, int32_t block_size, int32_t layout,
-                 int32_t sparse_mode, float softmax_scale, void* out, float* lse, void* workspace,
-                 int64_t workspace_bytes, void* stream) {
+                 int32_t sparse_mode, float softmax_scale, const Forms& forms, void* out,
+                 float* lse, void* workspace, int64_t workspace_bytes, void* stream) {
   if (!query || !key || !value || !cu_seqlens_q) return MSA_ERR_NULL;
   if (batch > 0 && !kv_len) return MSA_ERR_NULL;
   if (query->ndim == 3 && query->shape[0] > 0 && !out) return MSA_ERR_NULL;
@@ -186,6 +222,13 @@ msa_status_t run(const msa_tensor_t* query, const msa_tensor_t* key, const msa_t
   if (batch == 0 && T > 0) return MSA_ERR_SHAPE;
   if (sparse_mode != 0 && sparse_mode != 3) return MSA_ERR_ATTR;
   if (!(softmax_scale > 0.f) || !std::isfinite(softmax_scale * msa::kLog2e)) return MSA_ERR_ATTR;
+  if (!(forms.softcap >= 0.f) || !std::isfinite(forms.softcap * msa::kLog2e)) return MSA_ERR_ATTR;
+  if (forms.softcap > 0.f && !std::isfinite(2.f * msa::kLog2e * softmax_scale / forms.softcap))
+    return MSA_ERR_ATTR;
+  if (forms.slopes && !std::isfinite(1.f / softmax_scale)) return MSA_ERR_ATTR;
+  if ((reinterpret_cast<uintptr_t>(forms.slopes) & 3u) ||
+      (reinterpret_cast<uintptr_t>(forms.visible) & 7u))
+    return MSA_ERR_STRIDE;
   if (selected) {
     if (num_blocks < 1 || num_blocks > 64) return MSA_ERR_ATTR;
     if (T > 0 && !blocks) return MSA_ERR_NULL;
@@ -255,9 +298,10 @@ msa_status_t run(const msa_tensor_t* query, const msa_tensor_t* key, const msa_t
   p.balanced = plan.balanced ? 1 : 0;
   p.join_rows = (int32_t)std::clamp<int64_t>(T * Hq / 8192, 1, 64);   // the chip holds 8192 waves
   p.per_target = 1.f / plan.target;
+  const int form = set_forms(forms, softmax_scale, p);
   hipStream_t s = static_cast<hipStream_t>(stream);
-  const hipError_t e = query->dtype == MSA_DTYPE_BF16 ? launch<msa::KBF16>(p, plan, grid, s)
-                                                      : launch<msa::KF16>(p, plan, grid, s);
+  const hipError_t e = query->dtype == MSA_DTYPE_BF16 ? launch<msa::KBF16>(p, plan, form, grid, s)
+                                                      : launch<msa::KF16>(p, plan, form, grid, s);
   return e == hipSuccess ? MSA_OK : MSA_ERR_HIP;
 }
 
@@ -272,8 +316,21 @@ msa_status_t msa_attention(const msa_tensor_t* query, const msa_tensor_t* key,
                            float softmax_scale, void* out, float* lse, void* workspace,
                            int64_t workspace_bytes, void* stream) {
   return run(query, key, value, nullptr, 0, false, block_table, max_blocks, cu_seqlens_q, kv_len,
-             batch, block_size, layout, sparse_mode, softmax_scale, out, lse, workspace,
+             batch, block_size, layout, sparse_mode, softmax_scale, Forms{}, out, lse, workspace,
              workspace_bytes, stream);
+}
+
+msa_status_t msa_attention_ex(const msa_tensor_t* query, const msa_tensor_t* key,
+                              const msa_tensor_t* value, const int32_t* block_table,
+                              int64_t max_blocks, const int32_t* cu_seqlens_q,
+                              const int32_t* kv_len, int32_t batch, int32_t block_size,
+                              int32_t layout, int32_t sparse_mode, float softmax_scale,
+                              float softcap, const float* slopes, const int32_t* visible,
+                              void* out, float* lse, void* workspace, int64_t workspace_bytes,
+                              void* stream) {
+  return run(query, key, value, nullptr, 0, false, block_table, max_blocks, cu_seqlens_q, kv_len,
+             batch, block_size, layout, sparse_mode, softmax_scale,
+             Forms{softcap, slopes, visible}, out, lse, workspace, workspace_bytes, stream);
 }
 
 msa_status_t msa_block_attention(const msa_tensor_t* query, const msa_tensor_t* key,
@@ -285,8 +342,8 @@ msa_status_t msa_block_attention(const msa_tensor_t* query, const msa_tensor_t* 
                                  void* out, float* lse, void* workspace, int64_t workspace_bytes,
                                  void* stream) {
   return run(query, key, value, blocks, num_blocks, true, block_table, max_blocks, cu_seqlens_q,
-             kv_len, batch, block_size, layout, sparse_mode, softmax_scale, out, lse, workspace,
-             workspace_bytes, stream);
+             kv_len, batch, block_size, layout, sparse_mode, softmax_scale, Forms{}, out, lse,
+             workspace, workspace_bytes, stream);
 }
 
 int64_t msa_attention_workspace(int64_t T, int32_t batch, int32_t Hq, int32_t Hkv,

@@ -53,7 +53,21 @@ struct AttnParams {
   int32_t join_rows;           // rows of a wave of attn_join_kernel
   int32_t balanced;            // dense tiles are split by attn_part
   float per_target;            // 1 / the parts per KV head that attn_part aims at
+  // the scores' forms (kCap, kBias, kRange)
+  const float* slopes;         // [Hq] or nullptr
+  const int2* visible;         // [T]: first visible key and the end of them, or nullptr
+  float per_scale;             // 1 / softmax_scale
+  float cap_top;               // softcap * log2(e)
+  float cap_twice;             // 2 log2(e) softmax_scale / softcap
+  float cap_near;              // products up to which the polynomial is the tanh
+  float cap_poly[5];           // its coefficients, on a product's square
 };
+
+// Forms of the scores that a kernel is compiled for (0: plain ones).
+//  kCap    capped by softcap * tanh(S / softcap)
+//  kBias   less slopes[h] * |pos - j|
+//  kRange  keys narrowed by `visible`, where it is given (set in every form but 0)
+enum ScoreForm : int { kCap = 1, kBias = 2, kRange = 4 };
 
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
@@ -225,6 +239,78 @@ __device__ __forceinline__ int attn_last(const AttnParams& p, const AttnTile& w,
   return min(p.causal ? w.len - w.Lq + i : w.L - 1, w.L - 1);
 }
 
+// First and last visible key of the request's i-th new token (none: last < first).
+struct Span {
+  int first, last;
+};
+template <int F>
+__device__ __forceinline__ Span attn_span(const AttnParams& p, const AttnTile& w, int i) {
+  Span s{0, attn_last(p, w, i)};
+  if constexpr (F != 0) {
+    if (p.visible) {
+      const int2 v = p.visible[w.t0 - w.i0 + i];
+      s.first = max(v.x, 0);
+      s.last = min(s.last, max(v.y, 0) - 1);
+      if (s.first > s.last) s = Span{0, -1};
+    }
+  }
+  return s;
+}
+
+// Over a tile's tokens: the smallest and largest first visible key (of tokens
+// that see one), the smallest and largest last one.
+struct TileSpan {
+  int first, first_hi, last_lo, last;
+};
+template <int F>
+__device__ __forceinline__ TileSpan tile_span(const AttnParams& p, const AttnTile& w) {
+  if constexpr (F != 0) {
+    if (p.visible) {
+      uint32_t a = ~0u, b = 0, c = ~0u, d = 0;         // (numbers one higher: none is 0)
+      for (int i = lane_id(); i < w.ntok; i += 64) {
+        const Span s = attn_span<F>(p, w, w.i0 + i);
+        if (s.last >= 0) {
+          a = min(a, (uint32_t)s.first);
+          b = max(b, (uint32_t)s.first);
+        }
+        c = min(c, (uint32_t)(s.last + 1));
+        d = max(d, (uint32_t)(s.last + 1));
+      }
+      uint32_t lo, hi, end_lo, end;
+      wave_min_max(a, b, lo, hi);
+      wave_min_max(c, d, end_lo, end);
+      return TileSpan{end ? (int)lo : 0, (int)hi, (int)end_lo - 1, (int)end - 1};
+    }
+  }
+  return TileSpan{0, 0, attn_last(p, w, w.i0), attn_last(p, w, w.i0 + w.ntok - 1)};
+}
+
+// Capped scores in units of log2: cap_top * tanh(a s) of the products s, with a =
+// softmax_scale / softcap.  Where all of a wave's |a s| are at most 0.6, an odd
+// polynomial of degree 9 (off by 3e-8 of the cap at most, fitted to tanh for the
+// smallest largest error; a multiplication and 4 fused ones, 10 cycles of a SIMD
+// against 22), elsewhere 1 - 2 / (exp(2 a s) + 1), whose error is a few roundings
+// of the cap itself (infinities give the cap).
+__device__ __forceinline__ float cap_slope(const AttnParams& p, float s) {   // capped / s
+  const float u = s * s;
+  float r = __builtin_fmaf(u, p.cap_poly[4], p.cap_poly[3]);
+  r = __builtin_fmaf(u, r, p.cap_poly[2]);
+  r = __builtin_fmaf(u, r, p.cap_poly[1]);
+  return __builtin_fmaf(u, r, p.cap_poly[0]);
+}
+__device__ __forceinline__ float cap_far(const AttnParams& p, float s) {
+  const float e = __builtin_amdgcn_exp2f(s * p.cap_twice);
+  return __builtin_fmaf(-2.f * p.cap_top, __builtin_amdgcn_rcpf(e + 1.f), p.cap_top);
+}
+
+// Values of keys j and j + 1 with those outside the span cleared.
+template <int F>
+__device__ __forceinline__ int seen_pair(int v, int j, const Span& s) {
+  v = j + 1 <= s.last ? v : j <= s.last ? v & 0xFFFF : 0;
+  if constexpr (F != 0) v = j >= s.first ? v : j + 1 >= s.first ? v & (int)0xFFFF0000u : 0;
+  return v;
+}
+
 // Two floats -> one register of two 16-bit operands, rounded to nearest.
 template <int KK>
 __device__ __forceinline__ int pack2(float a, float b) {
@@ -353,7 +439,7 @@ constexpr int kAttnRows = 16;
 constexpr int kRowWaves = 4;
 constexpr int kRowStage = 16384;     // 32 keys' K and V rows
 
-template <int KK, bool SEL>
+template <int KK, bool SEL, int F = 0>
 __global__ __launch_bounds__(256, 1) void attn_rows_kernel(AttnParams p) {
   __shared__ __attribute__((aligned(16))) uint8_t ring[kRowWaves][2][kRowStage];
   int rest = blockIdx.x, split = 0, parts = 1;
@@ -383,13 +469,22 @@ __global__ __launch_bounds__(256, 1) void attn_rows_kernel(AttnParams p) {
   const int ti = n / p.hpt;
   const int hg = hc * p.hpt + (n - ti * p.hpt);
   const bool row_ok = ti < w.ntok && ti < p.tpt && hg < p.g;
-  const int lim = row_ok ? attn_last(p, w, w.i0 + ti) : -1;
-  const int lim_lo = attn_last(p, w, w.i0);
-  const int lim_hi = attn_last(p, w, w.i0 + w.ntok - 1);
-  const int nb = lim_hi >= 0 ? lim_hi / kP + 1 : 0;    // blocks with a visible key
+  const Span mine_sees = row_ok ? attn_span<F>(p, w, w.i0 + ti) : Span{0, -1};
+  const int lim = mine_sees.last;
+  const TileSpan sees = tile_span<F>(p, w);
+  const int lim_lo = sees.last_lo, lim_hi = sees.last;
+  const int nb = lim_hi >= 0 ? lim_hi / kP + 1 : 0;    // end of the blocks with a visible key
+  const int nb0 = F ? sees.first / kP : 0;             // and the first of them
+  // (a bias's slope in units of log2, and the row's position)
+  float slope = 0.f;
+  int pos = 0;
+  if constexpr (F & kBias) {
+    if (row_ok) slope = p.slopes[hk * p.g + hg] * kLog2e;
+    pos = w.len - w.Lq + w.i0 + ti;
+  }
 
   // the part's blocks: [b0, b1) of the visible ones, or of the selected list
-  int sel = -1, total = nb;
+  int sel = -1, total = nb - nb0;
   if constexpr (SEL) {
     // one entry per lane; entries outside the visible blocks and repeats of
     // an earlier entry count as none; the rest move to the front.  (The top-k
@@ -410,8 +505,8 @@ __global__ __launch_bounds__(256, 1) void attn_rows_kernel(AttnParams p) {
     if (l >= total) sel = -1;
   }
   if constexpr (SEL) parts = max(1, min(p.nsplit, (total + p.min_blocks - 1) / p.min_blocks));
-  const int b0 = (int)((int64_t)total * split / parts);
-  const int b1 = split < parts ? (int)((int64_t)total * (split + 1) / parts) : b0;
+  const int b0 = nb0 + (int)((int64_t)total * split / parts);
+  const int b1 = split < parts ? nb0 + (int)((int64_t)total * (split + 1) / parts) : b0;
   if (SEL && split >= parts) return;
   const int nst = max(b1 - b0, 0);
 
@@ -499,6 +594,39 @@ __global__ __launch_bounds__(256, 1) void attn_rows_kernel(AttnParams p) {
   f32x4 o[8];
   float m, lsum;
 
+  // products of keys j0 + 4 G + r and j0 + 16 + 4 G + r to scores in units of log2
+  [[maybe_unused]] auto form = [&](f32x4& sa, f32x4& sb, int j0) __attribute__((always_inline)) {
+    if constexpr (F & kCap) {
+      float far = 0.f;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) far = fmaxf(far, fmaxf(fabsf(sa[r]), fabsf(sb[r])));
+      if (!__ballot(far > p.cap_near)) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          sa[r] *= cap_slope(p, sa[r]);
+          sb[r] *= cap_slope(p, sb[r]);
+        }
+      } else {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          sa[r] = cap_far(p, sa[r]);
+          sb[r] = cap_far(p, sb[r]);
+        }
+      }
+    } else {
+      sa *= p.c;
+      sb *= p.c;
+    }
+    if constexpr (F & kBias) {
+      const float away = (float)(pos - j0 - 4 * G);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        sa[r] = __builtin_fmaf(-slope, fabsf(away - r), sa[r]);
+        sb[r] = __builtin_fmaf(-slope, fabsf(away - (16 + r)), sb[r]);
+      }
+    }
+  };
+
   // One block's keys and values at kt; with CAREFUL as in attn_tile_kernel.
   // (kt is one half of the ring while copies into the other are in flight, and
   // the parameters say that the two do not overlap: reads of LDS that may
@@ -525,17 +653,20 @@ __global__ __launch_bounds__(256, 1) void attn_rows_kernel(AttnParams p) {
       sa = mfma16x16x32<KK>(*reinterpret_cast<const i32x4*>(kt + n * 256 + ch), qv[k], sa);
       sb = mfma16x16x32<KK>(*reinterpret_cast<const i32x4*>(kt + (16 + n) * 256 + ch), qv[k], sb);
     }
-    if (!there || j0 + 31 > lim_lo) {
+    if constexpr (F != 0) form(sa, sb, j0);
+    if (!there || j0 + 31 > lim_lo || (F && j0 < sees.first_hi)) {
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         const int j = j0 + 4 * G + r;
-        sa[r] = there && j <= lim ? sa[r] : -__builtin_inff();
-        sb[r] = there && j + 16 <= lim ? sb[r] : -__builtin_inff();
+        sa[r] = there && j <= lim && (!F || j >= mine_sees.first) ? sa[r] : -__builtin_inff();
+        sb[r] = there && j + 16 <= lim && (!F || j + 16 >= mine_sees.first) ? sb[r]
+                                                                          : -__builtin_inff();
       }
     }
     float mx = fmaxf(fmaxf(fmaxf(sa[0], sa[1]), fmaxf(sa[2], sa[3])),
                      fmaxf(fmaxf(sb[0], sb[1]), fmaxf(sb[2], sb[3])));
-    mx = max_xor32(max_xor16(mx)) * p.c;
+    const float c = F ? 1.f : p.c;               // (other forms are in units of log2)
+    mx = max_xor32(max_xor16(mx)) * c;
     if (__ballot(mx > m + kReach<KK>)) {
       const float mn = moved<KK>(m, mx);
       const float alpha = exp2_hw(m - (mn == -__builtin_inff() ? 0.f : mn));
@@ -548,8 +679,8 @@ __global__ __launch_bounds__(256, 1) void attn_rows_kernel(AttnParams p) {
     float pa[4], pb[4];
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-      pa[r] = exp2_hw(__builtin_fmaf(sa[r], p.c, -ms));
-      pb[r] = exp2_hw(__builtin_fmaf(sb[r], p.c, -ms));
+      pa[r] = exp2_hw(__builtin_fmaf(sa[r], c, -ms));
+      pb[r] = exp2_hw(__builtin_fmaf(sb[r], c, -ms));
     }
     lsum += ((pa[0] + pa[1]) + (pa[2] + pa[3])) + ((pb[0] + pb[1]) + (pb[2] + pb[3]));
     const i32x4 pf = {pack2<KK>(pa[0], pa[1]), pack2<KK>(pa[2], pa[3]), pack2<KK>(pb[0], pb[1]),
@@ -566,15 +697,13 @@ __global__ __launch_bounds__(256, 1) void attn_rows_kernel(AttnParams p) {
       for (int d = 0; d < 8; ++d) o[d] = mfma16x16x32<KK>(value(d), pf, o[d]);
     } else {
       for (int tk = 0; tk < w.ntok; ++tk) {
-        const int end = attn_last(p, w, w.i0 + tk);
+        const Span sp = attn_span<F>(p, w, w.i0 + tk);
 #pragma unroll
         for (int d = 0; d < 8; ++d) {
           i32x4 v = value(d);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int j = j0 + 16 * (e >> 1) + 4 * G + 2 * (e & 1);
-            v[e] = j + 1 <= end ? v[e] : j <= end ? v[e] & 0xFFFF : 0;
-          }
+          for (int e = 0; e < 4; ++e)
+            v[e] = seen_pair<F>(v[e], j0 + 16 * (e >> 1) + 4 * G + 2 * (e & 1), sp);
           const f32x4 x = mfma16x16x32<KK>(v, pf, o[d]);
 #pragma unroll
           for (int r = 0; r < 4; ++r) o[d][r] = ti == tk ? x[r] : o[d][r];
@@ -629,7 +758,7 @@ __global__ __launch_bounds__(256, 1) void attn_rows_kernel(AttnParams p) {
   };
 
   pass(std::false_type{});
-  if (w.ntok > 1) {
+  if (F || w.ntok > 1) {
     float odd = 0.f;
 #pragma unroll
     for (int d = 0; d < 8; ++d)
@@ -864,7 +993,7 @@ __device__ __forceinline__ void copy_plain(const AttnParams& p, uint8_t* kring, 
 // inputs costs only the look at its accumulators.
 // ---------------------------------------------------------------------------
 
-template <int KK, int NW>
+template <int KK, int NW, int F = 0>
 __global__ __launch_bounds__(64 * NW, 2) void attn_tile_kernel(AttnParams p) {
   constexpr int SB = kTileKeys * 256;          // bytes of a stage's K (or V) rows
   constexpr int NI = SB / 1024 / NW;           // copies of each per wave and stage
@@ -908,14 +1037,27 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tile_kernel(AttnParams p) {
   const int ti = row / p.hpt;
   const int hg = hc * p.hpt + (row - ti * p.hpt);
   const bool row_ok = row < p.hpt * p.tpt && ti < w.ntok && hg < p.g;
-  const int lim = row_ok ? attn_last(p, w, w.i0 + ti) : -1;
-  const int lim_lo = attn_last(p, w, w.i0);
-  const int lim_hi = attn_last(p, w, w.i0 + w.ntok - 1);
-  const int total = lim_hi >= 0 ? lim_hi / kP + 1 : 0;
+  const TileSpan sees = tile_span<F>(p, w);
+  const int lim_lo = sees.last_lo, lim_hi = sees.last;
+  const int nb0 = F ? sees.first / kP : 0;
+  const int total = lim_hi >= 0 ? lim_hi / kP + 1 - nb0 : 0;
+  // (F: a lane without a row sees everything, so that it calls for no mask)
+  const Span mine = row_ok ? attn_span<F>(p, w, w.i0 + ti) : Span{0, F ? INT32_MAX : -1};
+  const int lim = mine.last;
+  // a bias's slope, in units of log2 where it is added to capped scores, of the
+  // products where it is what their sums begin with; and the row's position
+  [[maybe_unused]] float slope = 0.f;
+  [[maybe_unused]] int pos = INT32_MAX;
+  if constexpr (F & kBias) {
+    if (row_ok) {
+      slope = p.slopes[hk * p.g + hg] * (F & kCap ? kLog2e : p.per_scale);
+      pos = w.len - w.Lq + w.i0 + ti;
+    }
+  }
   parts = max(1, min(parts, (total + p.min_blocks - 1) / p.min_blocks));
   if (split >= parts) return;
-  const int b0 = (int)((int64_t)total * split / parts);
-  const int b1 = (int)((int64_t)total * (split + 1) / parts);
+  const int b0 = nb0 + (int)((int64_t)total * split / parts);
+  const int b1 = nb0 + (int)((int64_t)total * (split + 1) / parts);
 
   i32x4 qv[8];
 #pragma unroll
@@ -956,10 +1098,38 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tile_kernel(AttnParams p) {
   // other parts of the rings, and the parameters say so, as in
   // attn_rows_kernel.)
   f32x16 st[2];
-  auto scores = [&](const uint8_t* __restrict kt) __attribute__((always_inline)) {
+  // A stage that some row of the wave does not see whole, or (with a bias) has
+  // keys behind its own position in.
+  auto at_edge = [&](const Entry& cur, int in) __attribute__((always_inline)) -> bool {
+    const int j0 = cur.beta * kP + in * kTileKeys;
+    if constexpr (F == 0) return !cur.there || j0 + kTileKeys - 1 > lim_lo;
+    const int end = F & kBias ? min(lim, pos) : lim;
+    return !cur.there || __ballot(j0 + kTileKeys - 1 > end || j0 < mine.first);
+  };
+  auto scores = [&](const uint8_t* __restrict kt, [[maybe_unused]] int j0,
+                    [[maybe_unused]] bool edge) __attribute__((always_inline)) {
     // S^T, two tiles of 32 keys: register r of tile t is key
     // j0 + 32 t + 8 (r / 4) + 4 h + r % 4 of row n
-    st[0] = st[1] = f32x16{};
+    if constexpr ((F & kBias) && !(F & kCap)) {
+      // (the bias costs one instruction a score: the sums begin with it)
+      const float away = (float)(pos - j0 - 4 * h);
+      if (edge) {
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int r = 0; r < 16; ++r)
+            st[t][r] = -slope * fabsf(away - (32 * t + 8 * (r >> 2) + (r & 3)));
+      } else {
+        const float from = -slope * away;
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int r = 0; r < 16; ++r)
+            st[t][r] = __builtin_fmaf(slope, 32 * t + 8 * (r >> 2) + (r & 3), from);
+      }
+    } else {
+      st[0] = st[1] = f32x16{};
+    }
     // (K fragments are read KLEAD ahead of their MFMAs and pinned there: left to
     // itself the compiler read each right before its use, and every MFMA waited
     // for the LDS)
@@ -979,26 +1149,70 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tile_kernel(AttnParams p) {
       __builtin_amdgcn_sched_barrier(0);
     }
   };
-  auto absorb = [&](const uint8_t* __restrict vt, const Entry& cur, int in, auto careful)
-      __attribute__((always_inline)) {
+  auto absorb = [&](const uint8_t* __restrict vt, const Entry& cur, int in, bool edge,
+                    auto careful) __attribute__((always_inline)) {
     const int j0 = cur.beta * kP + in * kTileKeys;
     const bool there = cur.there;
-    if (!there || j0 + kTileKeys - 1 > lim_lo) {
-      // (compared as constants against one value per lane: the keys' numbers
-      // themselves would take 32 registers through the whole loop)
-      const int rel = there ? lim - j0 - 4 * h : -1;
+    // Capped scores: near ones stay products until their weights are taken (the
+    // cap keeps the order, so the maximum is capped by itself); otherwise they
+    // are capped here, in units of log2, and a bias is added.
+    [[maybe_unused]] bool near = false;
+    if constexpr (F & kCap) {
+      float far = 0.f;
 #pragma unroll
       for (int t = 0; t < 2; ++t)
 #pragma unroll
-        for (int r = 0; r < 16; ++r)
-          st[t][r] = 32 * t + 8 * (r >> 2) + (r & 3) <= rel ? st[t][r] : -__builtin_inff();
+        for (int r = 0; r < 16; ++r) far = fmaxf(far, fabsf(st[t][r]));
+      const bool poly = !__ballot(far > p.cap_near);
+      near = poly && !edge && !(F & kBias);
+      if (!near) {
+        if (poly) {
+#pragma unroll
+          for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) st[t][r] *= cap_slope(p, st[t][r]);
+        } else {
+#pragma unroll
+          for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) st[t][r] = cap_far(p, st[t][r]);
+        }
+        if constexpr (F & kBias) {
+          const float away = (float)(pos - j0 - 4 * h);
+#pragma unroll
+          for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int r = 0; r < 16; ++r)
+              st[t][r] = __builtin_fmaf(
+                  -slope, fabsf(away - (32 * t + 8 * (r >> 2) + (r & 3))), st[t][r]);
+        }
+      }
+    }
+    if (edge) {
+      // (compared as constants against one value per lane: the keys' numbers
+      // themselves would take 32 registers through the whole loop)
+      const int rel = there ? lim - j0 - 4 * h : -1;
+      [[maybe_unused]] const int from = mine.first - j0 - 4 * h;
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          const int k = 32 * t + 8 * (r >> 2) + (r & 3);
+          st[t][r] = k <= rel && (!F || k >= from) ? st[t][r] : -__builtin_inff();
+        }
     }
     float mx = st[0][0];
 #pragma unroll
     for (int t = 0; t < 2; ++t)
 #pragma unroll
       for (int r = 0; r < 16; ++r) mx = fmaxf(mx, st[t][r]);
-    mx = max_xor32(mx) * p.c;
+    mx = max_xor32(mx);
+    const float c = F & kCap ? 1.f : p.c;
+    if constexpr (F & kCap) {
+      if (near) mx *= cap_slope(p, mx);
+    } else {
+      mx *= c;
+    }
     if (__ballot(mx > m + kReach<KK>)) {
       const float mn = moved<KK>(m, mx);
       const float alpha = exp2_hw(m - (mn == -__builtin_inff() ? 0.f : mn));
@@ -1011,9 +1225,16 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tile_kernel(AttnParams p) {
     float add = 0.f;
     i32x4 pf[4];
     // weights 2 i and 2 i + 1 of this lane's 32, rounded and packed
-    auto weigh = [&](int i) __attribute__((always_inline)) {
-      const float a = exp2_hw(__builtin_fmaf(st[i >> 3][2 * (i & 7)], p.c, -ms));
-      const float b = exp2_hw(__builtin_fmaf(st[i >> 3][2 * (i & 7) + 1], p.c, -ms));
+    auto weigh = [&](int i, auto poly) __attribute__((always_inline)) {
+      const float x = st[i >> 3][2 * (i & 7)], y = st[i >> 3][2 * (i & 7) + 1];
+      float a, b;
+      if constexpr (decltype(poly)::value) {
+        a = exp2_hw(__builtin_fmaf(x, cap_slope(p, x), -ms));
+        b = exp2_hw(__builtin_fmaf(y, cap_slope(p, y), -ms));
+      } else {
+        a = exp2_hw(__builtin_fmaf(x, c, -ms));
+        b = exp2_hw(__builtin_fmaf(y, c, -ms));
+      }
       add += a + b;
       pf[i >> 2][i & 3] = pack2<KK>(a, b);
     };
@@ -1031,30 +1252,48 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tile_kernel(AttnParams p) {
     if constexpr (!decltype(careful)::value) {
       // (a step's MFMAs run beside the next step's weights, each with one pair
       // of them and the read of a later operand, pinned)
-      constexpr int VLEAD = 3;
-      i32x4 vf[16];
+      auto products = [&](auto poly) __attribute__((always_inline)) {
+        constexpr int VLEAD = 3;
+        i32x4 vf[16];
 #pragma unroll
-      for (int i = 0; i < VLEAD; ++i) vf[i] = value(i);
+        for (int i = 0; i < VLEAD; ++i) vf[i] = value(i);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) weigh(i);
+        for (int i = 0; i < 4; ++i) weigh(i, poly);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        if (i + VLEAD < 16) vf[i + VLEAD] = value(i + VLEAD);
-        o[i & 3] = mfma32x32x16<KK>(vf[i], pf[i >> 2], o[i & 3]);
-        if (i < 12) weigh(i + 4);
-        __builtin_amdgcn_sched_barrier(0);
+        for (int i = 0; i < 16; ++i) {
+          if (i + VLEAD < 16) vf[i + VLEAD] = value(i + VLEAD);
+          o[i & 3] = mfma32x32x16<KK>(vf[i], pf[i >> 2], o[i & 3]);
+          if (i < 12) weigh(i + 4, poly);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      };
+      if constexpr (F & kCap) {
+        if (near)
+          products(std::true_type{});
+        else
+          products(std::false_type{});
+      } else {
+        products(std::false_type{});
       }
       lsum += add;
     } else {
       // token by token: the values of keys that it does not see cleared, its
       // rows' sums kept
+      if constexpr (F & kCap) {
+        if (near) {
 #pragma unroll
-      for (int i = 0; i < 16; ++i) weigh(i);
+          for (int i = 0; i < 16; ++i) weigh(i, std::true_type{});
+        }
+      }
+      if (!near) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) weigh(i, std::false_type{});
+      }
       lsum += add;
       const int first = wave * 32 / p.hpt, last = min((wave * 32 + 31) / p.hpt, w.ntok - 1);
       for (int tk = first; tk <= last; ++tk) {
         if (!__ballot(row_ok && ti == tk)) continue;
-        const int end = attn_last(p, w, w.i0 + tk);
+        const Span sp = attn_span<F>(p, w, w.i0 + tk);
 #pragma unroll
         for (int d = 0; d < 4; ++d) {
           f32x16 x = o[d];
@@ -1062,10 +1301,8 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tile_kernel(AttnParams p) {
           for (int u = 0; u < 4; ++u) {
             i32x4 v = value(4 * u + d);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int j = j0 + 16 * u + 8 * (e >> 1) + 4 * h + 2 * (e & 1);
-              v[e] = j + 1 <= end ? v[e] : j <= end ? v[e] & 0xFFFF : 0;
-            }
+            for (int e = 0; e < 4; ++e)
+              v[e] = seen_pair<F>(v[e], j0 + 16 * u + 8 * (e >> 1) + 4 * h + 2 * (e & 1), sp);
             x = mfma32x32x16<KK>(v, pf[u], x);
           }
 #pragma unroll
@@ -1085,8 +1322,9 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tile_kernel(AttnParams p) {
         __syncthreads();
         copy_plain<NI>(p, kring, vring, wave, rows_of(x, s & 1), kof, vof);
         __syncthreads();
-        scores(kring);
-        absorb(vring, x, s & 1, careful);
+        const bool edge = at_edge(x, s & 1);
+        scores(kring, x.beta * kP + (s & 1) * kTileKeys, edge);
+        absorb(vring, x, s & 1, edge, careful);
       }
       return;
     }
@@ -1099,8 +1337,9 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tile_kernel(AttnParams p) {
         __attribute__((always_inline)) {
       copy_rows<NI>(kd + wave * NI * 1024, r.k, r.kb, kof);
       copy_rows<NI>(vd + wave * NI * 1024, r.v, r.vb, vof);
-      scores(kt);
-      absorb(vt, x, in, careful);
+      const bool edge = at_edge(x, in);
+      scores(kt, x.beta * kP + in * kTileKeys, edge);
+      absorb(vt, x, in, edge, careful);
     };
     copy_rows<NI>(kring + wave * NI * 1024, r.k, r.kb, kof);
     copy_rows<NI>(vring + wave * NI * 1024, r.v, r.vb, vof);
@@ -1135,7 +1374,7 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tile_kernel(AttnParams p) {
 #pragma unroll
   for (int s = 0; s < 8; ++s) landed(qv[s]);
   pass(std::false_type{});
-  if (w.ntok > 1) {
+  if (F || w.ntok > 1) {
     // (x - x is 0 for a finite x only; the products add no rounding of their own)
     float odd = 0.f;
 #pragma unroll

@@ -438,7 +438,43 @@ msa_status_t msa_attention(const msa_tensor_t* query, const msa_tensor_t* key,
                            float softmax_scale, void* out, float* lse, void* workspace,
                            int64_t workspace_bytes, void* stream);
 
-/* The same over selected blocks: j is visible to the heads of KV head h only
+/*
+ * The same with other scores, and other keys that a token sees.  In this order:
+ *
+ *   S1 = softcap tanh(S / softcap)       with softcap > 0
+ *   S2 = S1 - slopes[h] |pos(t) - j|     with slopes
+ *
+ * take the place of S, and with `visible` token t sees only j with
+ * visible[t, 0] <= j < visible[t, 1] among those that sparse_mode lets it see:
+ * with mode 3 the documents of a packed sequence (a document's first key, and any
+ * end past the token), with mode 0 images or prefixes whose tokens see each other
+ * both ways (0, and the larger of pos(t) + 1 and the end of the token's image or
+ * of the prefix).  Blocks that no token of a tile sees are not read.
+ *
+ * softcap      0 (none) or positive, finite; MSA_ERR_ATTR otherwise, and where
+ *              softmax_scale / softcap has no float32.  A capped score is off by a
+ *              few units in the last place of the cap at most, and by as many of
+ *              its own where the scores beside it are below 0.6 softcap too.
+ * slopes       device float32 [Hq], compact, finite; or NULL.  (Bias and scores are
+ *              added in float32: far keys of a steep head lose digits that their
+ *              weights do not have.)
+ * visible      device int32 [T, 2], compact, 8-byte aligned; or NULL.  Any values: a
+ *              token with visible[t, 1] <= visible[t, 0] sees nothing.  Rows of
+ *              tokens behind the last request are not read.
+ *
+ * With none of the three it is msa_attention, bit for bit.  The workspace is
+ * msa_attention's.  lse is the log of the sum of exp(S2).
+ */
+msa_status_t msa_attention_ex(const msa_tensor_t* query, const msa_tensor_t* key,
+                              const msa_tensor_t* value, const int32_t* block_table,
+                              int64_t max_blocks, const int32_t* cu_seqlens_q,
+                              const int32_t* kv_len, int32_t batch, int32_t block_size,
+                              int32_t layout, int32_t sparse_mode, float softmax_scale,
+                              float softcap, const float* slopes, const int32_t* visible,
+                              void* out, float* lse, void* workspace, int64_t workspace_bytes,
+                              void* stream);
+
+/* msa_attention over selected blocks: j is visible to the heads of KV head h only
  * if also floor(j / 128) is among blocks[t, h, 0:num_blocks] (device int32
  * [T, Hkv, num_blocks], compact, num_blocks 1..64: msa_block_topk's output for
  * one index head per KV head).  Entries may stand in any order; one outside the

@@ -298,3 +298,101 @@ def step_tables(new_tokens, ctx_len, rows, pool, free_pages, free_count: int, ma
     out["positions"] += [0] * pad
     out["slots"] += [-1] * pad
     return out | {"pool": pool, "free": [len(stack), missing]}
+
+
+# ---------------------------------------------------------------------------
+# attention with other forms of the scores
+# ---------------------------------------------------------------------------
+
+
+class Forms(NamedTuple):
+    """Capped, biased, narrowed attention of every token, in binary64, with what
+    its bounds take (all [T, Hq] but the first, the third and the fourth)."""
+    out: torch.Tensor      # [T, Hq, D]
+    lse: torch.Tensor
+    spread: torch.Tensor   # [T, Hq, D]: sum of |weight * value|
+    drift: torch.Tensor    # [T, Hq, D]: sum of |weight's error * value|
+    loss: torch.Tensor     # sum of the weights' errors
+    keys: torch.Tensor     # visible keys
+    top: torch.Tensor      # largest |value| of a visible key
+
+
+def attention_forms(query, key, value, block_table, cu_seqlens_q, kv_len, layout, sparse_mode,
+                    scale: Optional[float] = None, softcap: float = 0.0, slopes=None,
+                    visible=None) -> Forms:
+    """``msa_attention_ex`` from its definition, a request and a head at a time.
+
+    A weight's error, with e = 2^-24: the product of 128 terms is off by at most
+    130 e of its size (the sum of its terms' magnitudes and, as the sums may begin
+    with it, the bias), the cap by 12 e of softcap (exponential, sum, reciprocal,
+    product: 10 e; the polynomial 0.5 e and its own 6 roundings of at most 0.54
+    softcap), the bias by 2 e, and the exponent by 4 e (1 + |S2| + max |S2|); the
+    weight exp(S2) then changes by the factor exp(+-d)."""
+    T, Hq, _ = query.shape
+    scale = 1.0 / math.sqrt(D) if scale is None else scale
+    e = 2.0 ** -24
+    f = Forms(*(torch.zeros(T, Hq, *([D] if i in (0, 2, 3) else []), dtype=torch.float64)
+                for i in range(7)))
+    f.lse.fill_(-math.inf)
+    first = 0
+    cu = [int(x) for x in cu_seqlens_q]
+    for b in range(len(kv_len)):
+        length = max(int(kv_len[b]), 0)
+        keys, there = request_rows(key, layout, block_table, b, length, first)
+        vals, _ = request_rows(value, layout, block_table, b, length, first)
+        first += length
+        lo, hi = max(cu[b], 0), min(cu[b + 1], T)
+        if hi <= lo or not len(keys):
+            continue
+        pos = (int(kv_len[b]) - (cu[b + 1] - cu[b]) + torch.arange(lo, hi) - cu[b])[:, None]
+        j = torch.arange(keys.shape[0])[None]
+        seen = there[None].expand(hi - lo, -1)
+        if sparse_mode == 3:
+            seen = seen & (j <= pos)
+        if visible is not None:
+            span = visible[lo:hi].long()
+            seen = seen & (j >= span[:, :1]) & (j < span[:, 1:])
+        away = (pos - j).abs().double()
+        g = Hq // keys.shape[1]
+        some = seen.any(1)
+        for h in range(Hq):
+            k, v, q = keys[:, h // g].double(), vals[:, h // g].double(), query[lo:hi, h].double()
+            s = scale * (q @ k.T)
+            d = 130 * e * scale * (q.abs() @ k.abs().T)
+            if softcap:
+                s, d = softcap * torch.tanh(s / softcap), d + 12 * e * softcap
+            if slopes is not None:
+                bias = float(slopes[h]) * away
+                s, d = s - bias, d + (0 if softcap else 130 * e) * bias.abs() + 2 * e * bias.abs()
+            s = torch.where(seen, s, -math.inf)
+            m = torch.where(some, s.amax(1), 0.0)[:, None]
+            d = d + 4 * e * (1 + torch.where(seen, s, 0.0).abs() + m.abs())
+            w = torch.where(seen, torch.exp(s - m), 0.0)
+            w = w / torch.where(some, w.sum(1), 1.0)[:, None]
+            off = torch.where(seen, w * torch.expm1(d), 0.0)
+            v = torch.where(seen.any(0)[:, None], v, 0.0)
+            f.out[lo:hi, h] = w @ v
+            f.spread[lo:hi, h] = w @ v.abs()
+            f.drift[lo:hi, h] = off @ v.abs()
+            f.loss[lo:hi, h] = off.sum(1)
+            f.lse[lo:hi, h] = torch.logsumexp(s, 1)
+            f.keys[lo:hi, h] = seen.sum(1).double()
+            big = v.abs().amax(1)
+            f.top[lo:hi, h] = torch.where(seen, big[None], 0.0).amax(1)
+    return f
+
+
+def forms_bounds(f: Forms, dtype: torch.dtype):
+    """(largest |out error| [T, Hq, D], largest |lse error| [T, Hq]), as
+    ``attention_bounds``: the weights' errors, n e for each of the two sums of n
+    terms and as much for their rescalings, half a step for a weight and for the
+    result, and float16's smallest step."""
+    e = 2.0 ** -24
+    u = torch.finfo(dtype).eps / 2
+    share = 2 * f.keys * e + 4 * e
+    out = (1.01 * (f.drift + f.spread * f.loss[..., None])
+           + f.spread * (share + u * (1.01 + f.loss))[..., None] + u * f.out.abs() * 1.01)
+    if dtype == torch.float16:
+        out = out + (f.keys * 2.0 ** -36 * f.top)[..., None] + 2.0 ** -25
+    lse = 1.01 * f.loss + f.keys * e + 4 * e * (1 + f.lse.abs().nan_to_num(0, 0, 0))
+    return out, lse
