@@ -163,13 +163,13 @@ int set_forms(const Forms& f, float scale, AttnParams& p) {
   if (f.slopes) form |= msa::kBias;
   if (f.softcap > 0.f) {
     form |= msa::kCap;
-    // tanh(x) = x (1 + c1 x^2 + .. + c4 x^8) for |x| <= 0.6, off by 2.8e-8 at most
-    constexpr double kTanh[5] = {1.0, -0.33332248, 0.133080983, -0.0519943375, 0.0153192069};
+    // tanh(x) = x (1 + c1 x^2 + .. + c4 x^8) for |x| <= 0.75, off by 2.7e-7 at most
+    constexpr double kTanh[5] = {1.0, -0.333280453, 0.132533633, -0.0498660864, 0.0127505841};
     const double a = (double)scale / f.softcap;
     double unit = (double)scale * msa::kLog2e;
     p.cap_top = f.softcap * msa::kLog2e;
     p.cap_twice = (float)(2.0 * msa::kLog2e * a);
-    p.cap_near = (float)(0.6 / a);
+    p.cap_near = (float)(0.75 / a);
     for (int i = 0; i < 5; ++i, unit *= a * a) {
       p.cap_poly[i] = (float)(kTanh[i] * unit);
       // (a cap so small that a coefficient has no float32: never near)

@@ -286,11 +286,11 @@ __device__ __forceinline__ TileSpan tile_span(const AttnParams& p, const AttnTil
 }
 
 // Capped scores in units of log2: cap_top * tanh(a s) of the products s, with a =
-// softmax_scale / softcap.  Where all of a wave's |a s| are at most 0.6, an odd
-// polynomial of degree 9 (off by 3e-8 of the cap at most, fitted to tanh for the
-// smallest largest error; a multiplication and 4 fused ones, 10 cycles of a SIMD
-// against 22), elsewhere 1 - 2 / (exp(2 a s) + 1), whose error is a few roundings
-// of the cap itself (infinities give the cap).
+// softmax_scale / softcap.  Where all of a wave's |a s| are at most 0.75, an odd
+// polynomial of degree 9 (off by 2.7e-7 of the cap at most, 4.4 of float32's half
+// steps, fitted to tanh for the smallest largest error), elsewhere 1 - 2 /
+// (exp(2 a s) + 1), whose error is a few roundings of the cap itself (infinities
+// give the cap).
 __device__ __forceinline__ float cap_slope(const AttnParams& p, float s) {   // capped / s
   const float u = s * s;
   float r = __builtin_fmaf(u, p.cap_poly[4], p.cap_poly[3]);

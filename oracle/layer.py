@@ -325,7 +325,7 @@ def attention_forms(query, key, value, block_table, cu_seqlens_q, kv_len, layout
     A weight's error, with e = 2^-24: the product of 128 terms is off by at most
     130 e of its size (the sum of its terms' magnitudes and, as the sums may begin
     with it, the bias), the cap by 12 e of softcap (exponential, sum, reciprocal,
-    product: 10 e; the polynomial 0.5 e and its own 6 roundings of at most 0.54
+    product: 10 e; the polynomial 4.5 e and its own 6 roundings of at most 0.75
     softcap), the bias by 2 e, and the exponent by 4 e (1 + |S2| + max |S2|); the
     weight exp(S2) then changes by the factor exp(+-d)."""
     T, Hq, _ = query.shape
