@@ -77,7 +77,8 @@ struct Plan {
 // while one request far longer than the rest then holds the launch up (one of
 // 131072 keys beside 127, 255 or 1023 of 512: 1380, 1430 and 1790 us, in parts
 // 167, 246 and 890).
-Plan plan_for(int64_t T, int64_t B, int64_t Hq, int64_t Hkv, int64_t MB, int64_t nsel) {
+Plan plan_for(int64_t T, int64_t B, int64_t Hq, int64_t Hkv, int64_t MB, int64_t nsel,
+              int most_rows = 256, int64_t most_split = kMaxSplit) {
   Plan p{};
   const int64_t g = Hq / Hkv;
   const bool few = nsel > 0 ? T < 8 * B || T * Hkv < 640 : T * std::min<int64_t>(g, 16) <= 16 * B;
@@ -85,7 +86,8 @@ Plan plan_for(int64_t T, int64_t B, int64_t Hq, int64_t Hkv, int64_t MB, int64_t
   if (!few && nsel == 0) {
     const int64_t rows = T * std::min<int64_t>(g, 256);
     const int64_t big = (rows + 255) / 256 * Hkv;
-    if (rows >= 192 * B && big >= 128 && big * std::max<int64_t>(MB / 8, 1) >= 256) p.rows = 256;
+    if (rows >= 192 * B && big >= 128 && big * std::max<int64_t>(MB / 8, 1) >= 256)
+      p.rows = most_rows;
   }
   p.hpt = (int)std::min<int64_t>(g, p.rows);
   p.tpt = few && nsel > 0 ? 1 : p.rows / p.hpt;
@@ -105,7 +107,7 @@ Plan plan_for(int64_t T, int64_t B, int64_t Hq, int64_t Hkv, int64_t MB, int64_t
     p.balanced = true;
   }
   n = std::min(n, (blocks + p.min_blocks - 1) / p.min_blocks);
-  p.nsplit = (int)std::max<int64_t>(1, std::min(n, kMaxSplit));
+  p.nsplit = (int)std::max<int64_t>(1, std::min(n, most_split));
   p.units = p.ntiles * Hkv * p.hchunks * p.nsplit;
   if (p.balanced && p.nsplit > 1) p.units = (p.target + 1 + p.ntiles) * Hkv * p.hchunks;
   return p;
@@ -243,7 +245,17 @@ msa_status_t run(const msa_tensor_t* query, const msa_tensor_t* key, const msa_t
   if (T == 0) return MSA_OK;
   if (!query->data || (kv.pages > 0 && (!key->data || !value->data))) return MSA_ERR_NULL;
 
-  const Plan plan = plan_for(T, batch, Hq, Hkv, max_blocks, selected ? num_blocks : 0);
+  Plan plan = plan_for(T, batch, Hq, Hkv, max_blocks, selected ? num_blocks : 0);
+  // The other forms take 128 rows in place of 256 below 128 blocks, and where a
+  // causal range narrows the keys, as documents do (32 heads on 4, us with 128 and
+  // 256 rows: 2048 tokens over 4096 keys biased 127 and 138, over 16384 553 and 540,
+  // over 32768 capped 1363 and 1294; 16 requests of 300 over 2000 keys capped 222 and
+  // 256; one prompt of 4096 biased 170 and 159; 4 requests of 1000 in documents of
+  // 1024 tokens 72 and 86), in as many parts as the workspace, which does not know
+  // the form, has room for.
+  if (plan.rows == 256 && (forms.softcap > 0.f || forms.slopes || forms.visible) &&
+      (max_blocks < 128 || (forms.visible && sparse_mode == 3)))
+    plan = plan_for(T, batch, Hq, Hkv, max_blocks, 0, 128, plan.nsplit);
   const int64_t need = workspace_for(plan, T, Hq);
   if (need > 0 && (!workspace || workspace_bytes < need)) return MSA_ERR_WORKSPACE;
   int64_t grid = plan.units;

@@ -497,8 +497,9 @@ int64_t msa_attention_workspace(int64_t T, int32_t batch, int32_t Hq, int32_t Hk
 
 /* Rows -- (query token, head) pairs of one KV head -- of the tiles that
  * msa_attention (num_blocks = 0) or msa_block_attention would use for a call of
- * these sizes: 16, 128 or 256; 0 for sizes that no call takes.  All tiles compute
- * the same definition.  Host-only; for benchmarks and tests. */
+ * these sizes: 16, 128 or 256; 0 for sizes that no call takes.  (msa_attention_ex
+ * may take 128 where this says 256.)  All tiles compute the same definition.
+ * Host-only; for benchmarks and tests. */
 int32_t msa_attention_tile_rows(int64_t T, int32_t batch, int32_t Hq, int32_t Hkv,
                                 int64_t max_blocks, int32_t num_blocks);
 

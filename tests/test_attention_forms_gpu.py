@@ -148,10 +148,11 @@ def test_many_rows(form, dtype, dev):
 def test_256_row_tiles(dev):
     import block_max_qk_amd as m
     for form in FORMS:
-        c = make([700, 900], [700, 2100], 32, 16, "BBND", BF, seed=8, **form)
-        assert m.msa_attention_tile_rows(1600, 2, 32, 16, c["table"].shape[1]) == 256
-        log("256", form)
-        run(c, dev)
+        for width in (17, 130):          # (256 rows only in tables of 128 blocks and more)
+            c = make([700, 900], [700, 2100], 32, 16, "BBND", BF, seed=8, width=width, **form)
+            assert m.msa_attention_tile_rows(1600, 2, 32, 16, width) == 256
+            log("256", form, width)
+            run(c, dev)
 
 
 @pytest.mark.parametrize("form", FORMS)
