@@ -878,6 +878,10 @@ def new_step_tables(batch: int, T: int, max_blocks: int, device=None) -> StepTab
                       torch.empty(T, dtype=torch.int64, device=device), ints(batch + 1))
 
 
+_TABLE_ARGS = ("new_tokens", "ctx_len", "rows", "pool", "free_pages", "free_count", "free_out",
+               "cu_seqlens_q", "kv_len", "start_loc", "block_table", "positions", "cu_pages")
+
+
 def msa_step_tables(new_tokens: torch.Tensor, ctx_len: torch.Tensor, pool: torch.Tensor,
                     free_pages: torch.Tensor, free_count: torch.Tensor, out: StepTables,
                     rows: Optional[torch.Tensor] = None, free_out: Optional[torch.Tensor] = None,
@@ -893,44 +897,41 @@ def msa_step_tables(new_tokens: torch.Tensor, ctx_len: torch.Tensor, pool: torch
     index = new_tokens.get_device()
     if free_out is None:
         free_out = free_count
-    i32 = torch.int32
-    B = new_tokens.numel()
-    T = out.positions.numel()
-    if pool.dim() != 2 or out.block_table.dim() != 2:
-        raise ValueError(f"pool must be [rows, blocks] and block_table [{B}, max_blocks], got "
-                         f"{tuple(pool.shape)} and {tuple(out.block_table.shape)}")
-    max_blocks = out.block_table.shape[1]
-    if free_pages.dim() != 1:
-        raise ValueError(f"free_pages must be 1-D, got {tuple(free_pages.shape)}")
-    for name, t, shape in (("new_tokens", new_tokens, (B,)), ("ctx_len", ctx_len, (B,)),
-                           ("rows", rows, (B,)), ("pool", pool, None),
-                           ("free_pages", free_pages, None), ("free_count", free_count, (2,)),
-                           ("free_out", free_out, (2,)),
-                           ("cu_seqlens_q", out.cu_seqlens_q, (B + 1,)),
-                           ("kv_len", out.kv_len, (B,)), ("start_loc", out.start_loc, (B,)),
-                           ("block_table", out.block_table, (B, max_blocks)),
-                           ("positions", out.positions, (T,)), ("slots", out.slots, (T,)),
-                           ("cu_pages", out.cu_pages, (B + 1,))):
-        if t is None:
-            continue
-        want = torch.int64 if name == "slots" else i32
-        if t.dtype != want or not t.is_contiguous() or (shape is not None and t.shape != shape):
-            raise ValueError(f"{name} must be a contiguous {want} tensor"
-                             f"{'' if shape is None else f' {list(shape)}'}, got {t.dtype} "
-                             f"{tuple(t.shape)}")
-        if t.get_device() != index:
-            raise ValueError(f"{name} is on {t.device}, new_tokens on {new_tokens.device}")
+    cu, kv, start, table, positions, slots, pages = out
+    B, T = new_tokens.numel(), positions.numel()
+    if pool.dim() != 2 or table.dim() != 2 or free_pages.dim() != 1:
+        raise ValueError(f"pool must be [rows, blocks], block_table [{B}, max_blocks] and "
+                         f"free_pages 1-D, got {tuple(pool.shape)}, {tuple(table.shape)} and "
+                         f"{tuple(free_pages.shape)}")
+    max_blocks = table.shape[1]
+    # (a step of few requests is bound by the host: elements are counted, which a
+    # compact tensor's shape adds nothing to)
+    i32, n, free = torch.int32, B + 1, free_pages.numel()
+    pool_rows, pool_blocks = pool.shape
+    for i, (t, size) in enumerate(((new_tokens, B), (ctx_len, B), (rows, B),
+                                   (pool, pool_rows * pool_blocks), (free_pages, free),
+                                   (free_count, 2), (free_out, 2), (cu, n), (kv, B), (start, B),
+                                   (table, B * max_blocks), (positions, T), (pages, n))):
+        if t is not None and (t.dtype is not i32 or t.numel() != size or
+                              not t.is_contiguous() or t.get_device() != index):
+            raise ValueError(f"{_TABLE_ARGS[i]} must be a contiguous int32 tensor of {size} "
+                             f"elements on {new_tokens.device}, got {t.dtype} {tuple(t.shape)} "
+                             f"on {t.device}")
+    if (slots.dtype is not torch.int64 or slots.numel() != T or not slots.is_contiguous() or
+            slots.get_device() != index):
+        raise ValueError(f"slots must be a contiguous int64 tensor of {T} elements on "
+                         f"{new_tokens.device}, got {slots.dtype} {tuple(slots.shape)} on "
+                         f"{slots.device}")
     if index < 0:
         raise ValueError(f"the tensors must be on a GPU, new_tokens is on {new_tokens.device}")
     handle = _raw_stream(stream, index)
     with _guard(index):
         st = lib.msa_step_tables(
             new_tokens.data_ptr(), ctx_len.data_ptr(), _address(rows), B, pool.data_ptr(),
-            pool.shape[0], pool.shape[1], free_pages.data_ptr(), free_pages.numel(),
-            free_count.data_ptr(), free_out.data_ptr(), max_blocks, T, int(block_size),
-            out.cu_seqlens_q.data_ptr(), out.kv_len.data_ptr(), out.start_loc.data_ptr(),
-            out.block_table.data_ptr(), out.positions.data_ptr(), out.slots.data_ptr(),
-            out.cu_pages.data_ptr(), handle)
+            pool_rows, pool_blocks, free_pages.data_ptr(), free, free_count.data_ptr(),
+            free_out.data_ptr(), max_blocks, T, int(block_size), cu.data_ptr(), kv.data_ptr(),
+            start.data_ptr(), table.data_ptr(), positions.data_ptr(), slots.data_ptr(),
+            pages.data_ptr(), handle)
     if st:
         _raise_status(st)
     return out
