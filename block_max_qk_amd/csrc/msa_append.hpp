@@ -129,18 +129,19 @@ __global__ __launch_bounds__(64 * kAppendWaves) void append_kernel(AppendParams 
   int step = (int)(wid - t * p.groups) * p.per_wave;
   const int step_end = min(step + p.per_wave, p.steps);
 
+  // (a token's angle rows by axis, read beside the search for its request)
+  int turn[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) turn[k] = k < p.axes ? p.axis_pos[k * p.T + t] : 0;
   const int b = __builtin_amdgcn_readfirstlane(request_of(p.cu_q, p.B, t));
   if (b < 0) return;
   const int q0 = p.cu_q[b];
   const int lq = p.cu_q[b + 1] - q0;
   const int64_t pos = (int64_t)p.kv_len[b] - lq + (t - q0);
   if (pos < 0 || (p.half > 0 && p.axes == 0 && pos >= p.positions)) return;
-  int64_t turn[4];                                 // a token's angle rows, by axis
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    turn[k] = k < p.axes ? p.axis_pos[k * p.T + t] : 0;
+  for (int k = 0; k < 4; ++k)
     if (k < p.axes && (turn[k] < 0 || turn[k] >= p.positions)) return;
-  }
   const int l = lane_id();
   const int i = l & 15, rr = l >> 4;
 
@@ -168,8 +169,8 @@ __global__ __launch_bounds__(64 * kAppendWaves) void append_kernel(AppendParams 
 #pragma unroll
     for (int x = 0; x < 4; ++x) {
       if (x >= p.axes) break;
-      const float* cr = p.cos + turn[x] * p.half + at;
-      const float* sr = p.sin + turn[x] * p.half + at;
+      const float* cr = p.cos + (int64_t)turn[x] * p.half + at;
+      const float* sr = p.sin + (int64_t)turn[x] * p.half + at;
 #pragma unroll
       for (int k = 0; k < 8; k += 4) {
         if (p.interleaved && k > 0) break;
