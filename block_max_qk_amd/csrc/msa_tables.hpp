@@ -76,10 +76,18 @@ __global__ __launch_bounds__(64 * kTableWaves) void tables_kernel(TablesParams p
   // tokens and pages of the requests before, and this group's own
   __shared__ int64_t sums[kTableWaves][2];
   int64_t tokens = 0, pages = 0;
-  for (int64_t b = tid; b < b0; b += 64 * kTableWaves) {
-    const TablesRequest r = tables_request(p, (int)b);
-    tokens += r.fresh;
-    pages += r.need;
+  // (four requests a lane at a time, whose reads are in flight together)
+  for (int64_t b = tid; b < b0; b += 4 * 64 * kTableWaves) {
+    TablesRequest r[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      r[u] = tables_request(p, (int)min(b + u * 64 * kTableWaves, (int64_t)b0 - 1));
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const bool is = b + u * 64 * kTableWaves < b0;
+      tokens += is ? r[u].fresh : 0;
+      pages += is ? r[u].need : 0;
+    }
   }
   tokens = lane_at(wave_incl_scan(tokens), 63);
   pages = lane_at(wave_incl_scan(pages), 63);
@@ -138,11 +146,13 @@ __global__ __launch_bounds__(64 * kTableWaves) void tables_kernel(TablesParams p
       const int64_t nth = pf + (k - held);
       return nth < count ? p.free_pages[count - 1 - nth] : -1;
     };
-    for (int64_t k = at; k < p.MB; k += step) {
-      const int page = k < now ? page_of((int)k) : -1;
+    int64_t k = at;
+    for (; k < now; k += step) {
+      const int page = page_of((int)k);
       p.block_table[(int64_t)(b0 + i) * p.MB + k] = page;
-      if (row >= 0 && k >= held && k < now) pr[k] = page;
+      if (row >= 0 && k >= held) pr[k] = page;
     }
+    for (; k < p.MB; k += step) p.block_table[(int64_t)(b0 + i) * p.MB + k] = -1;
     const int64_t te = min(tf + lane_at(mine.fresh, i), p.T);
     for (int64_t t = tf + at; t < te; t += step) {
       const int64_t pos = ctx + (t - tf);
