@@ -35,7 +35,8 @@ extern "C" msa_status_t msa_step_tables(
     int32_t block_size, int32_t* cu_seqlens_q, int32_t* kv_len, int32_t* start_loc,
     int32_t* block_table, int32_t* positions, int64_t* slots, int32_t* cu_pages, void* stream) {
   if (!cu_seqlens_q || !cu_pages || !free_count || !free_out) return MSA_ERR_NULL;
-  if (batch < 0 || batch > (1 << 30) || T < 0 || T > INT32_MAX || block_size != msa::kP)
+  // (a launch holds less than 2^32 threads)
+  if (batch < 0 || batch > (1 << 29) || T < 0 || T > INT32_MAX || block_size != msa::kP)
     return MSA_ERR_SHAPE;
   if (max_blocks < 1 || max_blocks > (1 << 24) || pool_blocks < max_blocks ||
       pool_blocks > INT32_MAX || pool_rows < 0 || pool_rows > INT32_MAX || free_size < 0 ||
