@@ -5,6 +5,7 @@
 #include "msa_index_score.h"
 
 #include <algorithm>
+#include <cfloat>
 #include <cmath>
 #include <cstdint>
 
@@ -174,8 +175,12 @@ int set_forms(const Forms& f, float scale, AttnParams& p) {
     p.cap_near = (float)(0.75 / a);
     for (int i = 0; i < 5; ++i, unit *= a * a) {
       p.cap_poly[i] = (float)(kTanh[i] * unit);
-      // (a cap so small that a coefficient has no float32: never near)
+      // (a cap so small that a coefficient has no float32: never near; one so large
+      // that a coefficient is lost: near where it does not count, as far as a
+      // product's square has a float32)
       if (!std::isfinite(p.cap_poly[i])) p.cap_near = -1.f;
+      if (p.cap_poly[i] > -FLT_MIN && p.cap_poly[i] < FLT_MIN)
+        p.cap_near = std::min(p.cap_near, (float)std::min(1e-4 / a, 1e19));
     }
   }
   if (f.visible || form) form |= msa::kRange;

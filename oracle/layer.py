@@ -327,7 +327,10 @@ def attention_forms(query, key, value, block_table, cu_seqlens_q, kv_len, layout
     with it, the bias), the cap by 12 e of softcap (exponential, sum, reciprocal,
     product: 10 e; the polynomial 4.5 e and its own 6 roundings of at most 0.75
     softcap), the bias by 2 e, and the exponent by 4 e (1 + |S2| + max |S2|); the
-    weight exp(S2) then changes by the factor exp(+-d)."""
+    weight exp(S2) then changes by the factor exp(+-d).  Where the errors add up to
+    more than all weights (scores of 10^7 and more), the result is still a mean of
+    visible values, off by twice the largest of them at most, and the log of the sum
+    by the largest d."""
     T, Hq, _ = query.shape
     scale = 1.0 / math.sqrt(D) if scale is None else scale
     e = 2.0 ** -24
@@ -373,12 +376,14 @@ def attention_forms(query, key, value, block_table, cu_seqlens_q, kv_len, layout
             v = torch.where(seen.any(0)[:, None], v, 0.0)
             f.out[lo:hi, h] = w @ v
             f.spread[lo:hi, h] = w @ v.abs()
-            f.drift[lo:hi, h] = off @ v.abs()
-            f.loss[lo:hi, h] = off.sum(1)
+            big = torch.where(seen, v.abs().amax(1)[None], 0.0).amax(1)
+            loss = off.sum(1)
+            wild = ~(loss <= 1)          # (0 * inf among them)
+            f.drift[lo:hi, h] = torch.where(wild[:, None], 2 * big[:, None], off @ v.abs())
+            f.loss[lo:hi, h] = torch.where(wild, torch.where(seen, d, 0.0).amax(1), loss)
             f.lse[lo:hi, h] = torch.logsumexp(s, 1)
             f.keys[lo:hi, h] = seen.sum(1).double()
-            big = v.abs().amax(1)
-            f.top[lo:hi, h] = torch.where(seen, big[None], 0.0).amax(1)
+            f.top[lo:hi, h] = big
     return f
 
 

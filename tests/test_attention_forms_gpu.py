@@ -235,6 +235,18 @@ def test_caps(dev):
     check(d, out, lse)
 
 
+def test_large_caps(dev):
+    """Scores that come near caps of any size."""
+    for cap in (1e5, 1e7, 1e12, 1e20, 1e30):
+        for part in (0.02, 0.2, 0.7):
+            for q_lens, kv_lens in (([1, 2], [200, 130]), ([60], [200])):
+                c = make(q_lens, kv_lens, 8, 2, gain=1.0)
+                top = reference({**c, "cap": 0.0}).lse.max()
+                c["q"] = (c["q"].float() * float(part * cap / top)).to(BF)
+                c["cap"] = cap
+                run(c, dev)
+
+
 def test_slopes(dev):
     """Zero, negative and steep ones; positions before 0 (more new tokens than
     keys) without a causal mask."""
@@ -348,3 +360,53 @@ def test_refusals(dev):
         d = {n: (x.to(dev) if torch.is_tensor(x) else x) for n, x in c.items()}
         m.attention(d["q"], d["k"], d["v"], d["table"], d["cu"], d["kv"], "BBND",
                     slopes=c["slopes"])
+
+
+@pytest.mark.parametrize("form", [dict(cap=20.0), dict(bias=True), dict(cap=9.0, bias=True), {}])
+def test_ranges_far_into_long_contexts(form, dev):
+    """Windows that begin and end past the first 64 blocks, and such that span more
+    than 64; each tile's walk and the parts of one."""
+    for q_lens, kv_lens in (([1, 1], [20011, 9000]), ([40], [20011]), ([130, 3], [12000, 20011])):
+        c = make(q_lens, kv_lens, 4, 1, seed=3, **form)
+        pos = pos_of(c)
+        for first, end in ((pos - 700, pos - 100), (pos * 0 + 8300, pos * 0 + 8400),
+                           (pos * 0 + 130, pos + 1), (pos - 1, pos + 1)):
+            c["visible"] = torch.stack([first, end], 1).int()
+            log("far", form, q_lens, int(first[0]))
+            run(c, dev)
+
+
+@pytest.mark.parametrize("B", [70, 300])
+def test_many_requests(B, dev):
+    """Past the 64 requests that one look at the batch holds."""
+    gen = torch.Generator().manual_seed(B)
+    q = torch.randint(0, 4, (B,), generator=gen).tolist()
+    kv = [n + int(x) for n, x in zip(q, torch.randint(0, 500, (B,), generator=gen))]
+    kv[7] += 3000
+    for form in (dict(cap=20.0, mask="any"), dict(bias=True, mask="documents"), dict(cap=9.0)):
+        run(make(q, kv, 8, 2, "BNBD", FP, seed=B, **form), dev)
+    q[5] = 200
+    kv[5] += 200
+    run(make([3 * n for n in q], [n + 600 for n in kv], 8, 2, seed=B, bias=True, mask="any"), dev)
+    run(make(q, kv, 8, 2, "TND", BF, seed=B, cap=9.0, mask="any"), dev)
+
+
+def test_two_streams_at_once(dev):
+    """Calls of two forms on one cache, from two streams."""
+    import block_max_qk_amd as m
+    a = make([60, 1], [3000, 400], 8, 2, cap=20.0, mask="documents")
+    b = {**a, "cap": 0.0, "slopes": torch.linspace(0, 0.5, 8), "visible": spans(a, "any", 4)}
+    want = [call(x, dev) for x in (a, b)]
+    d = {n: (x.to(dev) if torch.is_tensor(x) else x) for n, x in a.items()}
+    kws = [dict(softcap=20.0, visible=a["visible"].to(dev)),
+           dict(slopes=b["slopes"].to(dev), visible=b["visible"].to(dev))]
+    streams = [torch.cuda.Stream(dev) for _ in kws]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream(dev))
+    got = []
+    for _ in range(8):
+        got = [m.attention(d["q"], d["k"], d["v"], d["table"], d["cu"], d["kv"], "BBND",
+                           return_lse=True, stream=s, **kw) for s, kw in zip(streams, kws)]
+    torch.cuda.synchronize()
+    for (o, lse), (wo, wl) in zip(got, want):
+        assert torch.equal(o.cpu(), wo) and torch.equal(lse.cpu(), wl)
