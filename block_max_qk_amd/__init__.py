@@ -3,8 +3,10 @@
 The operator lives in the HIP library ``libmsa_index_score.so`` (C ABI in
 ``include/msa_index_score.h``), with the top-k block selection over its
 output (``msa_block_topk``), the cache append in front of it
-(``msa_cache_append``) and the attention behind it (``msa_attention``,
-``msa_block_attention``); this package holds its sources (``csrc/``), the
+(``msa_cache_append``, by several position axes ``msa_cache_append_axes``), the
+attention behind it (``msa_attention``, ``msa_block_attention``, with capped,
+biased or narrowed scores ``msa_attention_ex``) and the tables of a serving step
+(``msa_step_tables``); this package holds its sources (``csrc/``), the
 hipcc build step (``build.py``) and a ctypes binding with the same names.
 """
 from ._binding import (  # noqa: F401

@@ -8,9 +8,15 @@
 // Bound by latency: a workgroup reads the lengths of every request before its own
 // (8 bytes each, out of the L2), adds them up, and knows from the two sums where
 // its requests' tokens begin and which pages of the free list are theirs; no
-// workgroup waits for another, and one launch does it all.  The lengths of
-// groups of `group` requests are scanned by one wave, so that there are about 512
-// workgroups however many requests there are.
+// workgroup waits for another, and one launch does it all (a scan of its own in
+// front would be a second launch, 5 us, for less than that of reads).  The lengths
+// of groups of `group` requests are scanned by one wave, so that there are about
+// 512 workgroups however many requests there are.
+//
+// 64 decode requests over tables of 256 blocks 4 us, 300 of 1 to 200 tokens 5,
+// 4096 over tables of 1024 blocks (19 MB) 9 to 10, 1.9 TB/s, 13.5 with one request's
+// lengths in flight a lane and one loop for the blocks and the rest of a row.  A
+// call takes 9 to 10 us of host time, so none of these waits for its kernel.
 #pragma once
 
 #include "msa_device.hpp"
