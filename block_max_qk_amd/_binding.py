@@ -11,6 +11,7 @@ import contextlib
 import ctypes
 import functools
 import math
+import operator
 import os
 import struct
 import threading
@@ -561,7 +562,9 @@ def _check_axes(axis_positions, pair_axes, lead, index, rotary) -> bytes:
     if pair_axes is None or len(pair_axes) != rotary // 2:
         raise ValueError(f"pair_axes must hold the axis of each of the {rotary // 2} pairs")
     try:
-        return bytes(pair_axes)
+        # (an array's own bytes would be those of its wider integers)
+        return bytes(pair_axes if isinstance(pair_axes, (bytes, list, tuple)) else
+                     [operator.index(x) for x in pair_axes])
     except (TypeError, ValueError) as e:
         raise ValueError("pair_axes must hold integers from 0 on") from e
 

@@ -160,6 +160,24 @@ def test_captured_and_replayed(dev):
         assert torch.equal(out, eager)
 
 
+def test_kinds_of_integers(dev):
+    """The pairs' axes as bytes, lists, arrays and tensors of any integers."""
+    import numpy as np
+    gen, cu, T, kv, table, pages = batch([4, 1], [4, 1], 75)
+    cos, sin = angles(30, 64)
+    src = torch.randn(T, 2, 128, generator=gen).to(BF)
+    ap = torch.randint(0, 30, (3, T), generator=gen).int()
+    axis = pair_axes(32, 3, "turns")
+    b = [[src, torch.zeros_like(src), "ROWS", None, True]]
+    want = call(b, cos, sin, None, cu, kv, dev, False, ap, axis)[0].dst
+    assert not torch.equal(want.cpu(), call(b, cos, sin, None, cu, kv, dev, False, ap,
+                                            [0] * 32)[0].dst.cpu())
+    for pairs in (bytes(axis), bytearray(axis), tuple(axis), np.array(axis, np.int32),
+                  np.array(axis, np.uint8), torch.tensor(axis)):
+        got = call(b, cos, sin, None, cu, kv, dev, False, ap, pairs)[0].dst
+        assert torch.equal(got, want), type(pairs)
+
+
 def test_refusals(dev):
     import block_max_qk_amd as m
     gen, cu, T, kv, table, pages = batch([4], [4], 74)
