@@ -35,12 +35,13 @@ extern "C" msa_status_t msa_step_tables(
     int32_t block_size, int32_t* cu_seqlens_q, int32_t* kv_len, int32_t* start_loc,
     int32_t* block_table, int32_t* positions, int64_t* slots, int32_t* cu_pages, void* stream) {
   if (!cu_seqlens_q || !cu_pages || !free_count || !free_out) return MSA_ERR_NULL;
-  // (a launch holds less than 2^32 threads)
-  if (batch < 0 || batch > (1 << 29) || T < 0 || T > INT32_MAX || block_size != msa::kP)
+  // (every workgroup adds up the lengths before its requests: 2^20 of them take
+  // milliseconds, and as the square)
+  if (batch < 0 || batch > (1 << 20) || T < 0 || T > INT32_MAX || block_size != msa::kP)
     return MSA_ERR_SHAPE;
   if (max_blocks < 1 || max_blocks > (1 << 24) || pool_blocks < max_blocks ||
       pool_blocks > INT32_MAX || pool_rows < 0 || pool_rows > INT32_MAX || free_size < 0 ||
-      free_size > INT32_MAX)
+      free_size > INT32_MAX || pool_rows * pool_blocks > ((int64_t)1 << 60))
     return MSA_ERR_SHAPE;
   if (batch > 0 && (!new_tokens || !ctx_len || !kv_len || !start_loc || !block_table ||
                     (pool_rows > 0 && !pool)))

@@ -548,8 +548,9 @@ int32_t msa_attention_tile_rows(int64_t T, int32_t batch, int32_t Hq, int32_t Hk
  * All arrays are compact; nothing that is written may overlap anything else
  * (MSA_ERR_STRIDE; but free_out and free_count).  Nothing is allocated or kept; a
  * call may be captured into a graph.  MSA_ERR_SHAPE for sizes out of range (batch
- * > 2^29, T, pool_rows, pool_blocks or free_size > 2^31 - 1), MSA_ERR_NULL for a
- * pointer that the call must use, MSA_ERR_HIP if a launch fails.
+ * > 2^20, T, pool_rows, pool_blocks or free_size > 2^31 - 1, a pool of more than
+ * 2^60 entries), MSA_ERR_NULL for a pointer that the call must use, MSA_ERR_HIP if a
+ * launch fails.
  */
 msa_status_t msa_step_tables(const int32_t* new_tokens, const int32_t* ctx_len,
                              const int32_t* rows, int32_t batch, int32_t* pool, int64_t pool_rows,

@@ -27,8 +27,8 @@ def test_nulls():
 
 
 def test_sizes():
-    for kw in (dict(B=-1), dict(B=(1 << 29) + 1), dict(B=(1 << 30) + 1),
-               dict(T=-1), dict(T=1 << 31), dict(bs=64),
+    for kw in (dict(B=-1), dict(B=(1 << 20) + 1), dict(B=(1 << 30) + 1),
+               dict(R=(1 << 31) - 1, W=(1 << 31) - 1), dict(T=-1), dict(T=1 << 31), dict(bs=64),
                dict(MB=0), dict(MB=9), dict(MB=(1 << 24) + 1, W=1 << 25), dict(R=-1),
                dict(R=1 << 31), dict(W=1 << 31), dict(F=-1), dict(F=1 << 31)):
         assert call(**kw) == SHAPE, kw

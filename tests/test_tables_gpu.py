@@ -141,6 +141,36 @@ def test_groups_of_64(dev):
              rows=None), dev)
 
 
+def test_the_most_requests(dev):
+    """2^20 requests, all but a few of them empty, and large page numbers."""
+    import block_max_qk_amd as m
+    B, T = 1 << 20, 1000
+    gen = torch.Generator().manual_seed(5)
+    at = torch.randperm(B, generator=gen)[:500].sort().values
+    new, ctx = torch.zeros(2, B, dtype=torch.int32)
+    new[at], ctx[at] = 2, 127
+    pool = torch.full((B, 2), 1 << 28, dtype=torch.int32)
+    free = (torch.randperm(600, generator=gen) + (1 << 30)).int()
+    d = [x.to(dev) for x in (new, ctx, pool, free, i32([600, 0]))]
+    out = m.new_step_tables(B, T, 2, dev)
+    m.msa_step_tables(*d, out)
+    torch.cuda.synchronize()
+    cu = torch.zeros(B + 1, dtype=torch.long)
+    cu[1:] = new.long().cumsum(0)
+    pages = free.flip(0)[:500].long()
+    assert torch.equal(out.cu_seqlens_q.cpu().long(), cu)
+    assert torch.equal(out.cu_pages.cpu().long(), cu // 2)
+    assert torch.equal(out.kv_len.cpu(), new + ctx) and not out.start_loc.any()
+    table = torch.full((B, 2), -1, dtype=torch.int32)
+    table[at, 0], table[at, 1] = 1 << 28, pages.int()
+    assert torch.equal(out.block_table.cpu(), table)
+    pool[at, 1] = pages.int()
+    assert torch.equal(d[2].cpu(), pool) and d[4].tolist() == [100, 0]
+    slots = torch.stack([torch.full((500,), (1 << 35) + 127), pages * P], 1).flatten()
+    assert torch.equal(out.slots.cpu(), slots)
+    assert torch.equal(out.positions.cpu().view(500, 2), i32([[127, 128]]).expand(500, 2))
+
+
 def test_long_prompt(dev):
     """One request's blocks and tokens shared by many workgroups."""
     run(case([70001], [130], 700, pad=100), dev)
