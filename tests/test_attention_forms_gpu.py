@@ -391,6 +391,32 @@ def test_many_requests(B, dev):
     run(make(q, kv, 8, 2, "TND", BF, seed=B, cap=9.0, mask="any"), dev)
 
 
+@pytest.mark.parametrize("layout", ["BBND", "BNBD"])
+def test_caches_past_4_gib(layout, dev):
+    """Pages that begin past 2^32 bytes give the bits that the same ones in a small
+    cache do."""
+    import block_max_qk_amd as m
+    NP, far = 40, (1 << 32) // (128 * 2 * 128 * 2) + 1000
+    gen = torch.Generator().manual_seed(9)
+    shape = (128, 2, 128) if layout == "BBND" else (2, 128, 128)
+    small = [torch.randn(NP, *shape, generator=gen).to(BF).to(dev) for _ in range(2)]
+    big = [torch.empty(far + NP, *shape, dtype=BF, device=dev) for _ in range(2)]
+    for x, y in zip(big, small):
+        x[far:] = y
+    for q_lens, kv_lens in (([1, 2], [700, 1500]), ([300], [2000]), ([1500], [2000])):
+        T = sum(q_lens)
+        q = torch.randn(T, 8, 128, generator=gen).to(BF).to(dev)
+        cu = torch.tensor([0, *q_lens]).cumsum(0).int().to(dev)
+        kv = torch.tensor(kv_lens).int().to(dev)
+        table = torch.randperm(NP, generator=gen)[:len(q_lens) * 16].int().view(-1, 16).to(dev)
+        first = torch.randint(0, 600, (T,), generator=gen)
+        kw = dict(softcap=20.0, visible=torch.stack([first, first + 900], 1).int().to(dev))
+        for form in (kw, {**kw, "softcap": None}, dict(slopes=torch.full((8,), 0.01, device=dev))):
+            a = m.attention(q, *small, table, cu, kv, layout, return_lse=True, **form)
+            b = m.attention(q, *big, table + far, cu, kv, layout, return_lse=True, **form)
+            assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
 def test_two_streams_at_once(dev):
     """Calls of two forms on one cache, from two streams."""
     import block_max_qk_amd as m
