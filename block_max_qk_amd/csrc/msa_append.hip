@@ -166,9 +166,12 @@ msa_status_t append(const msa_append_item_t* items, int32_t num_items, const flo
   if (grid * 64 * msa::kAppendWaves > (int64_t)UINT32_MAX) return MSA_ERR_SHAPE;
   hipStream_t s = static_cast<hipStream_t>(stream);
   const dim3 gr((unsigned)grid), bl(64 * msa::kAppendWaves);
-  const hipError_t e = dt == MSA_DTYPE_BF16
-                           ? msa::launch_kernel(msa::append_kernel<true>, gr, bl, s, p)
-                           : msa::launch_kernel(msa::append_kernel<false>, gr, bl, s, p);
+  const bool bf = dt == MSA_DTYPE_BF16;
+  const hipError_t e =
+      p.axes > 0 ? bf ? msa::launch_kernel(msa::append_kernel<true, true>, gr, bl, s, p)
+                      : msa::launch_kernel(msa::append_kernel<false, true>, gr, bl, s, p)
+      : bf ? msa::launch_kernel(msa::append_kernel<true, false>, gr, bl, s, p)
+           : msa::launch_kernel(msa::append_kernel<false, false>, gr, bl, s, p);
   return e == hipSuccess ? MSA_OK : MSA_ERR_HIP;
 }
 

@@ -127,7 +127,9 @@ __device__ __forceinline__ void rotate_pairs(F* x, const float* c, const float* 
   }
 }
 
-template <bool BF>
+// AXES: the angles go by position axes (compiled apart, as the test of it and its
+// registers cost the plain form 1 us of 140).
+template <bool BF, bool AXES>
 __global__ __launch_bounds__(64 * kAppendWaves) void append_kernel(AppendParams p) {
   const int64_t wid = (int64_t)blockIdx.x * kAppendWaves +
                       __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -137,18 +139,22 @@ __global__ __launch_bounds__(64 * kAppendWaves) void append_kernel(AppendParams 
   const int step_end = min(step + p.per_wave, p.steps);
 
   // (a token's angle rows by axis, read beside the search for its request)
-  int turn[4];
+  [[maybe_unused]] int turn[4];
+  if constexpr (AXES) {
 #pragma unroll
-  for (int k = 0; k < 4; ++k) turn[k] = k < p.axes ? p.axis_pos[k * p.T + t] : 0;
+    for (int k = 0; k < 4; ++k) turn[k] = k < p.axes ? p.axis_pos[k * p.T + t] : 0;
+  }
   const int b = __builtin_amdgcn_readfirstlane(request_of(p.cu_q, p.B, t));
   if (b < 0) return;
   const int q0 = p.cu_q[b];
   const int lq = p.cu_q[b + 1] - q0;
   const int64_t pos = (int64_t)p.kv_len[b] - lq + (t - q0);
-  if (pos < 0 || (p.half > 0 && p.axes == 0 && pos >= p.positions)) return;
+  if (pos < 0 || (!AXES && p.half > 0 && pos >= p.positions)) return;
+  if constexpr (AXES) {
 #pragma unroll
-  for (int k = 0; k < 4; ++k)
-    if (k < p.axes && (turn[k] < 0 || turn[k] >= p.positions)) return;
+    for (int k = 0; k < 4; ++k)
+      if (k < p.axes && (turn[k] < 0 || turn[k] >= p.positions)) return;
+  }
   const int l = lane_id();
   const int i = l & 15, rr = l >> 4;
 
@@ -167,7 +173,7 @@ __global__ __launch_bounds__(64 * kAppendWaves) void append_kernel(AppendParams 
   // this lane's angles: of its 8 elements (halves, whose partners lie p.half
   // elements away in another lane) or of its 4 pairs (interleaved)
   float c[8], s[8];
-  if (p.axes > 0) {
+  if constexpr (AXES) {
     // (a row of angles per axis; a lane reads those that its pairs belong to)
     const int at = 8 * i < 2 * p.half ? (p.interleaved ? 4 * i : (8 * i) % p.half) : 0;
     // two bits a pair from bit 2 at on: at is a multiple of 4, so 8 pairs lie in
