@@ -24,6 +24,7 @@ from ._binding import (  # noqa: F401
     index_score,
     load_library,
     msa_attention,
+    msa_attention_ex_workspace,
     msa_attention_tile_rows,
     msa_attention_workspace,
     msa_block_attention,

@@ -41,7 +41,7 @@ EXPORTED = ("msa_index_score", "msa_index_score_family", "msa_index_score_ex",
             "msa_index_score_kernel_family", "msa_block_topk", "msa_cache_append",
             "msa_attention", "msa_block_attention", "msa_attention_workspace",
             "msa_attention_tile_rows", "msa_step_tables", "msa_cache_append_axes",
-            "msa_attention_ex")
+            "msa_attention_ex", "msa_attention_ex_workspace")
 LOCAL_MODE_CODE = {"request": 0, "query": 1}
 
 
@@ -128,6 +128,8 @@ def load_library(path: Optional[str] = None):
         # softcap, slopes, visible after softmax_scale
         lib.msa_attention_ex.argtypes = three + tail[:9] + [ctypes.c_float, ptr, ptr] + tail[9:]
         lib.msa_attention_ex.restype = ctypes.c_int
+        lib.msa_attention_ex_workspace.argtypes = [i64, i32, i32, i32, i64]
+        lib.msa_attention_ex_workspace.restype = i64
         lib.msa_block_attention.argtypes = three + [ptr, i32] + tail
         lib.msa_block_attention.restype = ctypes.c_int
         lib.msa_attention_workspace.argtypes = [i64, i32, i32, i32, i64, i32]
@@ -672,7 +674,16 @@ def msa_attention_tile_rows(T: int, batch: int, Hq: int, Hkv: int, max_blocks: i
                                                       int(max_blocks), int(num_blocks)))
 
 
+def msa_attention_ex_workspace(T: int, batch: int, Hq: int, Hkv: int, max_blocks: int) -> int:
+    """Bytes of workspace with which an attention call of these sizes with
+    ``softcap``, ``slopes`` or ``visible`` is split as it would choose to
+    (``msa_attention_workspace``, or more)."""
+    return int(load_library().msa_attention_ex_workspace(int(T), int(batch), int(Hq), int(Hkv),
+                                                         int(max_blocks)))
+
+
 _workspace_bytes = functools.lru_cache(maxsize=1024)(msa_attention_workspace)
+_form_workspace_bytes = functools.lru_cache(maxsize=1024)(msa_attention_ex_workspace)
 
 
 def _attention(query, key, value, blocks, block_table, cu_seqlens_q, kv_len, layout, sparse_mode,
@@ -727,7 +738,10 @@ def _attention(query, key, value, blocks, block_table, cu_seqlens_q, kv_len, lay
     scale = 1.0 / math.sqrt(D) if softmax_scale is None else float(softmax_scale)
     handle = _raw_stream(stream, index)
     with _guard(index):
-        need = 0 if workspace is not None else _workspace_bytes(T, B, Hq, Hkv, max_blocks, k)
+        form = softcap or slopes is not None or visible is not None
+        need = (0 if workspace is not None else
+                _form_workspace_bytes(T, B, Hq, Hkv, max_blocks) if form else
+                _workspace_bytes(T, B, Hq, Hkv, max_blocks, k))
         if need:
             # memory of the stream that the kernels run on, so that it is
             # handed on only behind them
@@ -743,7 +757,7 @@ def _attention(query, key, value, blocks, block_table, cu_seqlens_q, kv_len, lay
         if blocks is not None:
             st = lib.msa_block_attention(_packed(query), _packed(key), _packed(value),
                                          blocks.data_ptr(), k, *lens, *rest)
-        elif softcap or slopes is not None or visible is not None:
+        elif form:
             st = lib.msa_attention_ex(_packed(query), _packed(key), _packed(value), *lens,
                                       float(softcap or 0.0), _address(slopes), _address(visible),
                                       *rest)
@@ -767,7 +781,8 @@ def msa_attention(query: torch.Tensor, key: torch.Tensor, value: torch.Tensor,
     ([T, Hq] float32, if given) the log of its softmax's sum; asynchronous on
     ``stream`` (default: torch's current stream).  ``softmax_scale`` None is
     1 / sqrt(128).  Without ``workspace`` the memory that a split over the keys
-    needs (``msa_attention_workspace``) is allocated here.
+    needs (``msa_attention_workspace``; with one of the following
+    ``msa_attention_ex_workspace``) is allocated here.
 
     ``softcap`` (None or 0: none) caps the scores by softcap * tanh(S / softcap);
     ``slopes`` ([Hq] float32) takes slopes[h] * |position - key| off them;

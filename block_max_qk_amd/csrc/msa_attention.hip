@@ -79,7 +79,7 @@ struct Plan {
 // 131072 keys beside 127, 255 or 1023 of 512: 1380, 1430 and 1790 us, in parts
 // 167, 246 and 890).
 Plan plan_for(int64_t T, int64_t B, int64_t Hq, int64_t Hkv, int64_t MB, int64_t nsel,
-              int most_rows = 256, int64_t most_split = kMaxSplit) {
+              int most_rows = 256, int64_t most_split = kMaxSplit, int least_blocks = 8) {
   Plan p{};
   const int64_t g = Hq / Hkv;
   const bool few = nsel > 0 ? T < 8 * B || T * Hkv < 640 : T * std::min<int64_t>(g, 16) <= 16 * B;
@@ -96,14 +96,14 @@ Plan plan_for(int64_t T, int64_t B, int64_t Hq, int64_t Hkv, int64_t MB, int64_t
   p.ntiles = std::min<int64_t>(T, (T + B * (p.tpt - 1)) / p.tpt);
   const int64_t items = std::max<int64_t>(p.ntiles * Hkv * p.hchunks, 1);
   const int64_t blocks = std::max<int64_t>(few && nsel > 0 ? std::min(nsel, MB) : MB, 1);
-  p.min_blocks = few ? 2 : 8;
+  p.min_blocks = few ? 2 : p.rows == 256 ? 8 : least_blocks;
   const int64_t want = nsel > 0 ? (few ? 128 : 256) : few ? 1536 : p.rows == 128 ? 512 : 256;
   int64_t n = items >= want ? 1 : (want + items - 1) / items;
   p.target = 1;
   if (nsel == 0 && (few || B > 1)) {
     const int64_t heads = Hkv * p.hchunks;
     p.target = (int)std::max<int64_t>((p.rows == 128 ? 384 : 192) / heads, 1);
-    n = items >= 1024 || MB < (few ? 8 : 16) ? 1
+    n = items >= 1024 || MB < (few ? 8 : 2 * p.min_blocks) ? 1
         : std::min<int64_t>(p.target, std::max<int64_t>((1 << 18) / (T * Hq), 1));
     p.balanced = true;
   }
@@ -114,8 +114,31 @@ Plan plan_for(int64_t T, int64_t B, int64_t Hq, int64_t Hkv, int64_t MB, int64_t
   return p;
 }
 
+// Bytes of one part's sums.
+int64_t part_bytes(int64_t T, int64_t Hq) {
+  return T * Hq * (int64_t)(msa::kD * sizeof(float) + sizeof(float2));
+}
+
 int64_t workspace_for(const Plan& p, int64_t T, int64_t Hq) {
-  return p.nsplit > 1 ? p.nsplit * T * Hq * (int64_t)(msa::kD * sizeof(float) + sizeof(float2)) : 0;
+  return p.nsplit > 1 ? p.nsplit * part_bytes(T, Hq) : 0;
+}
+
+// The plan of a call in another form, in at most `room` parts.  128 rows take the
+// place of 256 below 128 blocks, and where a causal range narrows the keys, as
+// documents do (32 heads on 4, us with 128 and 256 rows: 2048 tokens over 4096 keys
+// biased 127 and 138, over 16384 553 and 540, over 32768 capped 1363 and 1294; 16
+// requests of 300 over 2000 keys capped 222 and 256; one prompt of 4096 biased 170
+// and 159; 4 requests of 1000 in documents of 1024 tokens 72 and 86).  Tiles of 128
+// rows are split down to 4 blocks a part, as a stage takes longer and a range
+// leaves fewer of them: us with parts of 8, 4 and 2 blocks or more, 50 tokens over
+// 2992 keys capped 44, 30 and 26; 2 requests of 40 over 13600 46, 35 and 39; 5
+// prompts of 1750 tokens in all with images 55, 44 and 42; one of 1233 tokens with
+// images 46, 48 and 53; 5 requests of 976 over 1089 in documents 55, 58 and 58.
+Plan plan_form(int64_t T, int64_t B, int64_t Hq, int64_t Hkv, int64_t MB, bool narrow,
+               int64_t room) {
+  Plan p = plan_for(T, B, Hq, Hkv, MB, 0, 256, room, 4);
+  if (p.rows == 256 && (MB < 128 || narrow)) p = plan_for(T, B, Hq, Hkv, MB, 0, 128, room, 4);
+  return p;
 }
 
 // Sizes that a plan is asked for without a call.
@@ -251,18 +274,13 @@ msa_status_t run(const msa_tensor_t* query, const msa_tensor_t* key, const msa_t
   if (!query->data || (kv.pages > 0 && (!key->data || !value->data))) return MSA_ERR_NULL;
 
   Plan plan = plan_for(T, batch, Hq, Hkv, max_blocks, selected ? num_blocks : 0);
-  // The other forms take 128 rows in place of 256 below 128 blocks, and where a
-  // causal range narrows the keys, as documents do (32 heads on 4, us with 128 and
-  // 256 rows: 2048 tokens over 4096 keys biased 127 and 138, over 16384 553 and 540,
-  // over 32768 capped 1363 and 1294; 16 requests of 300 over 2000 keys capped 222 and
-  // 256; one prompt of 4096 biased 170 and 159; 4 requests of 1000 in documents of
-  // 1024 tokens 72 and 86), in as many parts as the workspace, which does not know
-  // the form, has room for.
-  if (plan.rows == 256 && (forms.softcap > 0.f || forms.slopes || forms.visible) &&
-      (max_blocks < 128 || (forms.visible && sparse_mode == 3)))
-    plan = plan_for(T, batch, Hq, Hkv, max_blocks, 0, 128, plan.nsplit);
   const int64_t need = workspace_for(plan, T, Hq);
   if (need > 0 && (!workspace || workspace_bytes < need)) return MSA_ERR_WORKSPACE;
+  if (forms.softcap > 0.f || forms.slopes || forms.visible) {
+    const int64_t room = workspace ? workspace_bytes / part_bytes(T, Hq) : 1;
+    plan = plan_form(T, batch, Hq, Hkv, max_blocks, forms.visible && sparse_mode == 3,
+                     std::clamp<int64_t>(room, 1, kMaxSplit));
+  }
   int64_t grid = plan.units;
   if (selected && plan.rows != msa::kAttnRows) {   // runs of 8 tiles, 8 runs at a time
     const int64_t runs = (plan.ntiles + 7) / 8 * Hkv * plan.hchunks;
@@ -286,7 +304,7 @@ msa_status_t run(const msa_tensor_t* query, const msa_tensor_t* key, const msa_t
   p.lse = lse;
   p.part_o = static_cast<float*>(workspace);
   p.part_ml = reinterpret_cast<float2*>(static_cast<float*>(workspace) +
-                                        (need > 0 ? plan.nsplit * T * Hq * msa::kD : 0));
+                                        (plan.nsplit > 1 ? plan.nsplit * T * Hq * msa::kD : 0));
   p.q_row_stride = q_row * 2;
   p.k_page_stride = kv.page;
   p.v_page_stride = vv.page;
@@ -367,6 +385,16 @@ int64_t msa_attention_workspace(int64_t T, int32_t batch, int32_t Hq, int32_t Hk
                                 int64_t max_blocks, int32_t num_blocks) {
   if (!sizes_ok(T, batch, Hq, Hkv, max_blocks, num_blocks)) return 0;
   return workspace_for(plan_for(T, batch, Hq, Hkv, max_blocks, num_blocks), T, Hq);
+}
+
+int64_t msa_attention_ex_workspace(int64_t T, int32_t batch, int32_t Hq, int32_t Hkv,
+                                   int64_t max_blocks) {
+  if (!sizes_ok(T, batch, Hq, Hkv, max_blocks, 0)) return 0;
+  int64_t most = msa_attention_workspace(T, batch, Hq, Hkv, max_blocks, 0);
+  for (const bool narrow : {false, true})
+    most = std::max(most, workspace_for(plan_form(T, batch, Hq, Hkv, max_blocks, narrow, kMaxSplit),
+                                        T, Hq));
+  return most;
 }
 
 int32_t msa_attention_tile_rows(int64_t T, int32_t batch, int32_t Hq, int32_t Hkv,

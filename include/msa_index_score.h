@@ -462,8 +462,12 @@ msa_status_t msa_attention(const msa_tensor_t* query, const msa_tensor_t* key,
  *              token with visible[t, 1] <= visible[t, 0] sees nothing.  Rows of
  *              tokens behind the last request are not read.
  *
- * With none of the three it is msa_attention, bit for bit.  The workspace is
- * msa_attention's.  lse is the log of the sum of exp(S2).
+ * workspace    at least msa_attention's; with msa_attention_ex_workspace(...) bytes
+ *              short calls are split into shorter parts (50 tokens over 2992 keys,
+ *              capped: 44 us without, 30 with it).
+ *
+ * With none of the three it is msa_attention, bit for bit.  lse is the log of the
+ * sum of exp(S2).
  */
 msa_status_t msa_attention_ex(const msa_tensor_t* query, const msa_tensor_t* key,
                               const msa_tensor_t* value, const int32_t* block_table,
@@ -494,6 +498,12 @@ msa_status_t msa_block_attention(const msa_tensor_t* query, const msa_tensor_t* 
  * Host-only. */
 int64_t msa_attention_workspace(int64_t T, int32_t batch, int32_t Hq, int32_t Hkv,
                                 int64_t max_blocks, int32_t num_blocks);
+
+/* Bytes of workspace with which msa_attention_ex splits a call of these sizes as
+ * it would choose to, whatever its form: msa_attention_workspace(..., 0) or more.
+ * Host-only. */
+int64_t msa_attention_ex_workspace(int64_t T, int32_t batch, int32_t Hq, int32_t Hkv,
+                                   int64_t max_blocks);
 
 /* Rows -- (query token, head) pairs of one KV head -- of the tiles that
  * msa_attention (num_blocks = 0) or msa_block_attention would use for a call of

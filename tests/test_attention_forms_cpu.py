@@ -33,3 +33,21 @@ def test_rejected():
     assert call(k=desc((6, 128, 2, 128))) == DTYPE          # what msa_attention rejects
     assert call(scale=0.0, cap=1.0) == ATTR
     assert call(T=2, mb=1000, cap=30.0) == WORKSPACE
+
+
+def test_workspace():
+    """Never less than the plain scores' and at most a part per 4 blocks; 0 for sizes
+    that no call takes."""
+    part = 50 * 32 * (128 * 4 + 8)
+    assert m.msa_attention_workspace(50, 1, 32, 4, 24) == 3 * part
+    assert m.msa_attention_ex_workspace(50, 1, 32, 4, 24) == 6 * part
+    for T in (1, 7, 50, 300, 2000, 9000):
+        for B in (1, 2, 9, 64):
+            for Hq, Hkv in ((8, 1), (32, 4), (64, 8), (12, 12)):
+                for mb in (1, 4, 9, 40, 130, 1000):
+                    plain = m.msa_attention_workspace(T, B, Hq, Hkv, mb)
+                    most = m.msa_attention_ex_workspace(T, B, Hq, Hkv, mb)
+                    row = T * Hq * (128 * 4 + 8)
+                    assert plain <= most <= max(plain, row * -(-mb // 4)) and most % row == 0
+    assert m.msa_attention_ex_workspace(50, 1, 32, 5, 24) == 0
+    assert m.msa_attention_ex_workspace(50, 0, 32, 4, 24) == 0

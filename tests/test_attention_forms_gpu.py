@@ -300,6 +300,30 @@ def test_none_of_the_forms_is_the_plain_call(dev):
         assert torch.equal(out, want) and torch.equal(lse, want_lse)
 
 
+@pytest.mark.parametrize("form", [dict(cap=20.0), dict(bias=True, mask="any"),
+                                  dict(mask="documents")])
+def test_workspaces_of_any_size(form, dev):
+    """A call is split into as many parts as its workspace holds."""
+    import block_max_qk_amd as m
+    for q_lens, kv_lens in (([50], [2992]), ([40, 2, 9], [1500, 2300, 128]), ([33], [700]),
+                            ([150, 90], [1100, 90]), ([900], [1000]), ([1, 1], [3000, 200])):
+        c = make(q_lens, kv_lens, 16, 2, "BNBD", BF, seed=7, **form)
+        T, B, mb = sum(q_lens), len(q_lens), c["table"].shape[1]
+        row = T * 16 * (128 * 4 + 8)
+        least = m.msa_attention_workspace(T, B, 16, 2, mb)
+        most = m.msa_attention_ex_workspace(T, B, 16, 2, mb)
+        ref = reference(c)
+        for size in sorted({least, least + row, (least + most) // 2 // row * row + 48, most,
+                            most + 5 * row}):
+            if size < least:
+                continue
+            log("workspace", form, q_lens, size // row)
+            # (bytes past the size that is given stay as they are)
+            ws = torch.full((size + 256,), 77, dtype=torch.uint8, device=dev)
+            check(c, *call(c, dev, workspace=ws[:size]), ref)
+            assert (ws[size:] == 77).all()
+
+
 def test_same_bits_again_and_on_a_stream(dev):
     import block_max_qk_amd as m
     for q_lens, kv_lens in (([1, 1], [3000, 20]), ([100], [2000])):
