@@ -11,7 +11,7 @@
 // workgroup waits for another, and one launch does it all (a scan of its own in
 // front would be a second launch, 5 us, for less than that of reads).  The lengths
 // of groups of `group` requests are scanned by one wave, so that there are about
-// 512 workgroups however many requests there are.
+// 512 workgroups up to 32768 requests (and the reads grow with their square).
 //
 // 64 decode requests over tables of 256 blocks 4 us, 300 of 1 to 200 tokens 5,
 // 4096 over tables of 1024 blocks (19 MB) 9 to 10, 1.9 TB/s, 13.5 with one request's
