@@ -189,13 +189,15 @@ int set_forms(const Forms& f, float scale, AttnParams& p) {
   if (f.slopes) form |= msa::kBias;
   if (f.softcap > 0.f) {
     form |= msa::kCap;
-    // tanh(x) = x (1 + c1 x^2 + .. + c4 x^8) for |x| <= 0.75, off by 2.7e-7 at most
-    constexpr double kTanh[5] = {1.0, -0.333280453, 0.132533633, -0.0498660864, 0.0127505841};
+    // tanh(x) = x (1 + c1 x^2 + .. + c4 x^8) for |x| <= 5/8, off by 1.22e-7 of itself
+    // at most (two of float32's half steps)
+    constexpr double kTanh[5] = {1.0, -0.333323412, 0.133081751, -0.0519479045, 0.0151953732};
+    constexpr double kNear = 0.625;
     const double a = (double)scale / f.softcap;
     double unit = (double)scale * msa::kLog2e;
     p.cap_top = f.softcap * msa::kLog2e;
     p.cap_twice = (float)(2.0 * msa::kLog2e * a);
-    p.cap_near = (float)(0.75 / a);
+    p.cap_near = (float)(kNear / a);
     for (int i = 0; i < 5; ++i, unit *= a * a) {
       p.cap_poly[i] = (float)(kTanh[i] * unit);
       // (a cap so small that a coefficient has no float32: never near; one so large

@@ -298,11 +298,11 @@ __device__ __forceinline__ TileSpan tile_span(const AttnParams& p, const AttnTil
 }
 
 // Capped scores in units of log2: cap_top * tanh(a s) of the products s, with a =
-// softmax_scale / softcap.  Where all of a wave's |a s| are at most 0.75, an odd
-// polynomial of degree 9 (off by 2.7e-7 of the cap at most, 4.4 of float32's half
-// steps, fitted to tanh for the smallest largest error), elsewhere 1 - 2 /
-// (exp(2 a s) + 1), whose error is a few roundings of the cap itself (infinities
-// give the cap).
+// softmax_scale / softcap.  Where all of a wave's |a s| are at most 5/8, an odd
+// polynomial of degree 9, fitted to tanh for the smallest largest error relative to
+// tanh itself, 1.22e-7 or two of float32's half steps (to 3/4 it would be 6.5e-7, or
+// one term more), elsewhere 1 - 2 / (exp(2 a s) + 1), whose error is a few roundings
+// of the cap itself (infinities give the cap).
 __device__ __forceinline__ float cap_slope(const AttnParams& p, float s) {   // capped / s
   const float u = s * s;
   float r = __builtin_fmaf(u, p.cap_poly[4], p.cap_poly[3]);

@@ -454,7 +454,7 @@ msa_status_t msa_attention(const msa_tensor_t* query, const msa_tensor_t* key,
  * softcap      0 (none) or positive, finite; MSA_ERR_ATTR otherwise, and where
  *              softmax_scale / softcap has no float32.  A capped score is off by a
  *              few units in the last place of the cap at most, and by as many of
- *              its own where the scores beside it are below 0.75 softcap too.
+ *              its own where the scores beside it are below 5/8 softcap too.
  * slopes       device float32 [Hq], compact, finite; or NULL.  (Bias and scores are
  *              added in float32: far keys of a steep head lose digits that their
  *              weights do not have.)

@@ -1,0 +1,76 @@
+"""Capped scores to their own last digits: over a single key the log of the
+softmax's sum is the capped score itself, and a query and a key of one non-zero
+element each make an exact product.
+
+With e = 2^-24 a capped score is off by at most 8 e of itself (below 5/8 of the
+cap 2.1 e of the polynomial's fit, 1 e each of its first coefficient, its last sum
+and the product, 0.5 e of the smaller terms; above it 2.9 e of the cap, at
+0.55 of it, of the exponential and the reciprocal, 1 e each of the cap and the last
+sum), and the log of the sum by 4 e (1 + |score|), and 24 e where float16's lift
+(2^11) is added and taken off."""
+import sys
+
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+BF, FP = torch.bfloat16, torch.float16
+E = 2.0 ** -24
+
+
+@pytest.fixture(scope="module")
+def dev():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    import block_max_qk_amd
+    block_max_qk_amd.load_library()
+    return torch.device("cuda:0")
+
+
+def capped(s, cap, scale, kernel, dtype, dev, key=1.0):
+    """lse of queries s (and a key) over one key each: one request of many tokens
+    (tiles of 128 rows) or many of one (16 rows)."""
+    import block_max_qk_amd as m
+    n = len(s)
+    q = torch.zeros(n, 1, 128, dtype=dtype)
+    q[:, 0, 5] = s
+    k = torch.zeros(1 if kernel == "tiles" else n, 1, 128, dtype=dtype)
+    k[:, 0, 5] = key
+    ints = dict(dtype=torch.int32, device=dev)
+    if kernel == "tiles":
+        cu, kv = torch.tensor([0, n], **ints), torch.ones(1, **ints)
+    else:
+        cu, kv = torch.arange(n + 1, **ints), torch.ones(n, **ints)
+    want = 16 if kernel == "rows" else 128
+    assert m.msa_attention_tile_rows(n, len(kv), 1, 1, 1) == want
+    print("capped", cap, kernel, dtype, file=sys.stderr, flush=True)
+    _, lse = m.attention(q.to(dev), k.to(dev), k.to(dev), None, cu, kv, "TND", 0, scale,
+                         max_blocks=1, return_lse=True, softcap=cap)
+    torch.cuda.synchronize()
+    return lse.cpu()[:, 0]
+
+
+def sweep(cap, scale, parts, dtype):
+    """Queries whose scores are these parts of the cap, of either sign."""
+    s = (parts * (cap / scale)).to(dtype)
+    return torch.cat([s, -s])
+
+
+def check(got, s, cap, scale, dtype):
+    want = cap * torch.tanh(s.double() * scale / cap)
+    tol = 8 * E * want.abs() + 4 * E * (1 + want.abs()) + (24 * E if dtype == FP else 0)
+    err = (got.double() - want).abs()
+    at = int((err / tol).nan_to_num(1e30).argmax())
+    assert (err <= tol).all(), (float((err / tol).max()), float(s[at] * scale / cap))
+
+
+NEAR = torch.logspace(-3, -0.30103, 300, dtype=torch.float64)       # to half the cap
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("kernel", ["rows", "tiles"])
+def test_below_the_cap(kernel, dtype, dev):
+    """Waves whose scores all stay below half the cap."""
+    for cap, scale in ((50.0, 0.125), (1000.0, 0.125), (1000.0, 1.0)):
+        s = sweep(cap, scale, NEAR, dtype)
+        check(capped(s, cap, scale, kernel, dtype, dev), s, cap, scale, dtype)
