@@ -193,20 +193,23 @@ int set_forms(const Forms& f, float scale, AttnParams& p) {
     // at most (two of float32's half steps)
     constexpr double kTanh[5] = {1.0, -0.333323412, 0.133081751, -0.0519479045, 0.0151953732};
     constexpr double kNear = 0.625;
-    const double a = (double)scale / f.softcap;
-    double unit = (double)scale * msa::kLog2e;
+    double a = (double)scale / f.softcap, unit = (double)scale * msa::kLog2e;
+    // A cap so large or small that a coefficient of the products' square has no
+    // float32 of full precision (at a scale of 1/sqrt(128), above 2170): the products
+    // are scaled by a power of two in front (2^-110 at the least, so that those above
+    // 2^-16 keep their digits), which changes no other rounding.
+    const double a4 = a * a * (a * a), c4 = kTanh[4] * unit * a4 * a4;
+    p.cap_unit = 1.f;
+    if (!(c4 >= FLT_MIN && c4 <= FLT_MAX)) {
+      const int e = std::clamp(std::ilogb(a) + 1, -110, 127);
+      p.cap_unit = std::ldexp(1.f, e);
+      a = std::ldexp(a, -e);
+      unit = std::ldexp(unit, -e);
+    }
     p.cap_top = f.softcap * msa::kLog2e;
     p.cap_twice = (float)(2.0 * msa::kLog2e * a);
-    p.cap_near = (float)(kNear / a);
-    for (int i = 0; i < 5; ++i, unit *= a * a) {
-      p.cap_poly[i] = (float)(kTanh[i] * unit);
-      // (a cap so small that a coefficient has no float32: never near; one so large
-      // that a coefficient is lost: near where it does not count, as far as a
-      // product's square has a float32)
-      if (!std::isfinite(p.cap_poly[i])) p.cap_near = -1.f;
-      if (p.cap_poly[i] > -FLT_MIN && p.cap_poly[i] < FLT_MIN)
-        p.cap_near = std::min(p.cap_near, (float)std::min(1e-4 / a, 1e19));
-    }
+    p.cap_near = (float)std::min(kNear / a, (double)FLT_MAX);
+    for (int i = 0; i < 5; ++i, unit *= a * a) p.cap_poly[i] = (float)(kTanh[i] * unit);
   }
   if (f.visible || form) form |= msa::kRange;
   return form;

@@ -58,9 +58,11 @@ struct AttnParams {
   const int2* visible;         // [T]: first visible key and the end of them, or nullptr
   float per_scale;             // 1 / softmax_scale
   float cap_top;               // softcap * log2(e)
-  float cap_twice;             // 2 log2(e) softmax_scale / softcap
-  float cap_near;              // products up to which the polynomial is the tanh
-  float cap_poly[5];           // its coefficients, on a product's square
+  float cap_unit;              // the products are scaled by this power of two: 1 but for
+                               // very large and small caps
+  float cap_twice;             // 2 log2(e) softmax_scale / softcap / cap_unit
+  float cap_near;              // scaled products up to which the polynomial is the tanh
+  float cap_poly[5];           // its coefficients, on a scaled product's square
 };
 
 // Forms of the scores that a kernel is compiled for (0: plain ones).
@@ -297,8 +299,8 @@ __device__ __forceinline__ TileSpan tile_span(const AttnParams& p, const AttnTil
   return TileSpan{0, 0, attn_last(p, w, w.i0), attn_last(p, w, w.i0 + w.ntok - 1)};
 }
 
-// Capped scores in units of log2: cap_top * tanh(a s) of the products s, with a =
-// softmax_scale / softcap.  Where all of a wave's |a s| are at most 5/8, an odd
+// Capped scores in units of log2: cap_top * tanh(a s) of the products s (scaled by
+// cap_unit), with a = softmax_scale / softcap / cap_unit.  Where all of a wave's |a s| are at most 5/8, an odd
 // polynomial of degree 9, fitted to tanh for the smallest largest error relative to
 // tanh itself, 1.22e-7 or two of float32's half steps (to 3/4 it would be 6.5e-7, or
 // one term more), elsewhere 1 - 2 / (exp(2 a s) + 1), whose error is a few roundings
@@ -609,6 +611,10 @@ __global__ __launch_bounds__(256, 1) void attn_rows_kernel(AttnParams p) {
   // products of keys j0 + 4 G + r and j0 + 16 + 4 G + r to scores in units of log2
   [[maybe_unused]] auto form = [&](f32x4& sa, f32x4& sb, int j0) __attribute__((always_inline)) {
     if constexpr (F & kCap) {
+      if (p.cap_unit != 1.f) {
+        sa *= p.cap_unit;
+        sb *= p.cap_unit;
+      }
       float far = 0.f;
 #pragma unroll
       for (int r = 0; r < 4; ++r) far = fmaxf(far, fmaxf(fabsf(sa[r]), fabsf(sb[r])));
@@ -1170,13 +1176,19 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tile_kernel(AttnParams p) {
     // are capped here, in units of log2, and a bias is added.
     [[maybe_unused]] bool near = false;
     if constexpr (F & kCap) {
+      if (p.cap_unit != 1.f) {
+        st[0] *= p.cap_unit;
+        st[1] *= p.cap_unit;
+      }
       float far = 0.f;
 #pragma unroll
       for (int t = 0; t < 2; ++t)
 #pragma unroll
         for (int r = 0; r < 16; ++r) far = fmaxf(far, fabsf(st[t][r]));
       const bool poly = !__ballot(far > p.cap_near);
-      near = poly && !edge && !(F & kBias);
+      // (scores of large caps are rounded before the largest is taken off them, whose
+      // rounding may be more than an exponent holds)
+      near = poly && !edge && !(F & kBias) && p.cap_unit == 1.f;
       if (!near) {
         if (poly) {
 #pragma unroll

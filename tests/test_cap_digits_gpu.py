@@ -74,3 +74,16 @@ def test_below_the_cap(kernel, dtype, dev):
     for cap, scale in ((50.0, 0.125), (1000.0, 0.125), (1000.0, 1.0)):
         s = sweep(cap, scale, NEAR, dtype)
         check(capped(s, cap, scale, kernel, dtype, dev), s, cap, scale, dtype)
+
+
+@pytest.mark.parametrize("kernel", ["rows", "tiles"])
+def test_caps_of_any_size(kernel, dev):
+    """Caps whose polynomial has no float32 coefficients without a scaling of its
+    argument: large ones, whose scores are ordinary or near them, and small ones."""
+    for cap in (2000.0, 2200.0, 1e4, 1e5, 1e7, 1e12, 1e20, 1e30, 1e-4, 1e-12):
+        for low in (-1.0, -4.0, -7.0):
+            s = sweep(cap, 0.125, torch.logspace(low, low + 0.7, 200, dtype=torch.float64), BF)
+            check(capped(s, cap, 0.125, kernel, BF, dev), s, cap, 0.125, BF)
+    s = torch.logspace(-1, 3, 400, dtype=torch.float64).to(BF)      # ordinary scores
+    for cap in (1e4, 1e5, 1e7, 1e30):
+        check(capped(s, cap, 0.125, kernel, BF, dev), s, cap, 0.125, BF)
