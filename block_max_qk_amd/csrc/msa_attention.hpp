@@ -314,7 +314,9 @@ __device__ __forceinline__ float cap_slope(const AttnParams& p, float s) {   // 
 }
 __device__ __forceinline__ float cap_far(const AttnParams& p, float s) {
   const float e = __builtin_amdgcn_exp2f(s * p.cap_twice);
-  return __builtin_fmaf(-2.f * p.cap_top, __builtin_amdgcn_rcpf(e + 1.f), p.cap_top);
+  // (-2 / (e + 1), as twice the cap may have no float32)
+  return __builtin_fmaf(p.cap_top, __builtin_amdgcn_rcpf(__builtin_fmaf(e, -0.5f, -0.5f)),
+                        p.cap_top);
 }
 
 // Values of keys j and j + 1 with those outside the span cleared.

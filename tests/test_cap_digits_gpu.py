@@ -87,3 +87,15 @@ def test_caps_of_any_size(kernel, dev):
     s = torch.logspace(-1, 3, 400, dtype=torch.float64).to(BF)      # ordinary scores
     for cap in (1e4, 1e5, 1e7, 1e30):
         check(capped(s, cap, 0.125, kernel, BF, dev), s, cap, 0.125, BF)
+
+
+@pytest.mark.parametrize("kernel", ["rows", "tiles"])
+def test_caps_next_to_the_types_end(kernel, dev):
+    """Twice the cap in units of log2 has no float32."""
+    for cap in (1e38, 2e38):
+        s = (torch.tensor([0.7, -1.1, 0.9, 1.5] * 10).double() * (cap * 2.0 ** -63)).to(BF)
+        check(capped(s, cap, 1.0, kernel, BF, dev, 2.0 ** 63), s.double() * 2.0 ** 63, cap, 1.0, BF)
+        s = torch.tensor([1.0, -3.0, 1e5, 1e9, -1e12, 1e15]).to(BF).repeat(10)
+        for key in (1.0, 2.0 ** 33, 2.0 ** 60):
+            s1 = s.double() * key
+            check(capped(s, cap, 1.0, kernel, BF, dev, key), s1, cap, 1.0, BF)
