@@ -63,6 +63,7 @@ struct AttnParams {
   float cap_twice;             // 2 log2(e) softmax_scale / softcap / cap_unit
   float cap_near;              // scaled products up to which the polynomial is the tanh
   float cap_poly[5];           // its coefficients, on a scaled product's square
+  int32_t cap_late;            // capped scores may stay products until their weights
 };
 
 // Forms of the scores that a kernel is compiled for (0: plain ones).
@@ -311,6 +312,10 @@ __device__ __forceinline__ float cap_slope(const AttnParams& p, float s) {   // 
   r = __builtin_fmaf(u, r, p.cap_poly[2]);
   r = __builtin_fmaf(u, r, p.cap_poly[1]);
   return __builtin_fmaf(u, r, p.cap_poly[0]);
+}
+__device__ __forceinline__ float cap_now(const AttnParams& p, float s) {
+#pragma clang fp contract(off)   // (rounded, not a factor of a later sum)
+  return s * cap_slope(p, s);
 }
 __device__ __forceinline__ float cap_far(const AttnParams& p, float s) {
   const float e = __builtin_amdgcn_exp2f(s * p.cap_twice);
@@ -623,8 +628,8 @@ __global__ __launch_bounds__(256, 1) void attn_rows_kernel(AttnParams p) {
       if (!__ballot(far > p.cap_near)) {
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          sa[r] *= cap_slope(p, sa[r]);
-          sb[r] *= cap_slope(p, sb[r]);
+          sa[r] = cap_now(p, sa[r]);
+          sb[r] = cap_now(p, sb[r]);
         }
       } else {
 #pragma unroll
@@ -1188,15 +1193,13 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tile_kernel(AttnParams p) {
 #pragma unroll
         for (int r = 0; r < 16; ++r) far = fmaxf(far, fabsf(st[t][r]));
       const bool poly = !__ballot(far > p.cap_near);
-      // (scores of large caps are rounded before the largest is taken off them, whose
-      // rounding may be more than an exponent holds)
-      near = poly && !edge && !(F & kBias) && p.cap_unit == 1.f;
+      near = poly && !edge && !(F & kBias) && p.cap_late;
       if (!near) {
         if (poly) {
 #pragma unroll
           for (int t = 0; t < 2; ++t)
 #pragma unroll
-            for (int r = 0; r < 16; ++r) st[t][r] *= cap_slope(p, st[t][r]);
+            for (int r = 0; r < 16; ++r) st[t][r] = cap_now(p, st[t][r]);
         } else {
 #pragma unroll
           for (int t = 0; t < 2; ++t)
