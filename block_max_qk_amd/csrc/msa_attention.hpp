@@ -272,6 +272,25 @@ __device__ __forceinline__ Span attn_span(const AttnParams& p, const AttnTile& w
   return s;
 }
 
+// A biased row's scores are taken against the bias of its nearest key, which all of
+// the row's scores have in common and no weight depends on: slope * |pos - j| is then
+// slope * |near - j| over the keys that it sees, with near the key of its span next
+// to its position, and a row of far keys alone (distances of 10^5, say) keeps the
+// digits that tell them apart.  What was left out is put back in lse.
+__device__ __forceinline__ int nearest(const Span& s, int pos) {
+  return s.last < s.first ? pos : min(max(pos, s.first), s.last);
+}
+// That bias, of the i-th new token and query head h.
+template <int F>
+__device__ __forceinline__ float lse_shift(const AttnParams& p, const AttnTile& w, int i, int h) {
+  if constexpr (F & kBias) {
+    const int pos = w.len - w.Lq + i;
+    const float away = (float)pos - (float)nearest(attn_span<F>(p, w, i), pos);
+    return -p.slopes[h] * fabsf(away);
+  }
+  return 0.f;
+}
+
 // Over a tile's tokens: the smallest and largest first visible key (of tokens
 // that see one), the smallest and largest last one.
 struct TileSpan {
@@ -496,12 +515,12 @@ __global__ __launch_bounds__(256, 1) void attn_rows_kernel(AttnParams p) {
   const int lim_lo = sees.last_lo, lim_hi = sees.last;
   const int nb = lim_hi >= 0 ? lim_hi / kP + 1 : 0;    // end of the blocks with a visible key
   const int nb0 = F ? sees.first / kP : 0;             // and the first of them
-  // (a bias's slope in units of log2, and the row's position)
+  // (a bias's slope in units of log2, and the row's nearest key)
   float slope = 0.f;
-  int pos = 0;
+  int near = 0;
   if constexpr (F & kBias) {
     if (row_ok) slope = p.slopes[hk * p.g + hg] * kLog2e;
-    pos = w.len - w.Lq + w.i0 + ti;
+    near = nearest(mine_sees, w.len - w.Lq + w.i0 + ti);
   }
 
   // the part's blocks: [b0, b1) of the visible ones, or of the selected list
@@ -643,7 +662,7 @@ __global__ __launch_bounds__(256, 1) void attn_rows_kernel(AttnParams p) {
       sb *= p.c;
     }
     if constexpr (F & kBias) {
-      const float away = (float)(pos - j0 - 4 * G);
+      const float away = (float)(near - j0 - 4 * G);
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         sa[r] = __builtin_fmaf(-slope, fabsf(away - r), sa[r]);
@@ -824,7 +843,10 @@ __global__ __launch_bounds__(256, 1) void attn_rows_kernel(AttnParams p) {
   if (!row_ok) return;
   const int64_t rows = p.T * p.Hq;
   if (wave == 0 && split == 0) mark_parts(p, out_row, parts, G, 4);
+  const bool shifted = (F & kBias) && p.lse && wave == 0 && split == 0 && G == 0;
+  const float shift = shifted ? lse_shift<F>(p, w, w.i0 + ti, hk * p.g + hg) : 0.f;
   if (parts > 1) {
+    if (shifted) p.lse[out_row] = shift;         // (for the join)
     const int64_t pr = split * rows + out_row;
     if (wave == 0 && G == 0) p.part_ml[pr] = float2{mt, lt};
     if (nst > 0) {
@@ -839,7 +861,7 @@ __global__ __launch_bounds__(256, 1) void attn_rows_kernel(AttnParams p) {
                      pack2<KK>(s1[0] * inv, s1[1] * inv), pack2<KK>(s1[2] * inv, s1[3] * inv)};
   *reinterpret_cast<i32x4*>(p.out + out_row * (2 * kD) + 64 * wave + 16 * G) = res;
   if (p.lse && wave == 0 && G == 0)
-    p.lse[out_row] = lse_of<KK>(mt, lt);
+    p.lse[out_row] = lse_of<KK>(mt, lt) + shift;
 }
 
 // ---------------------------------------------------------------------------
@@ -897,8 +919,9 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnParams p) {
     if (half == 0)
       *reinterpret_cast<i32x2*>(p.out + row * (2 * kD) + 8 * l) =
           i32x2{pack2<KK>(o[0] * inv, o[1] * inv), pack2<KK>(o[2] * inv, o[3] * inv)};
+    // (of a biased row its first part has written what lse is taken against)
     if (p.lse && l == 0)
-      p.lse[row] = lse_of<KK>(mt, lt);
+      p.lse[row] = lse_of<KK>(mt, lt) + (p.slopes ? p.lse[row] : 0.f);
   }
 }
 
@@ -1070,13 +1093,13 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tile_kernel(AttnParams p) {
   const Span mine = row_ok ? attn_span<F>(p, w, w.i0 + ti) : Span{0, F ? INT32_MAX : -1};
   const int lim = mine.last;
   // a bias's slope, in units of log2 where it is added to capped scores, of the
-  // products where it is what their sums begin with; and the row's position
+  // products where it is what their sums begin with; and the row's nearest key
   [[maybe_unused]] float slope = 0.f;
-  [[maybe_unused]] int pos = INT32_MAX;
+  [[maybe_unused]] int at = INT32_MAX;
   if constexpr (F & kBias) {
     if (row_ok) {
       slope = p.slopes[hk * p.g + hg] * (F & kCap ? kLog2e : p.per_scale);
-      pos = w.len - w.Lq + w.i0 + ti;
+      at = nearest(mine, w.len - w.Lq + w.i0 + ti);
     }
   }
   parts = max(1, min(parts, (total + p.min_blocks - 1) / p.min_blocks));
@@ -1124,11 +1147,11 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tile_kernel(AttnParams p) {
   // attn_rows_kernel.)
   f32x16 st[2];
   // A stage that some row of the wave does not see whole, or (with a bias) has
-  // keys behind its own position in.
+  // keys behind its nearest one in.
   auto at_edge = [&](const Entry& cur, int in) __attribute__((always_inline)) -> bool {
     const int j0 = cur.beta * kP + in * kTileKeys;
     if constexpr (F == 0) return !cur.there || j0 + kTileKeys - 1 > lim_lo;
-    const int end = F & kBias ? min(lim, pos) : lim;
+    const int end = F & kBias ? min(lim, at) : lim;
     return !cur.there || __ballot(j0 + kTileKeys - 1 > end || j0 < mine.first);
   };
   auto scores = [&](const uint8_t* __restrict kt, [[maybe_unused]] int j0,
@@ -1137,7 +1160,7 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tile_kernel(AttnParams p) {
     // j0 + 32 t + 8 (r / 4) + 4 h + r % 4 of row n
     if constexpr ((F & kBias) && !(F & kCap)) {
       // (the bias costs one instruction a score: the sums begin with it)
-      const float away = (float)(pos - j0 - 4 * h);
+      const float away = (float)(at - j0 - 4 * h);
       if (edge) {
 #pragma unroll
         for (int t = 0; t < 2; ++t)
@@ -1207,7 +1230,7 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tile_kernel(AttnParams p) {
             for (int r = 0; r < 16; ++r) st[t][r] = cap_far(p, st[t][r]);
         }
         if constexpr (F & kBias) {
-          const float away = (float)(pos - j0 - 4 * h);
+          const float away = (float)(at - j0 - 4 * h);
 #pragma unroll
           for (int t = 0; t < 2; ++t)
 #pragma unroll
@@ -1439,7 +1462,10 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tile_kernel(AttnParams p) {
   const int64_t out_row = ((int64_t)(w.t0 + ti) * p.Hq + hk * p.g + hg);
   // register r of o[d] is head element 32 d + 8 (r / 4) + 4 h + r % 4
   if (split == 0) mark_parts(p, out_row, parts, h, 2);
+  const bool shifted = (F & kBias) && p.lse && split == 0 && h == 0;
+  const float shift = shifted ? lse_shift<F>(p, w, w.i0 + ti, hk * p.g + hg) : 0.f;
   if (parts > 1) {
+    if (shifted) p.lse[out_row] = shift;         // (for the join)
     const int64_t pr = (int64_t)split * p.T * p.Hq + out_row;
     if (h == 0) p.part_ml[pr] = float2{m, lsum};
     if (b0 < b1) {
@@ -1461,7 +1487,7 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tile_kernel(AttnParams p) {
           i32x2{pack2<KK>(o[d][4 * q] * inv, o[d][4 * q + 1] * inv),
                 pack2<KK>(o[d][4 * q + 2] * inv, o[d][4 * q + 3] * inv)};
   if (p.lse && h == 0)
-    p.lse[out_row] = lse_of<KK>(m, lsum);
+    p.lse[out_row] = lse_of<KK>(m, lsum) + shift;
 }
 
 // ---------------------------------------------------------------------------

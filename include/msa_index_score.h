@@ -456,8 +456,9 @@ msa_status_t msa_attention(const msa_tensor_t* query, const msa_tensor_t* key,
  *              few units in the last place of the cap at most, and by as many of
  *              its own where the scores beside it are below 5/8 softcap too.
  * slopes       device float32 [Hq], compact, finite; or NULL.  (Bias and scores are
- *              added in float32: far keys of a steep head lose digits that their
- *              weights do not have.)
+ *              added in float32, with the biases taken against that of the nearest key
+ *              that the token's range and sparse_mode leave: keys far behind that one
+ *              lose digits that their weights do not have.)
  * visible      device int32 [T, 2], compact, 8-byte aligned; or NULL.  Any values: a
  *              token with visible[t, 1] <= visible[t, 0] sees nothing.  Rows of
  *              tokens behind the last request are not read.

@@ -315,6 +315,7 @@ class Forms(NamedTuple):
     loss: torch.Tensor     # sum of the weights' errors
     keys: torch.Tensor     # visible keys
     top: torch.Tensor      # largest |value| of a visible key
+    shift: torch.Tensor    # |bias| of the nearest key in the token's range
 
 
 def attention_forms(query, key, value, block_table, cu_seqlens_q, kv_len, layout, sparse_mode,
@@ -335,7 +336,7 @@ def attention_forms(query, key, value, block_table, cu_seqlens_q, kv_len, layout
     scale = 1.0 / math.sqrt(D) if scale is None else scale
     e = 2.0 ** -24
     f = Forms(*(torch.zeros(T, Hq, *([D] if i in (0, 2, 3) else []), dtype=torch.float64)
-                for i in range(7)))
+                for i in range(8)))
     f.lse.fill_(-math.inf)
     first = 0
     cu = [int(x) for x in cu_seqlens_q]
@@ -349,13 +350,15 @@ def attention_forms(query, key, value, block_table, cu_seqlens_q, kv_len, layout
             continue
         pos = (int(kv_len[b]) - (cu[b + 1] - cu[b]) + torch.arange(lo, hi) - cu[b])[:, None]
         j = torch.arange(keys.shape[0])[None]
-        seen = there[None].expand(hi - lo, -1)
+        inside = torch.ones(hi - lo, keys.shape[0], dtype=torch.bool)
         if sparse_mode == 3:
-            seen = seen & (j <= pos)
+            inside = inside & (j <= pos)
         if visible is not None:
             span = visible[lo:hi].long()
-            seen = seen & (j >= span[:, :1]) & (j < span[:, 1:])
+            inside = inside & (j >= span[:, :1]) & (j < span[:, 1:])
+        seen = inside & there[None]
         away = (pos - j).abs().double()
+        least = torch.where(inside, away, math.inf).amin(1, keepdim=True).nan_to_num(0, 0, 0)
         g = Hq // keys.shape[1]
         some = seen.any(1)
         for h in range(Hq):
@@ -364,9 +367,12 @@ def attention_forms(query, key, value, block_table, cu_seqlens_q, kv_len, layout
             d = 130 * e * scale * (q.abs() @ k.abs().T)
             if softcap:
                 s, d = softcap * torch.tanh(s / softcap), d + 12 * e * softcap
+            base = 0.0
             if slopes is not None:
-                bias = float(slopes[h]) * away
-                s, d = s - bias, d + (0 if softcap else 130 * e) * bias.abs() + 2 * e * bias.abs()
+                bias, base = float(slopes[h]) * (away - least), float(slopes[h]) * least
+                d = d + (0 if softcap else 130 * e) * bias.abs() + 2 * e * bias.abs()
+                s = s - bias
+                f.shift[lo:hi, h] = base[:, 0].abs()
             s = torch.where(seen, s, -math.inf)
             m = torch.where(some, s.amax(1), 0.0)[:, None]
             d = d + 4 * e * (1 + torch.where(seen, s, 0.0).abs() + m.abs())
@@ -381,7 +387,7 @@ def attention_forms(query, key, value, block_table, cu_seqlens_q, kv_len, layout
             wild = ~(loss <= 1)          # (0 * inf among them)
             f.drift[lo:hi, h] = torch.where(wild[:, None], 2 * big[:, None], off @ v.abs())
             f.loss[lo:hi, h] = torch.where(wild, torch.where(seen, d, 0.0).amax(1), loss)
-            f.lse[lo:hi, h] = torch.logsumexp(s, 1)
+            f.lse[lo:hi, h] = torch.logsumexp(s - base, 1)
             f.keys[lo:hi, h] = seen.sum(1).double()
             f.top[lo:hi, h] = big
     return f
@@ -399,5 +405,6 @@ def forms_bounds(f: Forms, dtype: torch.dtype):
            + f.spread * (share + u * (1.01 + f.loss))[..., None] + u * f.out.abs() * 1.01)
     if dtype == torch.float16:
         out = out + (f.keys * 2.0 ** -36 * f.top)[..., None] + 2.0 ** -25
-    lse = 1.01 * f.loss + f.keys * e + 4 * e * (1 + f.lse.abs().nan_to_num(0, 0, 0))
+    lse = (1.01 * f.loss + f.keys * e + 4 * e * (1 + f.lse.abs().nan_to_num(0, 0, 0))
+           + 4 * e * f.shift)
     return out, lse

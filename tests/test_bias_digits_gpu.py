@@ -1,0 +1,47 @@
+"""Biased scores of tokens that see far keys only: what all of a row's keys have in
+common of their biases costs none of their weights' digits, within the oracle's
+bounds (oracle/layer.py), which take the bias relative to the nearest key's."""
+import pytest
+import torch
+
+from test_attention_forms_gpu import BF, FP, call, check, dev, make, pos_of  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("dtype,cap", [(BF, 0.0), (FP, 0.0), (BF, 20.0)])
+@pytest.mark.parametrize("q_lens,kv_lens,Hq,Hkv", [
+    ([1, 1], [30000, 9000], 4, 1), ([40], [30000], 8, 2), ([130, 3], [12000, 30000], 4, 1),
+    ([2, 30], [400, 20000], 4, 4)])
+def test_far_keys_only(q_lens, kv_lens, Hq, Hkv, dtype, cap, dev):
+    """Ranges before the token (their last keys the nearest), and without a causal mask
+    behind it too; whole, split and joined."""
+    for mode in (3, 0):
+        c = make(q_lens, kv_lens, Hq, Hkv, "BNBD", dtype, mode, cap, gain=2.0)
+        c["slopes"] = torch.tensor([0.7, 0.31, 0.011, 3.3, -0.2, 0.0, 17.0, 0.1])[:Hq].contiguous()
+        pos = pos_of(c)
+        ranges = [(pos * 0, pos * 0 + 200), (pos // 2 - 70, pos // 2 + 1),
+                  (pos * 0 + 100, pos - 300)]
+        if mode == 0:
+            ranges += [(pos + 1, pos + 150)]
+        for first, end in ranges:
+            c["visible"] = torch.stack([first, end], 1).int()
+            print("far keys", q_lens, mode, dtype, cap, int(first[0]), flush=True)
+            check(c, *call(c, dev))
+
+
+def test_no_keys_and_no_pages(dev):
+    """Rows that see nothing, and rows whose nearest keys lie on no page."""
+    c = make([1, 40], [900, 2000], 4, 2, bias=True)
+    pos = pos_of(c)
+    c["visible"] = torch.stack([pos * 0 + 10, pos - 200], 1).int()
+    c["visible"][5::7] = 0
+    c["table"][1, 12] = c["table"][1, 13] = c["table"][0, 4] = -1
+    check(c, *call(c, dev))
+
+
+def test_tokens_before_all_keys(dev):
+    """More new tokens than keys, without a causal mask: positions below 0."""
+    c = make([9, 200], [4, 150], 8, 2, mode=0, bias=True)
+    c["visible"] = torch.tensor([[20, 140]], dtype=torch.int32).expand(209, 2).contiguous()
+    check(c, *call(c, dev))
