@@ -1146,12 +1146,12 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tile_kernel(AttnParams p) {
   // other parts of the rings, and the parameters say so, as in
   // attn_rows_kernel.)
   f32x16 st[2];
-  // A stage that some row of the wave does not see whole, or (with a bias) has
-  // keys behind its nearest one in.
+  // A stage that some row of the wave does not see whole, or (with a bias) has its
+  // nearest key or keys behind that one in.
   auto at_edge = [&](const Entry& cur, int in) __attribute__((always_inline)) -> bool {
     const int j0 = cur.beta * kP + in * kTileKeys;
     if constexpr (F == 0) return !cur.there || j0 + kTileKeys - 1 > lim_lo;
-    const int end = F & kBias ? min(lim, at) : lim;
+    const int end = F & kBias ? min(lim, at - 1) : lim;
     return !cur.there || __ballot(j0 + kTileKeys - 1 > end || j0 < mine.first);
   };
   auto scores = [&](const uint8_t* __restrict kt, [[maybe_unused]] int j0,
@@ -1159,7 +1159,9 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tile_kernel(AttnParams p) {
     // S^T, two tiles of 32 keys: register r of tile t is key
     // j0 + 32 t + 8 (r / 4) + 4 h + r % 4 of row n
     if constexpr ((F & kBias) && !(F & kCap)) {
-      // (the bias costs one instruction a score: the sums begin with it)
+      // (the bias costs one instruction a score: the sums begin with it.  In whole
+      // stages it is off by e times the distance of the stage's first key, up to 64
+      // times that of its last; the nearest key, whose bias is 0, is never in one.)
       const float away = (float)(at - j0 - 4 * h);
       if (edge) {
 #pragma unroll

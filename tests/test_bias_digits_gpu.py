@@ -45,3 +45,16 @@ def test_tokens_before_all_keys(dev):
     c = make([9, 200], [4, 150], 8, 2, mode=0, bias=True)
     c["visible"] = torch.tensor([[20, 140]], dtype=torch.int32).expand(209, 2).contiguous()
     check(c, *call(c, dev))
+
+
+@pytest.mark.parametrize("Hq,Hkv,q_lens,kv_lens", [
+    (32, 1, [8], [320]), (8, 2, [70], [448]), (64, 1, [2, 3], [192, 256])])
+def test_steep_heads(Hq, Hkv, q_lens, kv_lens, dev):
+    """A token's own key is off by none of its neighbours' biases, also where it ends a
+    stage of keys that all rows see whole: the last of 64."""
+    c = make(q_lens, kv_lens, Hq, Hkv, "BNBD", BF, gain=1.0, bias=True)
+    c["slopes"] = torch.linspace(37.7, 30011.3, Hq)
+    assert (pos_of(c) % 64 == 63).any()
+    check(c, *call(c, dev))
+    c["visible"] = torch.stack([pos_of(c) * 0, pos_of(c) - 64], 1).int()
+    check(c, *call(c, dev))
