@@ -280,6 +280,11 @@ __device__ __forceinline__ Span attn_span(const AttnParams& p, const AttnTile& w
 __device__ __forceinline__ int nearest(const Span& s, int pos) {
   return s.last < s.first ? pos : min(max(pos, s.first), s.last);
 }
+// Head h's slope in other units, kept finite: the nearest key's bias is 0 times it.
+__device__ __forceinline__ float slope_of(const AttnParams& p, int h, float unit) {
+  constexpr float kMost = 0x1.fffffep127f;
+  return fminf(fmaxf(p.slopes[h] * unit, -kMost), kMost);
+}
 // That bias, of the i-th new token and query head h.
 template <int F>
 __device__ __forceinline__ float lse_shift(const AttnParams& p, const AttnTile& w, int i, int h) {
@@ -519,7 +524,7 @@ __global__ __launch_bounds__(256, 1) void attn_rows_kernel(AttnParams p) {
   float slope = 0.f;
   int near = 0;
   if constexpr (F & kBias) {
-    if (row_ok) slope = p.slopes[hk * p.g + hg] * kLog2e;
+    if (row_ok) slope = slope_of(p, hk * p.g + hg, kLog2e);
     near = nearest(mine_sees, w.len - w.Lq + w.i0 + ti);
   }
 
@@ -1098,7 +1103,7 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tile_kernel(AttnParams p) {
   [[maybe_unused]] int at = INT32_MAX;
   if constexpr (F & kBias) {
     if (row_ok) {
-      slope = p.slopes[hk * p.g + hg] * (F & kCap ? kLog2e : p.per_scale);
+      slope = slope_of(p, hk * p.g + hg, F & kCap ? kLog2e : p.per_scale);
       at = nearest(mine, w.len - w.Lq + w.i0 + ti);
     }
   }

@@ -58,3 +58,22 @@ def test_steep_heads(Hq, Hkv, q_lens, kv_lens, dev):
     check(c, *call(c, dev))
     c["visible"] = torch.stack([pos_of(c) * 0, pos_of(c) - 64], 1).int()
     check(c, *call(c, dev))
+
+
+@pytest.mark.parametrize("q_lens,kv_lens,cap", [([1], [130], 0.0), ([90], [300], 0.0),
+                                                ([90], [300], 9.0)])
+def test_the_steepest_slopes(q_lens, kv_lens, cap, dev):
+    """Slopes whose product with 1 / softmax_scale has no float32 leave each token its
+    own key alone: its value, and its score as lse."""
+    c = make(q_lens, kv_lens, 4, 2, "TND", BF, cap=cap)
+    c["slopes"] = torch.tensor([3.4e38, 1e38, 2.6e38, 4e37])
+    out, lse = call(c, dev)
+    own = pos_of(c)
+    k, v = (c[n][own].repeat_interleave(2, 1).double() for n in ("k", "v"))
+    assert torch.equal(out.double(), v)
+    s = (c["q"].double() * k).sum(-1) * 128 ** -0.5
+    size = (c["q"].double() * k).abs().sum(-1) * 128 ** -0.5
+    if cap:
+        s = cap * torch.tanh(s / cap)
+    e = 2.0 ** -24
+    assert ((lse.double() - s).abs() <= 130 * e * size + 12 * e * cap + 8 * e * (1 + s.abs())).all()
