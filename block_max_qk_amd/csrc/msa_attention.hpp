@@ -77,8 +77,8 @@ struct AttnParams {
 // the same cards: a near score takes 5 vector instructions more, 160 a stage and
 // wave on top of the plain kernel's 180 and its 32 matrix instructions, and the
 // vector and matrix instructions of the two waves of a SIMD overlap only in part.
-// A bias costs the tile kernels one vector instruction a score, in front of the
-// matrix instructions whose sums begin with it: packed prompts 305 / 268 to 292.  A
+// A bias costs the tile kernels two vector instructions a score, in front of the
+// matrix instructions whose sums begin with it: packed prompts 297 to 317 / 268 to 292.  A
 // range costs two comparisons a score in stages at its ends, and 14068 tokens of
 // documents of 40 to 2000 tokens 210 us, of which 65 are the tiles' beginnings and
 // ends, which nothing overlaps.
@@ -403,7 +403,8 @@ __device__ __forceinline__ void landed(i32x4& x) { asm volatile("" : "+v"(x)); }
 // rescaled, only when a score passes m + kReach, and then to kLift below that
 // score.  Almost every stage after the first skips the rescaling; m cancels in
 // out and is put back in lse.  (A row's own scores alone decide when its m
-// moves, so its bits do not depend on the rows it shares a tile with.)
+// moves, so in a tile that is not split its bits do not depend on the rows it shares
+// the tile with; capped scores, below, do by roundings.)
 //  - bf16 weights have float32's range: no lift, a lag of 2^8.
 //  - f16 weights end at 2^-24, in steps of that below 2^-14.  Against a largest
 //    weight of 1 the keys 17 nats below a row's largest score (a sink's, say)
@@ -1151,37 +1152,26 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tile_kernel(AttnParams p) {
   // other parts of the rings, and the parameters say so, as in
   // attn_rows_kernel.)
   f32x16 st[2];
-  // A stage that some row of the wave does not see whole, or (with a bias) has its
-  // nearest key or keys behind that one in.
+  // A stage that some row of the wave does not see whole.
   auto at_edge = [&](const Entry& cur, int in) __attribute__((always_inline)) -> bool {
     const int j0 = cur.beta * kP + in * kTileKeys;
     if constexpr (F == 0) return !cur.there || j0 + kTileKeys - 1 > lim_lo;
-    const int end = F & kBias ? min(lim, at - 1) : lim;
-    return !cur.there || __ballot(j0 + kTileKeys - 1 > end || j0 < mine.first);
+    return !cur.there || __ballot(j0 + kTileKeys - 1 > lim || j0 < mine.first);
   };
-  auto scores = [&](const uint8_t* __restrict kt, [[maybe_unused]] int j0,
-                    [[maybe_unused]] bool edge) __attribute__((always_inline)) {
+  auto scores = [&](const uint8_t* __restrict kt, [[maybe_unused]] int j0)
+      __attribute__((always_inline)) {
     // S^T, two tiles of 32 keys: register r of tile t is key
     // j0 + 32 t + 8 (r / 4) + 4 h + r % 4 of row n
     if constexpr ((F & kBias) && !(F & kCap)) {
-      // (the bias costs one instruction a score: the sums begin with it.  In whole
-      // stages it is off by e times the distance of the stage's first key, up to 64
-      // times that of its last; the nearest key, whose bias is 0, is never in one.)
+      // (the sums begin with it: two instructions a score, rounded once.  As one
+      // multiply-add behind -slope * away, which whole stages allow, packed prompts take
+      // 315.4 us for 316.9, and a row's bits go by whose stages are whole.)
       const float away = (float)(at - j0 - 4 * h);
-      if (edge) {
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
+      for (int t = 0; t < 2; ++t)
 #pragma unroll
-          for (int r = 0; r < 16; ++r)
-            st[t][r] = -slope * fabsf(away - (32 * t + 8 * (r >> 2) + (r & 3)));
-      } else {
-        const float from = -slope * away;
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-#pragma unroll
-          for (int r = 0; r < 16; ++r)
-            st[t][r] = __builtin_fmaf(slope, 32 * t + 8 * (r >> 2) + (r & 3), from);
-      }
+        for (int r = 0; r < 16; ++r)
+          st[t][r] = -slope * fabsf(away - (32 * t + 8 * (r >> 2) + (r & 3)));
     } else {
       st[0] = st[1] = f32x16{};
     }
@@ -1382,7 +1372,7 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tile_kernel(AttnParams p) {
         copy_plain<NI>(p, kring, vring, wave, rows_of(x, s & 1), kof, vof);
         __syncthreads();
         const bool edge = at_edge(x, s & 1);
-        scores(kring, x.beta * kP + (s & 1) * kTileKeys, edge);
+        scores(kring, x.beta * kP + (s & 1) * kTileKeys);
         absorb(vring, x, s & 1, edge, careful);
       }
       return;
@@ -1397,7 +1387,7 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tile_kernel(AttnParams p) {
       copy_rows<NI>(kd + wave * NI * 1024, r.k, r.kb, kof);
       copy_rows<NI>(vd + wave * NI * 1024, r.v, r.vb, vof);
       const bool edge = at_edge(x, in);
-      scores(kt, x.beta * kP + in * kTileKeys, edge);
+      scores(kt, x.beta * kP + in * kTileKeys);
       absorb(vt, x, in, edge, careful);
     };
     // (A range of keys may leave out the first half of the part's first block and
