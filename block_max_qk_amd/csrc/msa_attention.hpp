@@ -59,16 +59,15 @@ struct AttnParams {
   float per_scale;             // 1 / softmax_scale
   float cap_top;               // softcap * log2(e)
   float cap_unit;              // the products are scaled by this power of two: 1 but for
-                               // very large and small caps
+                               // very large and small caps (with kBias)
   float cap_twice;             // 2 log2(e) softmax_scale / softcap / cap_unit
   float cap_near;              // scaled products up to which the polynomial is the tanh
   float cap_poly[5];           // its coefficients, on a scaled product's square
-  int32_t cap_late;            // capped scores may stay products until their weights
 };
 
 // Forms of the scores that a kernel is compiled for (0: plain ones).
 //  kCap    capped by softcap * tanh(S / softcap)
-//  kBias   less slopes[h] * |pos - j|
+//  kBias   less slopes[h] * |pos - j| (0 without slopes)
 //  kRange  keys narrowed by `visible`, where it is given (set in every form but 0)
 //
 // What they cost, in us, with the plain scores of the same sizes behind the slash:
@@ -325,11 +324,17 @@ __device__ __forceinline__ TileSpan tile_span(const AttnParams& p, const AttnTil
 }
 
 // Capped scores in units of log2: cap_top * tanh(a s) of the products s (scaled by
-// cap_unit), with a = softmax_scale / softcap / cap_unit.  Where all of a wave's |a s| are at most 5/8, an odd
-// polynomial of degree 9, fitted to tanh for the smallest largest error relative to
-// tanh itself, 1.22e-7 or two of float32's half steps (to 3/4 it would be 6.5e-7, or
-// one term more), elsewhere 1 - 2 / (exp(2 a s) + 1), whose error is a few roundings
-// of the cap itself (infinities give the cap).
+// cap_unit), with a = softmax_scale / softcap / cap_unit.  Where all of a wave's |a s|
+// in a stage are at most 5/8, an odd polynomial of degree 9, fitted to tanh for the
+// smallest largest error relative to tanh itself, 1.22e-7 or two of float32's half
+// steps (to 3/4 it would be 6.5e-7, or one term more), elsewhere 1 - 2 / (exp(2 a s) +
+// 1), whose error is a few roundings of the cap itself (infinities give the cap).
+//
+// So a row's last digits go by the largest score beside it, and, as scores that stay
+// products until their weights are rounded once less, by whether its wave sees the
+// stage whole.  Each score by its own size, with the same roundings, needs both
+// formulas where some are far, and a rounding more: the chunk of 2048 tokens over 32768
+// keys 1233 -> 1267 us and 9 requests with images 87 -> 102, in the best of four forms.
 __device__ __forceinline__ float cap_slope(const AttnParams& p, float s) {   // capped / s
   const float u = s * s;
   float r = __builtin_fmaf(u, p.cap_poly[4], p.cap_poly[3]);
@@ -525,7 +530,7 @@ __global__ __launch_bounds__(256, 1) void attn_rows_kernel(AttnParams p) {
   float slope = 0.f;
   int near = 0;
   if constexpr (F & kBias) {
-    if (row_ok) slope = slope_of(p, hk * p.g + hg, kLog2e);
+    if (row_ok && p.slopes) slope = slope_of(p, hk * p.g + hg, kLog2e);
     near = nearest(mine_sees, w.len - w.Lq + w.i0 + ti);
   }
 
@@ -643,7 +648,7 @@ __global__ __launch_bounds__(256, 1) void attn_rows_kernel(AttnParams p) {
   // products of keys j0 + 4 G + r and j0 + 16 + 4 G + r to scores in units of log2
   [[maybe_unused]] auto form = [&](f32x4& sa, f32x4& sb, int j0) __attribute__((always_inline)) {
     if constexpr (F & kCap) {
-      if (p.cap_unit != 1.f) {
+      if ((F & kBias) && p.cap_unit != 1.f) {
         sa *= p.cap_unit;
         sb *= p.cap_unit;
       }
@@ -849,7 +854,7 @@ __global__ __launch_bounds__(256, 1) void attn_rows_kernel(AttnParams p) {
   if (!row_ok) return;
   const int64_t rows = p.T * p.Hq;
   if (wave == 0 && split == 0) mark_parts(p, out_row, parts, G, 4);
-  const bool shifted = (F & kBias) && p.lse && wave == 0 && split == 0 && G == 0;
+  const bool shifted = (F & kBias) && p.slopes && p.lse && wave == 0 && split == 0 && G == 0;
   const float shift = shifted ? lse_shift<F>(p, w, w.i0 + ti, hk * p.g + hg) : 0.f;
   if (parts > 1) {
     if (shifted) p.lse[out_row] = shift;         // (for the join)
@@ -1103,7 +1108,7 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tile_kernel(AttnParams p) {
   [[maybe_unused]] float slope = 0.f;
   [[maybe_unused]] int at = INT32_MAX;
   if constexpr (F & kBias) {
-    if (row_ok) {
+    if (row_ok && p.slopes) {
       slope = slope_of(p, hk * p.g + hg, F & kCap ? kLog2e : p.per_scale);
       at = nearest(mine, w.len - w.Lq + w.i0 + ti);
     }
@@ -1203,7 +1208,7 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tile_kernel(AttnParams p) {
     // are capped here, in units of log2, and a bias is added.
     [[maybe_unused]] bool near = false;
     if constexpr (F & kCap) {
-      if (p.cap_unit != 1.f) {
+      if ((F & kBias) && p.cap_unit != 1.f) {
         st[0] *= p.cap_unit;
         st[1] *= p.cap_unit;
       }
@@ -1213,7 +1218,7 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tile_kernel(AttnParams p) {
 #pragma unroll
         for (int r = 0; r < 16; ++r) far = fmaxf(far, fabsf(st[t][r]));
       const bool poly = !__ballot(far > p.cap_near);
-      near = poly && !edge && !(F & kBias) && p.cap_late;
+      near = poly && !edge && !(F & kBias);
       if (!near) {
         if (poly) {
 #pragma unroll
@@ -1317,10 +1322,13 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tile_kernel(AttnParams p) {
         }
       };
       if constexpr (F & kCap) {
-        if (near)
-          products(std::true_type{});
-        else
-          products(std::false_type{});
+        // (one after the other, the sums pinned between them: with an else the compiler
+        // kept two sets of their registers, 32 copies a stage; the chunk 1293 -> 1279
+        // us, 9 requests with images 92 -> 86.5)
+        if (near) products(std::true_type{});
+        asm volatile("" : "+v"(o[0]), "+v"(o[1]), "+v"(o[2]), "+v"(o[3]));
+        if (!near) products(std::false_type{});
+        asm volatile("" : "+v"(o[0]), "+v"(o[1]), "+v"(o[2]), "+v"(o[3]));
       } else {
         products(std::false_type{});
       }
@@ -1459,7 +1467,7 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tile_kernel(AttnParams p) {
   const int64_t out_row = ((int64_t)(w.t0 + ti) * p.Hq + hk * p.g + hg);
   // register r of o[d] is head element 32 d + 8 (r / 4) + 4 h + r % 4
   if (split == 0) mark_parts(p, out_row, parts, h, 2);
-  const bool shifted = (F & kBias) && p.lse && split == 0 && h == 0;
+  const bool shifted = (F & kBias) && p.slopes && p.lse && split == 0 && h == 0;
   const float shift = shifted ? lse_shift<F>(p, w, w.i0 + ti, hk * p.g + hg) : 0.f;
   if (parts > 1) {
     if (shifted) p.lse[out_row] = shift;         // (for the join)
