@@ -587,7 +587,8 @@ def msa_cache_append(items: Sequence[CacheItem], cos: Optional[torch.Tensor],
 
     With ``axis_positions`` ([axes, T] int32, 1 to 4 axes) pair r of a token is
     rotated by the position of axis ``pair_axes[r]`` (rotary_dim / 2 integers, or
-    the same as bytes) instead of the token's position in its sequence."""
+    the same as bytes) instead of the token's position in its sequence; if no item
+    is rotated, neither is looked at."""
     lib = _lib or load_library()
     if not 1 <= len(items) <= APPEND_MAX_ITEMS:
         raise ValueError(f"1 to {APPEND_MAX_ITEMS} items, got {len(items)}")
@@ -600,6 +601,7 @@ def msa_cache_append(items: Sequence[CacheItem], cos: Optional[torch.Tensor],
     max_blocks = block_table.shape[-1] if paged else 0
     B = _check_lengths(cu_seqlens_q, kv_len, block_table, max_blocks, paged)
     positions = rotary = 0
+    rotated = any(it[4] for it in items)
     if cos is not None and sin is not None:
         if cos.shape != sin.shape or cos.dim() != 2:
             raise ValueError("cos and sin must both be [positions, rotary_dim / 2]")
@@ -607,12 +609,12 @@ def msa_cache_append(items: Sequence[CacheItem], cos: Optional[torch.Tensor],
             if t.dtype != torch.float32 or not t.is_contiguous():
                 raise ValueError(f"{name} must be a contiguous float32 tensor")
         positions, rotary = cos.shape[0], 2 * cos.shape[1]
-    elif cos is not None or sin is not None or any(it[4] for it in items):
+    elif cos is not None or sin is not None or rotated:
         raise ValueError("rotated items need both cos and sin")
     axes = None
-    if axis_positions is not None:
+    if axis_positions is not None and rotated:
         axes = _check_axes(axis_positions, pair_axes, lead, index, rotary)
-    elif pair_axes is not None:
+    elif pair_axes is not None and rotated:
         raise ValueError("pair_axes needs axis_positions")
     packed, code = [], DTYPE_CODE.get
     for i, (src, dst, layout, scale, rotate) in enumerate(items):
