@@ -361,12 +361,17 @@ def attention_forms(query, key, value, block_table, cu_seqlens_q, kv_len, layout
         least = torch.where(inside, away, math.inf).amin(1, keepdim=True).nan_to_num(0, 0, 0)
         g = Hq // keys.shape[1]
         some = seen.any(1)
+        kd, qd = keys[there].double(), query[lo:hi].double()
+        near = bool(softcap) and all(
+            bool((scale * (qd[:, h] @ kd[:, h // g].T).abs() <= 0.62 * softcap).all())
+            for h in range(Hq))
         for h in range(Hq):
             k, v, q = keys[:, h // g].double(), vals[:, h // g].double(), query[lo:hi, h].double()
             s = scale * (q @ k.T)
             d = 130 * e * scale * (q.abs() @ k.abs().T)
             if softcap:
-                s, d = softcap * torch.tanh(s / softcap), d + 12 * e * softcap
+                s = softcap * torch.tanh(s / softcap)
+                d = d + (8 * e * s.abs() if near else 12 * e * softcap)
             base = 0.0
             if slopes is not None:
                 bias, base = float(slopes[h]) * (away - least), float(slopes[h]) * least

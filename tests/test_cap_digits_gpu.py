@@ -14,6 +14,9 @@ import sys
 import pytest
 import torch
 
+from test_attention_forms_gpu import call, make, reference
+from test_attention_forms_gpu import check as check_forms
+
 pytestmark = pytest.mark.gpu
 BF, FP = torch.bfloat16, torch.float16
 E = 2.0 ** -24
@@ -115,3 +118,15 @@ def test_scores_of_any_size(kernel, dev):
     for cap in (1e10, 1e12):
         s = sweep(cap, 1e6, torch.logspace(-4, -0.31, 100, dtype=torch.float64), BF)
         check(capped(s, cap, 1e6, kernel, BF, dev), s, cap, 1e6, kernel, BF)
+
+
+@pytest.mark.parametrize("q_lens,kv_lens", [([1, 2], [200, 130]), ([60], [200]), ([40], [3333])])
+def test_caps_far_above_the_scores(q_lens, kv_lens, dev):
+    """Ordinary scores under a huge cap are the uncapped ones, within their bounds (with
+    cap = 10^6 and scores of 100 a cap takes 10^-8 of a score off it, less than a tenth
+    of what the bounds hold)."""
+    for gain in (0.01, 1.0, 10.0):
+        c = make(q_lens, kv_lens, 8, 2, gain=gain)
+        want = reference(c)
+        for cap in (1e6, 1e7, 1e12, 1e30):
+            check_forms({**c, "cap": cap}, *call({**c, "cap": cap}, dev), want)
