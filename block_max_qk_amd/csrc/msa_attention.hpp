@@ -72,13 +72,14 @@ struct AttnParams {
 //
 // What they cost, in us, with the plain scores of the same sizes behind the slash:
 // 64 decode requests capped 195 / 192 and 24 biased 116 (memory hides both; 98 and
-// 95% of a read); 2048 tokens over 32768 keys capped 1197 to 1252 / 903 to 960 on
-// the same cards: a near score takes 5 vector instructions more, 160 a stage and
-// wave on top of the plain kernel's 180 and its 32 matrix instructions, and the
-// vector and matrix instructions of the two waves of a SIMD overlap only in part.
-// A bias costs the tile kernels two vector instructions a score, in front of the
-// matrix instructions whose sums begin with it: packed prompts 297 to 317 / 268 to 292.  A
-// range costs two comparisons a score in stages at its ends, and 14068 tokens of
+// 95% of a read); 2048 tokens over 32768 keys capped 1200 to 1281 by card / 903 to
+// 960: a near score takes 5 vector instructions more, 160 a stage and wave on top of
+// the plain kernel's 180 and its 32 matrix instructions, and the vector and matrix
+// instructions of the two waves of a SIMD overlap only in part (with caps above 2170,
+// or all scores far, 1300 to 1340).  A bias costs the tile kernels two vector
+// instructions a score, in front of the matrix instructions whose sums begin with it:
+// packed prompts 297 to 317 / 268 to 292; cap and bias 1384 for the chunk.  A range
+// costs two comparisons a score in stages at its ends, and 14068 tokens of
 // documents of 40 to 2000 tokens 210 us, of which 65 are the tiles' beginnings and
 // ends, which nothing overlaps.
 enum ScoreForm : int { kCap = 1, kBias = 2, kRange = 4 };

@@ -452,9 +452,10 @@ msa_status_t msa_attention(const msa_tensor_t* query, const msa_tensor_t* key,
  * of the prefix).  Blocks that no token of a tile sees are not read.
  *
  * softcap      0 (none) or positive, finite; MSA_ERR_ATTR otherwise, and where
- *              softmax_scale / softcap has no float32.  A capped score is off by a
- *              few units in the last place of the cap at most, and by as many of
- *              its own where the scores beside it are below 5/8 softcap too.
+ *              softmax_scale / softcap has no float32.  Beside S's own error a capped
+ *              score is off by 4 units in its last place at most where all scores of
+ *              its tile are below 5/8 softcap, and by 6 units in the last place of the
+ *              cap elsewhere (units of 2^-23).
  * slopes       device float32 [Hq], compact, finite; or NULL.  (Bias and scores are
  *              added in float32, with the biases taken against that of the nearest key
  *              that the token's range and sparse_mode leave: keys far behind that one
@@ -468,7 +469,10 @@ msa_status_t msa_attention(const msa_tensor_t* query, const msa_tensor_t* key,
  *              capped: 44 us without, 30 with it).
  *
  * With none of the three it is msa_attention, bit for bit.  lse is the log of the
- * sum of exp(S2).
+ * sum of exp(S2).  In tiles of the same rows whose keys are not split, a row's bits do
+ * not depend on the rows computed beside it, nor on keys that it does not see, but for
+ * capped scores, by the errors above.  Tiles and splits go by the sizes, the lengths,
+ * the ranges and the workspace.
  */
 msa_status_t msa_attention_ex(const msa_tensor_t* query, const msa_tensor_t* key,
                               const msa_tensor_t* value, const int32_t* block_table,
@@ -548,13 +552,16 @@ int32_t msa_attention_tile_rows(int64_t T, int32_t batch, int32_t Hq, int32_t Hk
  * max_blocks   blocks of a request that exist, 1..min(pool_blocks, 2^24): later ones get no
  *              page, and their tokens no slot.
  * T            rows of positions and slots: at least the sum of new_tokens.  (Where
- *              the sum is larger, nothing is written past T and cu_seqlens_q ends
- *              at T.)
+ *              the sum is larger, nothing is written past T and cu_seqlens_q ends at
+ *              T, but kv_len and the pages count all tokens: such a step's tables are
+ *              not for use.)
  * block_size   128, as for msa_index_score.
  * cu_seqlens_q, cu_pages   device int32 [batch + 1], written in full, as are
  * kv_len, start_loc        device int32 [batch],
  * block_table              device int32 [batch, max_blocks],
- * positions, slots         device int32 and int64 [T].
+ * positions, slots         device int32 and int64 [T].  (They and cu_pages are for the
+ *                          caller's own kernels and books: no entry point here takes
+ *                          them.)
  *
  * All arrays are compact; nothing that is written may overlap anything else
  * (MSA_ERR_STRIDE; but free_out and free_count).  Nothing is allocated or kept; a
