@@ -290,7 +290,8 @@ template <int F>
 __device__ __forceinline__ float lse_shift(const AttnParams& p, const AttnTile& w, int i, int h) {
   if constexpr (F & kBias) {
     const int pos = w.len - w.Lq + i;
-    const float away = (float)pos - (float)nearest(attn_span<F>(p, w, i), pos);
+    // (one rounding, past 2^24 tokens too)
+    const float away = (float)((int64_t)pos - nearest(attn_span<F>(p, w, i), pos));
     return -p.slopes[h] * fabsf(away);
   }
   return 0.f;

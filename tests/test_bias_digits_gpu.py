@@ -77,3 +77,32 @@ def test_the_steepest_slopes(q_lens, kv_lens, cap, dev):
         s = cap * torch.tanh(s / cap)
     e = 2.0 ** -24
     assert ((lse.double() - s).abs() <= 130 * e * size + 12 * e * cap + 8 * e * (1 + s.abs())).all()
+
+
+@pytest.mark.parametrize("n", [1, 40])
+def test_positions_past_2_to_the_24(n, dev):
+    """Only the distances count: keys near the end of a context of 2^25 tokens (a table
+    that names few pages many times) give the bits of a short context's."""
+    import block_max_qk_amd as m
+    gen = torch.Generator().manual_seed(n)
+    k, v = torch.randn(2, 8, 128, 1, 128, generator=gen).to(BF).to(dev)
+    q = torch.randn(n, 4, 128, generator=gen).to(BF).to(dev)
+    slopes = torch.tensor([0.5, 0.01, -0.1, 3.0], device=dev)
+    cu = torch.tensor([0, n], dtype=torch.int32, device=dev)
+    got = []
+    for blocks in (8, (1 << 18) + 8):
+        kv = blocks * 128 - 5
+        table = torch.arange(blocks, dtype=torch.int32, device=dev)[None] % 8
+        first = kv - 700
+        visible = torch.tensor([[first, kv - 60 - n]], dtype=torch.int32, device=dev)
+        got.append(m.attention(q, k, v, table, cu, torch.tensor([kv], dtype=torch.int32,
+                                                                device=dev),
+                               "BBND", return_lse=True, slopes=slopes,
+                               visible=visible.expand(n, 2).contiguous()))
+    torch.cuda.synchronize()
+    (a, al), (b, bl) = got
+    # (the parts may be split elsewhere: sums in another order and weights rounded to 16
+    # bits against another power of two, half a step of each and of the results)
+    tol = 2.0 ** -20 * (1 + al.abs())
+    assert ((al - bl).abs() <= tol).all(), float((al - bl).abs().max())
+    assert ((a.float() - b.float()).abs() <= 2.0 ** -7 * a.float().abs() + 2.0 ** -8).all()
